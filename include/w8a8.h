@@ -73,6 +73,7 @@ typedef void *w8a8_stream_t;  /* a cudaStream_t */
 #define W8A8_ERR_CUDA 4               /* a CUDA runtime call or launch failed */
 #define W8A8_ERR_TIMEOUT 5            /* a bounded device-side wait gave up */
 #define W8A8_ERR_WORKSPACE 6          /* workspace too small */
+#define W8A8_ERR_INDEX 7              /* a cache index on the device was out of range */
 
 /* 1 if the current CUDA device is a compute-capability 10.3 GPU (GB300)
  * that this library's kernels were built for, else 0.  The analogue of the
@@ -85,8 +86,10 @@ const char *w8a8_status_string(int status);
 /* Reads and clears the device-side error word that the kernels set when a
  * bounded wait on the tensor-core pipeline gives up, or when a GEMM kernel
  * finds its shared memory not 1 KB aligned and returns without doing
- * anything (both leave the outputs of that call undefined).  Synchronizes
- * `stream`.  Returns W8A8_OK, W8A8_ERR_TIMEOUT (for either cause) or
+ * anything (both leave the outputs of that call undefined), or when a
+ * key/value cache kernel meets a slot, page, length or query offset outside
+ * its range (which it leaves out).  Synchronizes `stream`.  Returns W8A8_OK,
+ * W8A8_ERR_TIMEOUT (for either of the first two causes), W8A8_ERR_INDEX or
  * W8A8_ERR_CUDA. */
 int w8a8_check_status(w8a8_stream_t stream);
 
@@ -264,6 +267,92 @@ int w8a8_gemm_i32(const int8_t *xq, const void *Wq, int M, int N, int K,
  * operation.  Returns W8A8_ERR_INVALID_ARG for a negative limit or a flag
  * other than 0 / 1. */
 int w8a8_test_set_fault(long long wait_limit_cycles, int skip_first_copy);
+
+/* ---- quantized key/value cache and attention over it -------------------
+ *
+ * What a decoder layer has between two linear() calls: the k and v of the
+ * fused projection go into a paged cache in the library's number format
+ * (symmetric, one fp32 scale per token and kv head: the per-token rule of
+ * quantize_act_per_token over the head_dim elements of a head; INT8, or INT4
+ * packed as pack_weight_int4 packs it), and attention reads it.  No
+ * counterpart on the method's pages, which stop at the linear layer: an
+ * addition of this library.
+ *
+ * The conventions at the top of this file hold, with these additions:
+ *  - head_dim D is 64 or 128; page_size is a power of two from 16 to 1024;
+ *    q_heads is a multiple of kv_heads (query head h reads kv head
+ *    h / (q_heads / kv_heads)).
+ *  - k, v and q are fp16 rows of D contiguous elements addressed by a token
+ *    and a head stride in elements (so slices of a fused projection go in as
+ *    they are): 16-byte aligned, strides non-negative multiples of 8.
+ *  - Values that live on the device (slots, tables, lengths, offsets) cannot
+ *    be checked by the host.  The kernels check them: what lies outside its
+ *    range is left out (no access leaves a buffer), and
+ *    w8a8_check_status() then reports W8A8_ERR_INDEX. */
+
+/* A paged cache of one layer (device pointers, owned by the caller, 16-byte
+ * aligned, contiguous).  Slot s is token s % page_size of page
+ * s / page_size. */
+typedef struct w8a8_kv_cache {
+  void *k_codes;   /* [num_pages, kv_heads, page_size, D] int8 (bits 8) or
+                      [num_pages, kv_heads, page_size, D/2] uint8 (bits 4) */
+  void *v_codes;   /* the same */
+  float *k_scale;  /* [num_pages, kv_heads, page_size] */
+  float *v_scale;
+  long long num_pages;
+  int kv_heads, page_size, head_dim, bits;
+} w8a8_kv_cache;
+
+/* Quantizes T tokens' k and v into their slots.
+ *   k, v   fp16 [T, kv_heads, D] by strides
+ *   slots  int64 [T]; a negative slot is not stored (padding); two tokens
+ *          with one slot race
+ * Non-finite inputs are defined here: NaN is stored as 0, +-Inf as +-65504,
+ * so a written cache holds finite values only. */
+int kv_cache_write(const w8a8_half *k, long long k_token_stride, long long k_head_stride,
+                   const w8a8_half *v, long long v_token_stride, long long v_head_stride,
+                   const int64_t *slots, int T, const w8a8_kv_cache *cache,
+                   w8a8_stream_t stream);
+
+/* Reads T tokens back: k, v fp16 [T, kv_heads, D] contiguous (out),
+ * fp16_rn((float)code * scale); zeros for a negative slot. */
+int kv_cache_read(const int64_t *slots, int T, const w8a8_kv_cache *cache, w8a8_half *k,
+                  w8a8_half *v, w8a8_stream_t stream);
+
+/* Bytes of workspace of kv_cache_attention() for these sizes (0 for invalid
+ * ones); grows with none of the device-side values. */
+size_t kv_cache_attention_workspace_bytes(int T, int q_heads, int B, int max_q, int table_width,
+                                          const w8a8_kv_cache *cache);
+
+/* Attention of T query tokens over the cached tokens of B sequences.
+ *   q           fp16 [T, q_heads, D] by strides
+ *   q_offsets   int32 [B + 1]: sequence b has queries q_offsets[b] ..
+ *               q_offsets[b + 1] - 1; NULL: one query per sequence (T == B)
+ *   max_q       upper bound of the queries of one sequence (T is always
+ *               one; a close bound makes a better launch)
+ *   block_table int32 [B, table_width]: page ids of the sequence's tokens
+ *   seq_lens    int32 [B]: tokens of the sequence in the cache, the queries'
+ *               own included (write them first)
+ *   softmax_scale  of the scores, 1 / sqrt(D) usually
+ *   causal      1: query i of n sits at position seq_len - n + i and sees the
+ *               keys up to its own; 0: every key of the sequence
+ *   window      > 0 (causal only): it sees the last `window` of these
+ *   workspace   at least kv_cache_attention_workspace_bytes(), 256-byte
+ *               aligned, else W8A8_ERR_WORKSPACE; its content does not matter
+ *   out         fp16 [T, q_heads, D] (out)
+ *   lse         fp32 [T, q_heads] (out) natural log of the row's sum of
+ *               exponentials, or NULL
+ * S_j = softmax_scale * k_scale[j] * (q . code_k[j]) with the codes exact and
+ * fp32 sums; out = sum_j softmax(S)_j * v_scale[j] * code_v[j], one fp16
+ * rounding at the end.  A query that sees no key gets out 0 and lse -inf.
+ * Cache rows past seq_len may hold anything.  Results do not depend on the
+ * order in which blocks run. */
+int kv_cache_attention(const w8a8_half *q, long long q_token_stride, long long q_head_stride,
+                       int T, int q_heads, const int32_t *q_offsets, int B, int max_q,
+                       const int32_t *block_table, int table_width, const int32_t *seq_lens,
+                       const w8a8_kv_cache *cache, float softmax_scale, int causal, int window,
+                       void *workspace, size_t ws_bytes, w8a8_half *out, float *lse,
+                       w8a8_stream_t stream);
 
 #ifdef __cplusplus
 }

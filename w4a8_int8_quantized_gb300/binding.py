@@ -23,14 +23,16 @@ _lib = None
 
 STATUS = {0: "ok", 1: "invalid argument", 2: "misaligned pointer or K",
           3: "unsupported device", 4: "CUDA error", 5: "device-side wait timed out",
-          6: "workspace too small or misaligned"}
+          6: "workspace too small or misaligned",
+          7: "slot, page, length or query offset out of range"}
 
 # every symbol that include/w8a8.h declares
 EXPORTS = ("w8a8_is_available", "w8a8_status_string", "w8a8_check_status",
            "quantize_weight_int8", "pack_weight_int4", "quantize_act_per_token",
            "w8a8_gemm", "w8a8_mv", "w4a8_gemm", "quantize_act_per_token_h", "w8a8_gemm_h",
            "w8a8_linear_workspace_bytes", "linear", "linear_noalloc", "w8a8_gemm_i32",
-           "w8a8_test_set_fault", "weight_only_gemm")
+           "w8a8_test_set_fault", "weight_only_gemm", "kv_cache_write", "kv_cache_read",
+           "kv_cache_attention_workspace_bytes", "kv_cache_attention")
 
 
 class W8A8Error(RuntimeError):
@@ -50,7 +52,7 @@ def load(path: str | None = None):
             raise RuntimeError(f"libw8a8 is not built ({p} missing): run "
                                "w4a8_int8_quantized_gb300.build.build() first")
         lib = ctypes.CDLL(p)
-        P, I, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+        P, I, Z, L = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_longlong
         sig = {
             "w8a8_is_available": ([], I),
             "w8a8_status_string": ([I], ctypes.c_char_p),
@@ -69,6 +71,11 @@ def load(path: str | None = None):
             "w8a8_gemm_i32": ([P, P, I, I, I, I, I, P, P], I),
             "w8a8_test_set_fault": ([ctypes.c_longlong, I], I),
             "weight_only_gemm": ([P, P, P, I, I, I, I, I, P, P], I),
+            "kv_cache_write": ([P, L, L, P, L, L, P, I, P, P], I),
+            "kv_cache_read": ([P, I, P, P, P, P], I),
+            "kv_cache_attention_workspace_bytes": ([I, I, I, I, I, P], Z),
+            "kv_cache_attention": ([P, L, L, I, I, P, I, I, P, I, P, P, ctypes.c_float, I, I, P,
+                                    Z, P, P, P], I),
         }
         for name, (args, res) in sig.items():
             f = getattr(lib, name)
@@ -324,3 +331,183 @@ def w8a8_test_set_fault(wait_limit_cycles: int = 0, skip_first_copy: bool = Fals
     launches that follow."""
     _check(load().w8a8_test_set_fault(int(wait_limit_cycles), int(bool(skip_first_copy))),
            "w8a8_test_set_fault")
+
+
+# ---- quantized key/value cache ---------------------------------------------
+
+class _CacheStruct(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("num_pages", ctypes.c_longlong), ("kv_heads", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("head_dim", ctypes.c_int), ("bits", ctypes.c_int)]
+
+
+class KVCache:
+    """Handle of one layer's paged cache (w8a8_kv_cache) over the caller's tensors.
+
+    ``k_codes``, ``v_codes``: int8 [num_pages, kv_heads, page_size, D] (8 bits)
+    or packed uint8 [num_pages, kv_heads, page_size, D / 2] (4 bits);
+    ``k_scale``, ``v_scale``: fp32 [num_pages, kv_heads, page_size].  All
+    contiguous, on one CUDA device.  The checks are made here, once; the calls
+    take the handle."""
+
+    def __init__(self, k_codes, v_codes, k_scale, v_scale):
+        for name, t in (("k_codes", k_codes), ("v_codes", v_codes)):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{name} must be a torch.Tensor")
+            if t.dtype not in (torch.int8, torch.uint8):
+                raise TypeError(f"{name} must be torch.int8 (8 bits) or torch.uint8 (4 bits), "
+                                f"got {t.dtype}")
+            if t.dim() != 4:
+                raise ValueError(f"{name} must have 4 dimensions")
+            _need(t, k_codes.dtype, name, k_codes.shape)
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            _need(t, torch.float32, name, k_codes.shape[:3])
+        if len({t.device for t in (k_codes, v_codes, k_scale, v_scale)}) != 1:
+            raise ValueError("the cache's tensors must be on one device")
+        self.k_codes, self.v_codes, self.k_scale, self.v_scale = k_codes, v_codes, k_scale, v_scale
+        self.bits = 8 if k_codes.dtype == torch.int8 else 4
+        self.num_pages, self.kv_heads, self.page_size, d = k_codes.shape
+        self.head_dim = d * 8 // self.bits
+        if self.head_dim not in (64, 128):
+            raise ValueError(f"head_dim must be 64 or 128, got {self.head_dim}")
+        if not 16 <= self.page_size <= 1024 or self.page_size & (self.page_size - 1):
+            raise ValueError(f"page_size must be a power of two from 16 to 1024, got {self.page_size}")
+        self.device = k_codes.device
+        self._struct = _CacheStruct(k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(),
+                                    v_scale.data_ptr(), self.num_pages, self.kv_heads,
+                                    self.page_size, self.head_dim, self.bits)
+        self._at = ctypes.addressof(self._struct)
+
+    @classmethod
+    def empty(cls, num_pages: int, kv_heads: int, page_size: int, head_dim: int, bits: int = 4,
+              device="cuda"):
+        """A cache over new, uninitialised tensors."""
+        if bits not in (4, 8):
+            raise ValueError(f"bits must be 4 or 8, got {bits}")
+        shape = (num_pages, kv_heads, page_size)
+        codes = [torch.empty((*shape, head_dim * bits // 8), device=device,
+                             dtype=torch.int8 if bits == 8 else torch.uint8) for _ in range(2)]
+        return cls(*codes, *(torch.empty(shape, dtype=torch.float32, device=device)
+                             for _ in range(2)))
+
+
+def _on(cache: KVCache, t: torch.Tensor, dtype, name: str):
+    """t is a tensor of this type on the cache's device."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != cache.device:
+        raise ValueError(f"{name} must be on the cache's device {cache.device}, got {t.device}")
+
+
+def _rows(cache: KVCache, t: torch.Tensor, name: str, shape):
+    """t is an fp16 [tokens, heads, D] of this shape (None: any) with contiguous rows."""
+    _on(cache, t, torch.float16, name)
+    if t.dim() != 3 or any(a is not None and a != b for a, b in zip(shape, t.shape)):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    ts, hs, ds = t.stride()
+    if ds != 1:
+        raise ValueError(f"{name} must be contiguous along the head dimension")
+    # the stride of a dimension of one element says nothing
+    return (ts if t.shape[0] > 1 else 0), (hs if t.shape[1] > 1 else 0)
+
+
+def _vector(cache: KVCache, t: torch.Tensor, dtype, name: str, shape):
+    _on(cache, t, dtype, name)
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _stream_of(cache: KVCache) -> int:
+    """The current stream of the cache's device, which has to be the current device."""
+    index = cache.device.index
+    if torch.cuda.current_device() != index:
+        raise ValueError(f"the cache is on {cache.device}, which is not the current device")
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+def kv_cache_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache: KVCache) -> None:
+    """Quantizes fp16 k, v [T, kv_heads, D] (any token and head strides that are
+    multiples of 8) into the cache's slots, int64 [T] (page * page_size +
+    offset; negative: not stored)."""
+    ks = _rows(cache, k, "k", (None, cache.kv_heads, cache.head_dim))
+    vs = _rows(cache, v, "v", k.shape)
+    T = k.shape[0]
+    _vector(cache, slots, torch.int64, "slots", (T,))
+    _check(load().kv_cache_write(k.data_ptr(), *ks, v.data_ptr(), *vs, slots.data_ptr(), T,
+                                 cache._at, _stream_of(cache)), "kv_cache_write")
+
+
+def kv_cache_read(slots: torch.Tensor, cache: KVCache, k=None, v=None):
+    """The dequantized fp16 (k, v) [T, kv_heads, D] of the slots, int64 [T]
+    (negative: zeros)."""
+    _on(cache, slots, torch.int64, "slots")
+    T = slots.numel()
+    _vector(cache, slots, torch.int64, "slots", (T,))
+    shape = (T, cache.kv_heads, cache.head_dim)
+    k = torch.empty(shape, dtype=torch.float16, device=cache.device) if k is None else k
+    v = torch.empty(shape, dtype=torch.float16, device=cache.device) if v is None else v
+    _vector(cache, k, torch.float16, "k", shape)
+    _vector(cache, v, torch.float16, "v", shape)
+    _check(load().kv_cache_read(slots.data_ptr(), T, cache._at, k.data_ptr(), v.data_ptr(),
+                                _stream_of(cache)), "kv_cache_read")
+    return k, v
+
+
+def kv_cache_attention_workspace_bytes(T: int, q_heads: int, cache: KVCache,
+                                       block_table: torch.Tensor, max_q: int | None = None) -> int:
+    """Workspace of kv_cache_attention() for T queries of q_heads heads."""
+    B, width = block_table.shape
+    return int(load().kv_cache_attention_workspace_bytes(
+        T, q_heads, B, max(T, 1) if max_q is None else max_q, width, cache._at))
+
+
+def kv_cache_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor,
+                       seq_lens: torch.Tensor, q_offsets=None, max_q: int | None = None,
+                       softmax_scale: float | None = None, causal: bool = True, window: int = 0,
+                       return_lse: bool = False, workspace=None, out=None, lse=None):
+    """Attention of fp16 q [T, q_heads, D] over the cached tokens.
+
+    block_table int32 [B, pages], seq_lens int32 [B]; q_offsets int32 [B + 1]
+    (None: one query per sequence); max_q: upper bound of one sequence's
+    queries (default T).  causal, window: which keys a query sees.  Returns out
+    fp16 [T, q_heads, D], or (out, lse fp32 [T, q_heads]) with return_lse."""
+    ts, hs = _rows(cache, q, "q", (None, None, cache.head_dim))
+    T, heads, D = q.shape
+    _on(cache, block_table, torch.int32, "block_table")
+    if block_table.dim() != 2 or not block_table.is_contiguous():
+        raise ValueError("block_table must be a contiguous [sequences, pages]")
+    B, width = block_table.shape
+    _vector(cache, seq_lens, torch.int32, "seq_lens", (B,))
+    offsets_at = 0
+    if q_offsets is not None:
+        _vector(cache, q_offsets, torch.int32, "q_offsets", (B + 1,))
+        offsets_at = q_offsets.data_ptr()
+        max_q = max(T, 1) if max_q is None else max_q
+    else:
+        max_q = 1
+    lib = load()
+    need = lib.kv_cache_attention_workspace_bytes(T, heads, B, max_q, width, cache._at)
+    if workspace is None:
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=cache.device)
+    elif workspace.dtype is not torch.uint8 or not workspace.is_contiguous() or workspace.device != cache.device:
+        raise ValueError("workspace must be a contiguous torch.uint8 tensor on the cache's device")
+    if out is None:
+        out = torch.empty((T, heads, D), dtype=torch.float16, device=cache.device)
+    else:
+        _vector(cache, out, torch.float16, "out", (T, heads, D))
+    if return_lse:
+        if lse is None:
+            lse = torch.empty((T, heads), dtype=torch.float32, device=cache.device)
+        else:
+            _vector(cache, lse, torch.float32, "lse", (T, heads))
+    _check(lib.kv_cache_attention(
+        q.data_ptr(), ts, hs, T, heads, offsets_at, B, max_q, block_table.data_ptr(), width,
+        seq_lens.data_ptr(), cache._at, D ** -0.5 if softmax_scale is None else softmax_scale,
+        int(causal), window, workspace.data_ptr(), workspace.numel(), out.data_ptr(),
+        lse.data_ptr() if return_lse else 0, _stream_of(cache)), "kv_cache_attention")
+    return (out, lse) if return_lse else out

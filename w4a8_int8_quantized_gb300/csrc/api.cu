@@ -120,6 +120,7 @@ const char *w8a8_status_string(int status) {
     case W8A8_ERR_CUDA: return "CUDA error";
     case W8A8_ERR_TIMEOUT: return "device-side wait timed out (or kernel did not run: shared memory misaligned)";
     case W8A8_ERR_WORKSPACE: return "workspace too small or misaligned";
+    case W8A8_ERR_INDEX: return "slot, page, length or query offset out of range";
     default: return "unknown status";
   }
 }
@@ -128,6 +129,7 @@ int w8a8_check_status(w8a8_stream_t stream) {
   if (cudaStreamSynchronize(as_stream(stream)) != cudaSuccess) return W8A8_ERR_CUDA;
   unsigned int code = 0;
   W8A8_TRY(read_and_clear_device_error(&code));
+  if (code == kDevErrIndex) return W8A8_ERR_INDEX;
   return code == 0 ? W8A8_OK : W8A8_ERR_TIMEOUT;
 }
 

@@ -40,6 +40,7 @@ enum DeviceErrorCode : unsigned int {
   kDevErrTmemEmpty = 4,      // MMA wait on a drained accumulator
   kDevErrSmemAlign = 5,      // dynamic shared memory not 1 KB aligned (kernel did nothing)
   kDevErrRowCopy = 6,        // decode kernel: bulk copy of the activation row did not land
+  kDevErrIndex = 7,          // cache kernels: a slot, page, length or offset outside its range
 };
 
 inline bool aligned16(const void *p) {

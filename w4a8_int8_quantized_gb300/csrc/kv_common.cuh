@@ -1,0 +1,83 @@
+// What the key/value cache kernels share: the cache as the kernels see it and
+// the exact conversion of its codes.
+#pragma once
+
+#include "common.cuh"
+
+namespace w8a8 {
+
+// A paged cache.  Token row (page, head, offset) of K and of V is row
+// ((page * heads + head) << page_shift) + offset of codes [rows, D bits / 8]
+// and scales [rows]; every row index is 64-bit (a cache of one layer may pass
+// 4 GB).
+struct KvView {
+  uint8_t *kc, *vc;
+  float *ks, *vs;
+  long long pages;
+  int heads, page_shift;
+  unsigned int *err;
+
+  __device__ __forceinline__ long long row(long long page, int h) const {
+    return (page * heads + h) << page_shift;
+  }
+};
+
+constexpr int kMinPage = 16, kMaxPage = 1024;
+
+struct KvAttnParams {
+  KvView kv;
+  const __half *q;
+  long long q_ts, q_hs;  // strides of q in elements: token, head
+  int T, Hq, group, B, max_q;
+  const int *q_offsets;  // [B + 1], or null: one query per sequence
+  const int *table;      // [B, table_w]
+  int table_w;
+  const int *lens;       // [B]
+  float scale;           // of the scores
+  int causal, window;
+  __half *out;           // [T, Hq, D]
+  float *lse;            // [T, Hq] or null
+  float *ws;
+};
+
+// Queries [q0, q0 + nq) and length of sequence b.  Offsets outside [0, T] or
+// out of order and lengths outside [0, table_w * page] are clamped, so that
+// no index taken from them leaves its buffer, and reported.
+__device__ __forceinline__ void seq_of(const KvAttnParams &p, int b, int &q0, int &nq, int &len) {
+  int bad = 0;
+  if (p.q_offsets != nullptr) {
+    const int a = __ldg(p.q_offsets + b), e = __ldg(p.q_offsets + b + 1);
+    q0 = min(max(a, 0), p.T);
+    const int q1 = min(max(e, q0), p.T);
+    nq = q1 - q0;
+    bad = (q0 != a) | (q1 != e) | (nq > p.max_q);
+    nq = min(nq, p.max_q);
+  } else {
+    q0 = b;
+    nq = 1;
+  }
+  const int n = __ldg(p.lens + b);
+  const long long cap = static_cast<long long>(p.table_w) << p.kv.page_shift;
+  len = static_cast<int>(min(static_cast<long long>(max(n, 0)), cap));
+  bad |= len != n;
+  if (bad && p.kv.err != nullptr)
+    atomicCAS(p.kv.err, 0u, static_cast<unsigned>(kDevErrIndex));
+}
+
+// Keys that the query at position pos of a sequence of len tokens sees:
+// [lo, hi).  pos may be negative (more queries than tokens): nothing.
+__device__ __forceinline__ void visible(const KvAttnParams &p, int pos, int len, int &lo, int &hi) {
+  hi = p.causal ? min(pos + 1, len) : len;
+  lo = p.window > 0 ? max(pos + 1 - p.window, 0) : 0;
+}
+
+// Page of a table entry; an entry outside the cache reads as -1 (its tokens
+// are left out) and is reported.
+__device__ __forceinline__ int page_of(const KvAttnParams &p, int b, int i) {
+  const int e = __ldg(p.table + static_cast<long long>(b) * p.table_w + i);
+  if (static_cast<unsigned>(e) < static_cast<unsigned long long>(p.kv.pages)) return e;
+  if (p.kv.err != nullptr) atomicCAS(p.kv.err, 0u, static_cast<unsigned>(kDevErrIndex));
+  return -1;
+}
+
+}  // namespace w8a8
