@@ -122,7 +122,8 @@ size_t kv_cache_attention_workspace_bytes(int T, int q_heads, int B, int max_q, 
   if (check_cache_shape(cache) != W8A8_OK || T < 0 || q_heads < 1 || B < 0 || max_q < 1 ||
       table_width < 0 || q_heads % cache->kv_heads != 0)
     return 0;
-  return kv_attn_workspace(T, q_heads, max_q, B,
+  if (T == 0 || B == 0) return 0;
+  return kv_attn_workspace(T, q_heads, max_q < T ? max_q : T, B,
                            static_cast<long long>(table_width) * cache->page_size,
                            view_of(cache), cache->head_dim);
 }
@@ -149,6 +150,7 @@ int kv_cache_attention(const w8a8_half *q, long long q_token_stride, long long q
   if (!aligned(out, 16) || !aligned(q_offsets, 4) || !aligned(block_table, 4) ||
       !aligned(seq_lens, 4) || !aligned(lse, 4))
     return W8A8_ERR_MISALIGNED;
+  if (q_offsets == nullptr) max_q = 1;
   if (max_q > T) max_q = T;
   const size_t need = kv_cache_attention_workspace_bytes(T, q_heads, B, max_q, table_width, cache);
   if (need > 0 && (workspace == nullptr || !aligned(workspace, 256) || ws_bytes < need))
@@ -164,7 +166,7 @@ int kv_cache_attention(const w8a8_half *q, long long q_token_stride, long long q
   p.Hq = q_heads;
   p.group = q_heads / cache->kv_heads;
   p.B = B;
-  p.max_q = q_offsets == nullptr ? 1 : max_q;
+  p.max_q = max_q;
   p.q_offsets = q_offsets;
   p.table = block_table;
   p.table_w = table_width;

@@ -8,6 +8,7 @@
 #include <math_constants.h>
 
 #include "common.cuh"
+#include "kv_attn.cuh"
 #include "kv_common.cuh"
 
 namespace w8a8 {
@@ -81,10 +82,12 @@ __global__ void __launch_bounds__(128) kv_attn_row_kernel(const KvAttnParams p) 
 
 size_t kv_attn_workspace(int T, int Hq, int max_q, int B, long long max_len, const KvView &kv,
                          int D) {
-  return 0;
+  const long long rows = static_cast<long long>(max_q) * (Hq / kv.heads);
+  return rows <= kFewRows ? kv_decode_workspace(D, static_cast<int>(rows)) : 0;
 }
 
 int launch_kv_attn(const KvAttnParams &p, int bits, int D, cudaStream_t s) {
+  if (static_cast<long long>(p.max_q) * p.group <= kFewRows) return launch_kv_decode(p, bits, D, s);
   const long long items = static_cast<long long>(p.B) * p.max_q * p.Hq;
   const long long blocks = (items + 3) / 4;
   if (blocks > 0x7fffffffLL) return W8A8_ERR_INVALID_ARG;

@@ -80,4 +80,54 @@ __device__ __forceinline__ int page_of(const KvAttnParams &p, int b, int i) {
   return -1;
 }
 
+// ---- exact conversion of codes to fp16 --------------------------------------
+
+// 0x6400 | u is the fp16 value 1024 + u for u < 1024
+__device__ __forceinline__ uint32_t h2_add(uint32_t a, float c) {
+  const __half2 r = __hadd2(*reinterpret_cast<const __half2 *>(&a), __float2half2_rn(c));
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t h2_fma(uint32_t a, float m, float c) {
+  const __half2 r = __hfma2(*reinterpret_cast<const __half2 *>(&a), __float2half2_rn(m), __float2half2_rn(c));
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// Two's-complement nibbles k and k + 4 of a word, k = 0 .. 3, as the fp16 pairs
+// o[k] = (nibble k, nibble k + 4): the nibble with its sign bit flipped (v + 8)
+// lands in the low bits of 1024 + (v + 8), or of 1024 + 16 (v + 8), which
+// one multiply-add brings back; every step is exact.
+__device__ __forceinline__ void nibbles_to_h(uint32_t w, uint32_t (&o)[4]) {
+  const uint32_t x = w >> 8;
+  o[0] = h2_add((w & 0x000f000fu) ^ 0x64086408u, -1032.f);
+  o[1] = h2_fma((w & 0x00f000f0u) ^ 0x64806480u, 0.0625f, -72.f);
+  o[2] = h2_add((x & 0x000f000fu) ^ 0x64086408u, -1032.f);
+  o[3] = h2_fma((x & 0x00f000f0u) ^ 0x64806480u, 0.0625f, -72.f);
+}
+
+// Bytes 0, 1 and 2, 3 (two's complement) of a word as two fp16 pairs.
+__device__ __forceinline__ void bytes_to_h(uint32_t w, uint32_t &h01, uint32_t &h23) {
+  const uint32_t x = w ^ 0x80808080u;
+  h01 = h2_add(__byte_perm(x, 0x64646464u, 0x5140), -1152.f);
+  h23 = h2_add(__byte_perm(x, 0x64646464u, 0x7362), -1152.f);
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float log2_fast(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// The running reference M of a row's exponents.  Weights are 2^(u - M); M is
+// kHead below the largest u seen when it was set and moves only when some u
+// passes it by kRoom, so a weight is below 2^kRoom (fp16 holds 2^15.99) and
+// the largest one above 2^kHead.  A row starts at kNoRef, under every u.
+constexpr float kHead = 7.f, kRoom = 15.f, kNoRef = -1e30f;
+
 }  // namespace w8a8

@@ -1,0 +1,655 @@
+// Attention of a few query rows per sequence over the quantized cache (one
+// token a step, or a handful for draft verification).
+//
+// Rows of one kv head share its keys, so an item is (sequence, kv head, block
+// of 8 NT rows = queries x heads of the group), and the cache is read once per
+// item.  Bound by that read: at 4 bits, D = 128, 136 bytes a token and kv head
+// against 4 D multiply-adds per row, far too many for scalar arithmetic at
+// the rate the bytes arrive (4 rows: 64 us of fused multiply-adds for 46 us of
+// bytes), so both products run on mma.sync.m16n8k16 with the tokens (then the
+// head dimension) as the 16 rows and the query rows as the 8 columns; with 8
+// columns tcgen05's 64 or 128-row tiles would be nearly empty.
+//
+// The contraction index of either product may be permuted freely as long as
+// both operands agree, which removes every shuffle between memory and the
+// tensor cores:
+//   S^T = K Q^T   lane (g, t) = (lane / 4, lane % 4) loads the same 16 bytes
+//                 (4 bits, D = 128) of the rows of tokens g and g + 8; its
+//                 codes are the operand of D / 16 products once converted, and
+//                 Q is laid out to match once per item;
+//   O^T = V^T P^T the lane loads the bytes of d = D/8 g .. of tokens 2t, 2t+1,
+//                 2t+8, 2t+9; two tokens' words are merged by a byte permute
+//                 so that one conversion gives pairs of tokens;
+//   P^T           the scores' accumulator holds (token g, rows 2t, 2t+1); one
+//                 8x8 transpose (movmatrix) per 8 tokens makes it the operand.
+// Codes go straight from global memory into registers, the next step's loads
+// issued as soon as the current ones are converted.
+//
+// Softmax: u = S * scale * log2e * s_k + log2 s_v, weight p = 2^(u - M), so the
+// weight carries the value's scale: O = sum p code_v with exact codes, and the
+// row's sum is sum p / s_v.  M is the lazy reference of kv_common.cuh: while no
+// weight passes 2^15 (one vote per step) nothing is rescaled or exchanged.
+// s_v = 0 means all codes are 0: any scale will do, 1 is taken.
+//
+// Split: the units (4 warps x one step of tokens) of all items form one line,
+// cut into equal ranges, one per resident block, so ragged lengths balance to
+// one unit.  An item inside one range is finished there; an item cut by
+// ranges leaves one partial (M, sum, O) per block, which a second kernel joins
+// in ascending order (the result does not depend on timing).
+#include <math_constants.h>
+
+#include <mutex>
+
+#include "common.cuh"
+#include "kv_attn.cuh"
+#include "kv_common.cuh"
+
+namespace w8a8 {
+namespace {
+
+constexpr int kWarps = 4, kThreads = kWarps * 32;
+
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+template <int BITS, int D, int NT>
+struct Plan {
+  static constexpr int ROW = D * BITS / 8;           // bytes of a token's codes
+  static constexpr int MT = 16 / BITS * 64 / D;      // 16-token tiles per step: 32 registers of codes
+  static constexpr int STEP = 16 * MT;               // tokens of a warp's step
+  static constexpr int UNIT = kWarps * STEP;         // tokens of a block's step
+  static constexpr int KW = ROW / 16;                // K words per token and lane
+  static constexpr int VW = ROW / 32;                // V words per token and lane
+  static constexpr int MMAS = D / 16;                // products along D
+  static constexpr int COLS = 8 * NT;
+  static constexpr int PAD = D + 4;                  // floats of a staged row
+  static constexpr int BLOCKS = NT == 1 ? 4 : 3;     // resident per SM
+};
+
+// W words from p, as the widest loads
+template <int W>
+__device__ __forceinline__ void load_words(const uint8_t *p, uint32_t *o) {
+  static_assert(W == 1 || W == 2 || W == 4, "");
+  if (W == 1) {
+    o[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
+  } else if (W == 2) {
+    const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p));
+    o[0] = v.x;
+    o[1] = v.y;
+  } else {
+    const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p));
+    o[0] = v.x;
+    o[1] = v.y;
+    o[2] = v.z;
+    o[3] = v.w;
+  }
+}
+
+// Keys that any query of sequence b sees: units of UNIT tokens from `first`
+// (a multiple of 16), at least one unit when there is a query to answer.
+template <int UNIT>
+__device__ __forceinline__ int units_of(const KvAttnParams &p, int nq, int len, int &first) {
+  int lo, hi, lo2, hi2;
+  visible(p, len - nq, len, lo, hi);
+  visible(p, len - 1, len, lo2, hi2);
+  first = min(lo, len) & ~15;
+  return max((hi2 - first + UNIT - 1) / UNIT, 1);
+}
+
+// The joined partials of a row: block c's range ends in an item whose first
+// unit it holds; later blocks hold the rest, up to `last`.
+struct Desc {
+  int b, h, rb, last;
+};
+
+template <int BITS, int D, int NT>
+__global__ void __launch_bounds__(kThreads, Plan<BITS, D, NT>::BLOCKS)
+    kv_decode_kernel(const KvAttnParams p) {
+  using PL = Plan<BITS, D, NT>;
+  constexpr int MT = PL::MT, COLS = PL::COLS, MMAS = PL::MMAS, ROW = PL::ROW;
+  __shared__ __align__(16) float o_sm[kWarps][COLS][PL::PAD];
+  __shared__ float m_sm[kWarps][COLS], l_sm[kWarps][COLS];
+  __shared__ long long sums[kThreads];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  // -- this block's range of units -------------------------------------------
+  // prefix sums over the sequences, `chunk` of them per thread
+  const int chunk = (p.B + kThreads - 1) / kThreads;
+  auto work_of = [&](int b, int &q0, int &nq, int &len, int &first, int &nu, int &nrb) {
+    seq_of(p, b, q0, nq, len);
+    nu = units_of<PL::UNIT>(p, nq, len, first);
+    nrb = (nq * p.group + COLS - 1) / COLS;
+    return static_cast<long long>(nu) * nrb * p.kv.heads;
+  };
+  {
+    long long mine = 0;
+    for (int i = 0; i < chunk; ++i) {
+      const int b = threadIdx.x * chunk + i;
+      int q0, nq, len, first, nu, nrb;
+      if (b < p.B) mine += work_of(b, q0, nq, len, first, nu, nrb);
+    }
+    long long x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    sums[threadIdx.x] = x;  // inclusive within the warp
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) x += sums[w * 32 + 31];
+    __syncthreads();
+    sums[threadIdx.x] = x;
+    __syncthreads();
+  }
+  const long long total = sums[kThreads - 1];
+  const long long per = (total + gridDim.x - 1) / gridDim.x;
+  const long long c0 = blockIdx.x * per, c1 = min(c0 + per, total);
+  Desc *descs = reinterpret_cast<Desc *>(p.ws);
+  float *parts = reinterpret_cast<float *>(descs + gridDim.x);
+  if (threadIdx.x == 0) descs[blockIdx.x].last = -1;
+  if (c0 >= c1) return;
+
+  // first sequence: binary search over the threads' sums, then along the chunk
+  int b;
+  long long start;  // first unit of sequence b
+  {
+    int lo = 0, hi = kThreads - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (sums[mid] > c0) hi = mid; else lo = mid + 1;
+    }
+    b = lo * chunk;
+    start = lo > 0 ? sums[lo - 1] : 0;
+  }
+  int q0, nq, len, first, nu, nrb;
+  long long work = work_of(b, q0, nq, len, first, nu, nrb);
+  while (start + work <= c0) {
+    start += work;
+    work = work_of(++b, q0, nq, len, first, nu, nrb);
+  }
+
+  const uint8_t *kc = p.kv.kc + g * ROW + t * (PL::KW >= 4 ? 16 : PL::KW * 4);
+  const uint8_t *vc = p.kv.vc + 2 * t * ROW + g * (PL::VW * 4);
+  const int pmask = (1 << p.kv.page_shift) - 1;
+
+  for (long long at = c0; at < c1;) {
+    while (at >= start + work) {
+      start += work;
+      work = work_of(++b, q0, nq, len, first, nu, nrb);
+    }
+    // item: units [istart, istart + nu) of the line
+    const int item = static_cast<int>((at - start) / nu);
+    const long long istart = start + static_cast<long long>(item) * nu;
+    const int h = item / nrb, rb = item % nrb;
+    const int u0 = static_cast<int>(at - istart);
+    const int u1 = static_cast<int>(min(static_cast<long long>(nu), c1 - istart));
+    at = istart + u1;
+    const int R = min(nq * p.group - rb * COLS, COLS);  // rows of this block
+
+    // limits of the rows
+    int lo[NT][2], hi[NT][2], lo_max, hi_min, hi_max;
+    {
+      int x;
+      visible(p, len - nq + rb * COLS / p.group, len, x, hi_min);
+      visible(p, len - nq + (rb * COLS + R - 1) / p.group, len, lo_max, hi_max);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int c = n * 8 + 2 * t + e;
+          lo[n][e] = hi[n][e] = 0;
+          if (c < R) visible(p, len - nq + (rb * COLS + c) / p.group, len, lo[n][e], hi[n][e]);
+        }
+    }
+
+    // Q, as the second operand of the products over D: column g of each n
+    uint32_t qf[NT][MMAS][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int c = n * 8 + g;
+      const bool on = c < R;
+      const int ri = rb * COLS + (on ? c : 0);
+      const __half *qp = p.q + (q0 + ri / p.group) * p.q_ts +
+                         static_cast<long long>(h * p.group + ri % p.group) * p.q_hs;
+#pragma unroll
+      for (int w = 0; w < PL::KW; ++w) {
+        uint32_t x[4] = {0, 0, 0, 0};
+        if (BITS == 4) {
+          // word w holds d = 8 (t KW + w) .. + 7
+          if (on) load_words<4>(reinterpret_cast<const uint8_t *>(qp + 8 * (t * PL::KW + w)), x);
+          qf[n][2 * w][0] = __byte_perm(x[0], x[2], 0x5410);
+          qf[n][2 * w][1] = __byte_perm(x[0], x[2], 0x7632);
+          qf[n][2 * w + 1][0] = __byte_perm(x[1], x[3], 0x5410);
+          qf[n][2 * w + 1][1] = __byte_perm(x[1], x[3], 0x7632);
+        } else {
+          // words 0-3: d = 16 t + 4 w .. + 3, words 4-7: 64 further on
+          const int d = (w & 4) * 16 + 16 * t + 4 * (w & 3);
+          if (on) load_words<2>(reinterpret_cast<const uint8_t *>(qp + d), x);
+          qf[n][w][0] = x[0];
+          qf[n][w][1] = x[1];
+        }
+      }
+    }
+
+    float o[NT][MMAS][4];
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int i = 0; i < MMAS; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[n][i][e] = 0.f;
+      m[n][0] = m[n][1] = kNoRef;
+      l[n][0] = l[n][1] = 0.f;
+    }
+
+    // -- steps: this warp's tokens are j .. j + STEP - 1 of each unit ----------
+    uint32_t kraw[MT][2][PL::KW], vraw[MT][4][PL::VW];
+    float ks[MT][2], vs[MT][2];
+    int pages[MT];
+    long long rows[MT];  // row of the tile's first token, or -1: left out
+    // pages of the tiles of the step at token j
+    auto load_pages = [&](int j) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const int a = j + 16 * i;
+        pages[i] = a < hi_max ? page_of(p, b, a >> p.kv.page_shift) : -1;
+      }
+    };
+    auto load_k = [&](int j) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        rows[i] = pages[i] < 0 ? -1 : p.kv.row(pages[i], h) + ((j + 16 * i) & pmask);
+        if (rows[i] >= 0) {
+          const uint8_t *a = kc + rows[i] * ROW;
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            load_words<(PL::KW < 4 ? PL::KW : 4)>(a + r * 8 * ROW, kraw[i][r]);
+            if (PL::KW == 8) load_words<4>(a + r * 8 * ROW + 64, &kraw[i][r][PL::KW - 4]);
+            ks[i][r] = __ldg(p.kv.ks + rows[i] + g + 8 * r);
+          }
+        }
+      }
+    };
+    auto load_v = [&]() {
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        if (rows[i] >= 0) {
+          const uint8_t *a = vc + rows[i] * ROW;
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            load_words<PL::VW>(a + ((r & 1) + (r & 2) * 4) * ROW, vraw[i][r]);
+#pragma unroll
+          for (int r = 0; r < 2; ++r) vs[i][r] = __ldg(p.kv.vs + rows[i] + g + 8 * r);
+        }
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+#pragma unroll
+      for (int w = 0; w < PL::KW; ++w) kraw[i][0][w] = kraw[i][1][w] = 0;
+#pragma unroll
+      for (int w = 0; w < PL::VW; ++w) vraw[i][0][w] = vraw[i][1][w] = vraw[i][2][w] = vraw[i][3][w] = 0;
+      ks[i][0] = ks[i][1] = vs[i][0] = vs[i][1] = 0.f;
+    }
+    int j = first + u0 * PL::UNIT + warp * PL::STEP;
+    load_pages(j);
+    load_k(j);
+    load_v();
+    load_pages(u0 + 1 < u1 ? j + PL::UNIT : hi_max);
+
+    for (int u = u0; u < u1; ++u, j += PL::UNIT) {
+      // scores
+      float s[NT][MT][4];
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) s[n][i][0] = s[n][i][1] = s[n][i][2] = s[n][i][3] = 0.f;
+#pragma unroll
+        for (int w = 0; w < PL::KW; ++w) {
+          if (BITS == 4) {
+            uint32_t a[4], c[4];
+            nibbles_to_h(kraw[i][0][w], a);
+            nibbles_to_h(kraw[i][1][w], c);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              mma16816(s[n][i], a[0], c[0], a[1], c[1], qf[n][2 * w][0], qf[n][2 * w][1]);
+              mma16816(s[n][i], a[2], c[2], a[3], c[3], qf[n][2 * w + 1][0], qf[n][2 * w + 1][1]);
+            }
+          } else {
+            uint32_t a0, a1, a2, a3;
+            bytes_to_h(kraw[i][0][w], a0, a2);
+            bytes_to_h(kraw[i][1][w], a1, a3);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma16816(s[n][i], a0, a1, a2, a3, qf[n][w][0], qf[n][w][1]);
+          }
+        }
+      }
+      // exponents, and per token 1 / s_v
+      float rv[MT][2];
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float sk = ks[i][r] * (p.scale * kLog2e);
+          const bool zero = vs[i][r] == 0.f;
+          const float lv = zero ? 0.f : log2_fast(vs[i][r]);
+          rv[i][r] = zero ? 1.f : __frcp_rn(vs[i][r]);
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) s[n][i][2 * r + e] = fmaf(s[n][i][2 * r + e], sk, lv);
+        }
+      bool left_out = false;
+#pragma unroll
+      for (int i = 0; i < MT; ++i) left_out |= rows[i] < 0;
+      if (j < lo_max || j + PL::STEP > hi_min || left_out) {
+        // a tile at an end of some row's keys (or with a page outside the cache)
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const int a = j + 16 * i + g + 8 * r;
+            if (a >= len || rows[i] < 0) rv[i][r] = 0.f;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (a < lo[n][e] || a >= hi[n][e] || rows[i] < 0) s[n][i][2 * r + e] = -CUDART_INF_F;
+          }
+      }
+      // the next step's keys come in while this one is worked off
+      const bool more = u + 1 < u1;
+      if (more) load_k(j + PL::UNIT);
+
+      // reference
+      bool over = false;
+      float top[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          top[n][e] = -CUDART_INF_F;
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+            top[n][e] = fmaxf(top[n][e], fmaxf(s[n][i][e], s[n][i][2 + e]));
+          over |= top[n][e] > m[n][e] + kRoom;
+        }
+      if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float x = top[n][e];
+#pragma unroll
+            for (int q = 4; q < 32; q <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, q));
+            const float nm = x > m[n][e] + kRoom ? x - kHead : m[n][e];
+            const float a = exp2_fast(m[n][e] - nm);
+            m[n][e] = nm;
+            l[n][e] *= a;
+#pragma unroll
+            for (int i = 0; i < MMAS; ++i) {
+              o[n][i][e] *= a;
+              o[n][i][2 + e] *= a;
+            }
+          }
+      }
+      // weights
+      uint32_t pf[NT][MT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float w0 = exp2_fast(s[n][i][2 * r] - m[n][0]);
+            const float w1 = exp2_fast(s[n][i][2 * r + 1] - m[n][1]);
+            l[n][0] = fmaf(w0, rv[i][r], l[n][0]);
+            l[n][1] = fmaf(w1, rv[i][r], l[n][1]);
+            pf[n][i][r] = transpose8x8(pack_h2(w0, w1));
+          }
+      // values
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int w = 0; w < PL::VW; ++w) {
+          const uint32_t x0 = vraw[i][0][w], x1 = vraw[i][1][w];
+          const uint32_t x2 = vraw[i][2][w], x3 = vraw[i][3][w];
+          if (BITS == 4) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const int sel = half ? 0x7632 : 0x5410;
+              uint32_t a[4], c[4];
+              nibbles_to_h(__byte_perm(x0, x1, sel), a);
+              nibbles_to_h(__byte_perm(x2, x3, sel), c);
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                mma16816(o[n][4 * w + 2 * half], a[0], a[1], c[0], c[1], pf[n][i][0], pf[n][i][1]);
+                mma16816(o[n][4 * w + 2 * half + 1], a[2], a[3], c[2], c[3], pf[n][i][0], pf[n][i][1]);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const int sel = half ? 0x7362 : 0x5140;
+              uint32_t a0, a1, a2, a3;
+              bytes_to_h(__byte_perm(x0, x1, sel), a0, a1);
+              bytes_to_h(__byte_perm(x2, x3, sel), a2, a3);
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+                mma16816(o[n][2 * w + half], a0, a1, a2, a3, pf[n][i][0], pf[n][i][1]);
+            }
+          }
+        }
+      if (more) {
+        load_v();
+        load_pages(u + 2 < u1 ? j + 2 * PL::UNIT : hi_max);
+      }
+    }
+
+    // -- join the warps -----------------------------------------------------------
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int c = n * 8 + 2 * t + e;
+        float x = l[n][e];
+#pragma unroll
+        for (int q = 4; q < 32; q <<= 1) x += __shfl_xor_sync(0xffffffffu, x, q);
+        if (g == 0) {
+          m_sm[warp][c] = m[n][e];
+          l_sm[warp][c] = x;
+        }
+        // this lane's d: MMAS pairs (2 i, 2 i + 1) from 2 MMAS g on
+        float *dst = &o_sm[warp][c][2 * MMAS * g];
+#pragma unroll
+        for (int i = 0; i < MMAS; i += 2)
+          *reinterpret_cast<float4 *>(dst + 2 * i) =
+              make_float4(o[n][i][e], o[n][i][2 + e], o[n][i + 1][e], o[n][i + 1][2 + e]);
+      }
+    __syncthreads();
+    const bool whole = u0 == 0 && u1 == nu;
+    // a block's first piece may go on from the block before: slot 0, else 1
+    const int slot = u0 == 0 ? 1 : 0;
+    float *part = parts + (static_cast<long long>(blockIdx.x) * 2 + slot) * COLS * (D + 2);
+    for (int i = threadIdx.x; i < R * (D / 4); i += kThreads) {
+      const int c = i / (D / 4), d = i % (D / 4) * 4;
+      float mm = m_sm[0][c];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) mm = fmaxf(mm, m_sm[w][c]);
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      float sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float a = exp2_fast(m_sm[w][c] - mm);
+        const float4 y = *reinterpret_cast<const float4 *>(&o_sm[w][c][d]);
+        x.x = fmaf(a, y.x, x.x);
+        x.y = fmaf(a, y.y, x.y);
+        x.z = fmaf(a, y.z, x.z);
+        x.w = fmaf(a, y.w, x.w);
+        sum = fmaf(a, l_sm[w][c], sum);
+      }
+      if (whole) {
+        const int ri = rb * COLS + c;
+        const long long row = (static_cast<long long>(q0) + ri / p.group) * p.Hq +
+                              h * p.group + ri % p.group;
+        store_row4<D>(p, row, d, x, mm, sum);
+      } else {
+        *reinterpret_cast<float4 *>(part + c * D + d) = x;
+        if (d == 0) {
+          part[COLS * D + 2 * c] = mm;
+          part[COLS * D + 2 * c + 1] = sum;
+        }
+      }
+    }
+    if (!whole && u0 == 0 && threadIdx.x == 0)
+      descs[blockIdx.x] = Desc{b, h, rb, static_cast<int>((istart + nu - 1) / per)};
+    __syncthreads();
+  }
+}
+
+// Joins the partials of the items cut by the ranges: block c takes the item
+// that starts in range c and ends in a later one.  A warp takes every 4th
+// piece of a row (16 warps: 4 rows at once), and the sums of the 4 are added
+// in order.
+template <int D, int NT>
+__global__ void __launch_bounds__(512) kv_decode_join_kernel(const KvAttnParams p, int ranges) {
+  constexpr int COLS = 8 * NT, WPR = 4, V = D / 32;
+  __shared__ float sh[16][D + 2];
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Desc *descs = reinterpret_cast<const Desc *>(p.ws);
+  const float *parts = reinterpret_cast<const float *>(descs + ranges);
+  const int c0 = blockIdx.x;
+  const Desc de = descs[c0];
+  if (de.last < 0) return;
+  int q0, nq, len;
+  seq_of(p, de.b, q0, nq, len);
+  const int R = min(nq * p.group - de.rb * COLS, COLS);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wp = warp % WPR;
+  for (int base = 0; base < R; base += 16 / WPR) {
+    const int c = base + warp / WPR;
+    float m = kNoRef, l = 0.f, o[V] = {};
+    if (c < R) {
+      // the largest reference first, then the sums against it
+      for (int i = c0 + lane; i <= de.last; i += 32) {
+        const float *part = parts + (static_cast<long long>(i) * 2 + (i == c0 ? 1 : 0)) * COLS * (D + 2);
+        m = fmaxf(m, part[COLS * D + 2 * c]);
+      }
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+#pragma unroll 4
+      for (int i = c0 + wp; i <= de.last; i += WPR) {
+        const float *part = parts + (static_cast<long long>(i) * 2 + (i == c0 ? 1 : 0)) * COLS * (D + 2);
+        const float a = exp2_fast(part[COLS * D + 2 * c] - m);
+        l = fmaf(a, part[COLS * D + 2 * c + 1], l);
+        const float *x = part + c * D + lane * V;
+#pragma unroll
+        for (int v = 0; v < V; ++v) o[v] = fmaf(a, x[v], o[v]);
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) sh[warp][lane * V + v] = o[v];
+    if (lane == 0) sh[warp][D] = l;
+    __syncthreads();
+    if (c < R && wp == 0) {
+      float sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < WPR; ++w) sum += sh[warp + w][D];
+      const int ri = de.rb * COLS + c;
+      const long long row = (static_cast<long long>(q0) + ri / p.group) * p.Hq +
+                            de.h * p.group + ri % p.group;
+      for (int d = lane * 4; d < D; d += 128) {
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < WPR; ++w) {
+          x.x += sh[warp + w][d];
+          x.y += sh[warp + w][d + 1];
+          x.z += sh[warp + w][d + 2];
+          x.w += sh[warp + w][d + 3];
+        }
+        store_row4<D>(p, row, d, x, m, sum);
+      }
+    }
+    __syncthreads();
+  }
+}
+
+template <int BITS, int D, int NT>
+long long most_units(const KvAttnParams &p) {
+  using PL = Plan<BITS, D, NT>;
+  const long long tokens = static_cast<long long>(p.table_w) << p.kv.page_shift;
+  const long long rb = (static_cast<long long>(p.max_q) * p.group + PL::COLS - 1) / PL::COLS;
+  // + 15: the first unit starts on a multiple of 16 before the first key
+  const long long units = tokens > 0 ? (tokens + 15 + PL::UNIT - 1) / PL::UNIT : 1;
+  return p.B * p.kv.heads * rb * units;
+}
+
+template <int BITS, int D, int NT>
+int launch_t(const KvAttnParams &p, cudaStream_t s) {
+  using PL = Plan<BITS, D, NT>;
+  const long long units = most_units<BITS, D, NT>(p);
+  const long long room = kNumSMsGB300 * PL::BLOCKS;
+  const int grid = static_cast<int>(units < room ? units : room);
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kv_decode_kernel<BITS, D, NT>, p) != cudaSuccess) {
+    cudaGetLastError();
+    return W8A8_ERR_CUDA;
+  }
+  // no item can be cut when none has more than one unit
+  if ((static_cast<long long>(p.table_w) << p.kv.page_shift) + 15 > PL::UNIT) {
+    cfg.blockDim = dim3(512);
+    if (cudaLaunchKernelEx(&cfg, kv_decode_join_kernel<D, NT>, p, grid) != cudaSuccess) {
+      cudaGetLastError();
+      return W8A8_ERR_CUDA;
+    }
+  }
+  return launch_status();
+}
+
+}  // namespace
+
+size_t kv_decode_workspace(int D, int rows) {
+  const int cols = rows <= 8 ? 8 : 16;
+  const size_t grid = kNumSMsGB300 * (rows <= 8 ? 4 : 3);
+  return grid * (sizeof(Desc) + 2 * sizeof(float) * cols * (D + 2));
+}
+
+int launch_kv_decode(const KvAttnParams &p, int bits, int D, cudaStream_t s) {
+  const bool one = p.max_q * p.group <= 8;
+  if (bits == 4) {
+    if (D == 64) return one ? launch_t<4, 64, 1>(p, s) : launch_t<4, 64, 2>(p, s);
+    return one ? launch_t<4, 128, 1>(p, s) : launch_t<4, 128, 2>(p, s);
+  }
+  if (D == 64) return one ? launch_t<8, 64, 1>(p, s) : launch_t<8, 64, 2>(p, s);
+  return one ? launch_t<8, 128, 1>(p, s) : launch_t<8, 128, 2>(p, s);
+}
+
+}  // namespace w8a8
