@@ -41,6 +41,7 @@ enum DeviceErrorCode : unsigned int {
   kDevErrSmemAlign = 5,      // dynamic shared memory not 1 KB aligned (kernel did nothing)
   kDevErrRowCopy = 6,        // decode kernel: bulk copy of the activation row did not land
   kDevErrIndex = 7,          // cache kernels: a slot, page, length or offset outside its range
+  kDevErrCacheCopy = 8,      // cache attention: a copy or a hand-over did not arrive
 };
 
 inline bool aligned16(const void *p) {

@@ -81,7 +81,65 @@ struct Plan {
   static constexpr int COLS = 8 * NT;
   static constexpr int PAD = D + 4;                  // floats of a staged row
   static constexpr int BLOCKS = NT == 1 ? 4 : 3;     // resident per SM
+  // a stage of a warp's ring: one step's K codes, V codes, K scales, V scales
+  static constexpr int OFF_V = STEP * ROW, OFF_KS = 2 * STEP * ROW, OFF_VS = OFF_KS + STEP * 4;
+  static constexpr int STAGE = OFF_VS + STEP * 4;
+  static constexpr int TILE_BYTES = 2 * 16 * ROW + 2 * 16 * 4;  // of one 16-token tile
+  static constexpr int STAGES = 3;
+  static constexpr int RING = kWarps * STAGES * STAGE;
+  static constexpr int JOIN = kWarps * COLS * PAD * 4;  // the warps' results, over the drained ring
+  static constexpr int SMEM = (RING > JOIN ? RING : JOIN) + kWarps * STAGES * 8;
 };
+
+__device__ __forceinline__ uint32_t smem_u32(const void *p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+
+// Waits for a phase of an mbarrier; false if it gave up after about 2 s.
+__device__ __forceinline__ bool wait_stage(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  long long t0 = 0;
+  for (int i = 0;; ++i) {
+    asm volatile(
+        "{\n.reg .pred p;\n"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        "selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if (i == 64) t0 = clock64();
+    if (i > 64 && clock64() - t0 > 4000000000LL) return false;
+  }
+}
+
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, int bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ float rcp_fast(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// W words from shared memory
+template <int W>
+__device__ __forceinline__ void lds_words(uint32_t a, uint32_t *o) {
+  static_assert(W == 1 || W == 2 || W == 4, "");
+  if (W == 1)
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(o[0]) : "r"(a));
+  else if (W == 2)
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(o[0]), "=r"(o[1]) : "r"(a));
+  else
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
+                 : "r"(a));
+}
 
 // W words from p, as the widest loads
 template <int W>
@@ -124,7 +182,8 @@ __global__ void __launch_bounds__(kThreads, Plan<BITS, D, NT>::BLOCKS)
     kv_decode_kernel(const KvAttnParams p) {
   using PL = Plan<BITS, D, NT>;
   constexpr int MT = PL::MT, COLS = PL::COLS, MMAS = PL::MMAS, ROW = PL::ROW;
-  __shared__ __align__(16) float o_sm[kWarps][COLS][PL::PAD];
+  extern __shared__ __align__(128) uint8_t dyn[];
+  float(*o_sm)[COLS][PL::PAD] = reinterpret_cast<float(*)[COLS][PL::PAD]>(dyn);
   __shared__ float m_sm[kWarps][COLS], l_sm[kWarps][COLS];
   __shared__ long long sums[kThreads];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
@@ -187,8 +246,33 @@ __global__ void __launch_bounds__(kThreads, Plan<BITS, D, NT>::BLOCKS)
     work = work_of(++b, q0, nq, len, first, nu, nrb);
   }
 
-  const uint8_t *kc = p.kv.kc + g * ROW + t * (PL::KW >= 4 ? 16 : PL::KW * 4);
-  const uint8_t *vc = p.kv.vc + 2 * t * ROW + g * (PL::VW * 4);
+  // the warp's ring, and its barriers (one arrival a phase: lane 0)
+  constexpr int S = PL::STAGES;
+  const uint32_t ring = smem_u32(dyn) + warp * (S * PL::STAGE);
+  const uint32_t bars = smem_u32(dyn) + PL::SMEM - kWarps * S * 8 + warp * (S * 8);
+  if (lane < S) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bars + 8 * lane));
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  __syncwarp();
+  uint32_t phases = 0;  // bit s: parity of the next wait on stage s
+  bool ok = true;
+
+  // Row r of a 16-token product stands for token tok(r) (+ 8 for the second
+  // half): rows 2t and 2t + 1 are tokens t and 4 + (t ^ 1), so that the lanes
+  // of a value load (rows 2t of four t) and of a key load (rows g, g + 1) read
+  // rows of both parities of 64 bytes, half of the bank conflicts of tokens
+  // in their own order.
+  const int tokg = (g & 1) ? 4 + ((g >> 1) ^ 1) : g >> 1;
+  const uint32_t k_at = ring + tokg * ROW + t * (PL::KW >= 4 ? 16 : PL::KW * 4);
+  const uint32_t v_at = ring + PL::OFF_V + g * (PL::VW * 4);
+  const uint32_t v_row[2] = {static_cast<uint32_t>(t) * ROW, static_cast<uint32_t>(4 + (t ^ 1)) * ROW};
+  // copies: lane i < 4 MT brings array i % 4 (K, V, K scales, V scales) of tile i / 4
+  const int ctile = lane >> 2, carr = lane & 3;
+  const bool copier = lane < 4 * MT;
+  const uint8_t *csrc = carr == 0 ? p.kv.kc : carr == 1 ? p.kv.vc
+                        : reinterpret_cast<const uint8_t *>(carr == 2 ? p.kv.ks : p.kv.vs);
+  const int cbytes = carr < 2 ? ROW : 4;  // per token
+  const uint32_t cdst = (carr == 0 ? 0 : carr == 1 ? PL::OFF_V : carr == 2 ? PL::OFF_KS : PL::OFF_VS) +
+                        ctile * 16 * cbytes;
   const int pmask = (1 << p.kv.page_shift) - 1;
 
   for (long long at = c0; at < c1;) {
@@ -263,73 +347,63 @@ __global__ void __launch_bounds__(kThreads, Plan<BITS, D, NT>::BLOCKS)
     }
 
     // -- steps: this warp's tokens are j .. j + STEP - 1 of each unit ----------
-    uint32_t kraw[MT][2][PL::KW], vraw[MT][4][PL::VW];
-    float ks[MT][2], vs[MT][2];
-    int pages[MT];
-    long long rows[MT];  // row of the tile's first token, or -1: left out
-    // pages of the tiles of the step at token j
-    auto load_pages = [&](int j) {
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        const int a = j + 16 * i;
-        pages[i] = a < hi_max ? page_of(p, b, a >> p.kv.page_shift) : -1;
-      }
+    // Page of the copier's tile of the step at token j (-1: left out, also
+    // past the last key); fetched a step before the copies that use it.
+    auto page_at = [&](int j) {
+      const int a = j + 16 * ctile;
+      return copier && a < hi_max ? page_of(p, b, a >> p.kv.page_shift) : -1;
     };
-    auto load_k = [&](int j) {
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        rows[i] = pages[i] < 0 ? -1 : p.kv.row(pages[i], h) + ((j + 16 * i) & pmask);
-        if (rows[i] >= 0) {
-          const uint8_t *a = kc + rows[i] * ROW;
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            load_words<(PL::KW < 4 ? PL::KW : 4)>(a + r * 8 * ROW, kraw[i][r]);
-            if (PL::KW == 8) load_words<4>(a + r * 8 * ROW + 64, &kraw[i][r][PL::KW - 4]);
-            ks[i][r] = __ldg(p.kv.ks + rows[i] + g + 8 * r);
-          }
-        }
-      }
+    // Issues the copies of a step; returns the tiles that are there, as bits.
+    auto issue = [&](int page, int j, int st) {
+      const uint32_t there = __ballot_sync(0xffffffffu, page >= 0);
+      const uint32_t bar = bars + 8 * st;
+      if (lane == 0)
+        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar),
+                     "r"(__popc(there) / 4 * PL::TILE_BYTES)
+                     : "memory");
+      __syncwarp();
+      if (page >= 0)
+        bulk_copy(ring + st * PL::STAGE + cdst,
+                  csrc + (p.kv.row(page, h) + ((j + 16 * ctile) & pmask)) * cbytes, 16 * cbytes, bar);
+      return there;
     };
-    auto load_v = [&]() {
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        if (rows[i] >= 0) {
-          const uint8_t *a = vc + rows[i] * ROW;
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            load_words<PL::VW>(a + ((r & 1) + (r & 2) * 4) * ROW, vraw[i][r]);
-#pragma unroll
-          for (int r = 0; r < 2; ++r) vs[i][r] = __ldg(p.kv.vs + rows[i] + g + 8 * r);
-        }
-      }
-    };
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-#pragma unroll
-      for (int w = 0; w < PL::KW; ++w) kraw[i][0][w] = kraw[i][1][w] = 0;
-#pragma unroll
-      for (int w = 0; w < PL::VW; ++w) vraw[i][0][w] = vraw[i][1][w] = vraw[i][2][w] = vraw[i][3][w] = 0;
-      ks[i][0] = ks[i][1] = vs[i][0] = vs[i][1] = 0.f;
-    }
     int j = first + u0 * PL::UNIT + warp * PL::STEP;
-    load_pages(j);
-    load_k(j);
-    load_v();
-    load_pages(u0 + 1 < u1 ? j + PL::UNIT : hi_max);
+    uint32_t there[S];
+    int page[S + 1];  // pages of the first steps; the last one: of the next to be issued
+#pragma unroll
+    for (int i = 0; i <= S; ++i) page[i] = u0 + i < u1 ? page_at(j + i * PL::UNIT) : -1;
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+      there[i] = 0;
+      if (u0 + i < u1) there[i] = issue(page[i], j + i * PL::UNIT, i);
+    }
+    int next = page[S];
+    int st = 0;
 
     for (int u = u0; u < u1; ++u, j += PL::UNIT) {
+      ok = ok && wait_stage(bars + 8 * st, (phases >> st) & 1u);
+      phases ^= 1u << st;
+      const uint32_t off = st * PL::STAGE;
+      const uint32_t now = there[0];  // this step's tiles
       // scores
       float s[NT][MT][4];
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
+        uint32_t kraw[2][PL::KW];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const uint32_t a = k_at + off + (16 * i + 8 * r) * ROW;
+          lds_words<(PL::KW < 4 ? PL::KW : 4)>(a, kraw[r]);
+          if (PL::KW == 8) lds_words<4>(a + 64, &kraw[r][PL::KW - 4]);
+        }
 #pragma unroll
         for (int n = 0; n < NT; ++n) s[n][i][0] = s[n][i][1] = s[n][i][2] = s[n][i][3] = 0.f;
 #pragma unroll
         for (int w = 0; w < PL::KW; ++w) {
           if (BITS == 4) {
             uint32_t a[4], c[4];
-            nibbles_to_h(kraw[i][0][w], a);
-            nibbles_to_h(kraw[i][1][w], c);
+            nibbles_to_h(kraw[0][w], a);
+            nibbles_to_h(kraw[1][w], c);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
               mma16816(s[n][i], a[0], c[0], a[1], c[1], qf[n][2 * w][0], qf[n][2 * w][1]);
@@ -337,8 +411,8 @@ __global__ void __launch_bounds__(kThreads, Plan<BITS, D, NT>::BLOCKS)
             }
           } else {
             uint32_t a0, a1, a2, a3;
-            bytes_to_h(kraw[i][0][w], a0, a2);
-            bytes_to_h(kraw[i][1][w], a1, a3);
+            bytes_to_h(kraw[0][w], a0, a2);
+            bytes_to_h(kraw[1][w], a1, a3);
 #pragma unroll
             for (int n = 0; n < NT; ++n) mma16816(s[n][i], a0, a1, a2, a3, qf[n][w][0], qf[n][w][1]);
           }
@@ -350,37 +424,35 @@ __global__ void __launch_bounds__(kThreads, Plan<BITS, D, NT>::BLOCKS)
       for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const float sk = ks[i][r] * (p.scale * kLog2e);
-          const bool zero = vs[i][r] == 0.f;
-          const float lv = zero ? 0.f : log2_fast(vs[i][r]);
-          rv[i][r] = zero ? 1.f : __frcp_rn(vs[i][r]);
+          uint32_t x, y;
+          lds_words<1>(ring + off + PL::OFF_KS + 4 * (16 * i + 8 * r + tokg), &x);
+          lds_words<1>(ring + off + PL::OFF_VS + 4 * (16 * i + 8 * r + tokg), &y);
+          const float sk = __uint_as_float(x) * (p.scale * kLog2e);
+          const float sv = y == 0 ? 1.f : __uint_as_float(y);
+          const float lv = log2_fast(sv);
+          rv[i][r] = rcp_fast(sv);
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) s[n][i][2 * r + e] = fmaf(s[n][i][2 * r + e], sk, lv);
         }
-      bool left_out = false;
-#pragma unroll
-      for (int i = 0; i < MT; ++i) left_out |= rows[i] < 0;
+      const bool left_out = __popc(now) != 4 * MT;
       if (j < lo_max || j + PL::STEP > hi_min || left_out) {
         // a tile at an end of some row's keys (or with a page outside the cache)
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            const int a = j + 16 * i + g + 8 * r;
-            if (a >= len || rows[i] < 0) rv[i][r] = 0.f;
+            const int a = j + 16 * i + 8 * r + tokg;
+            const bool out = ((now >> (4 * i)) & 1u) == 0;
+            if (a >= len || out) rv[i][r] = 0.f;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
               for (int e = 0; e < 2; ++e)
-                if (a < lo[n][e] || a >= hi[n][e] || rows[i] < 0) s[n][i][2 * r + e] = -CUDART_INF_F;
+                if (a < lo[n][e] || a >= hi[n][e] || out) s[n][i][2 * r + e] = -CUDART_INF_F;
           }
       }
-      // the next step's keys come in while this one is worked off
-      const bool more = u + 1 < u1;
-      if (more) load_k(j + PL::UNIT);
-
       // reference
       bool over = false;
       float top[NT][2];
@@ -428,6 +500,12 @@ __global__ void __launch_bounds__(kThreads, Plan<BITS, D, NT>::BLOCKS)
             pf[n][i][r] = transpose8x8(pack_h2(w0, w1));
           }
       // values
+      uint32_t vraw[MT][4][PL::VW];
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          lds_words<PL::VW>(v_at + off + v_row[r & 1] + (16 * i + (r & 2) * 4) * ROW, vraw[i][r]);
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -460,13 +538,26 @@ __global__ void __launch_bounds__(kThreads, Plan<BITS, D, NT>::BLOCKS)
             }
           }
         }
-      if (more) {
-        load_v();
-        load_pages(u + 2 < u1 ? j + 2 * PL::UNIT : hi_max);
+      // refill the stage: every lane has its registers
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i + 1 < S; ++i) there[i] = there[i + 1];
+      if (u + S < u1 && ok) {
+        const int now_page = next;
+        next = u + S + 1 < u1 ? page_at(j + (S + 1) * PL::UNIT) : -1;
+        there[S - 1] = issue(now_page, j + S * PL::UNIT, st);
       }
+      st = st + 1 == S ? 0 : st + 1;
+    }
+
+    if (!ok && u0 < u1) {
+      // a copy did not land: report it, and let the others land (bounded)
+      if (lane == 0) atomicCAS(p.kv.err, 0u, static_cast<unsigned>(kDevErrCacheCopy));
+      for (int i = 0; i < S; ++i) wait_stage(bars + 8 * i, (phases >> i) & 1u);
     }
 
     // -- join the warps -----------------------------------------------------------
+    __syncthreads();  // every ring is drained
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -523,6 +614,8 @@ __global__ void __launch_bounds__(kThreads, Plan<BITS, D, NT>::BLOCKS)
     }
     if (!whole && u0 == 0 && threadIdx.x == 0)
       descs[blockIdx.x] = Desc{b, h, rb, static_cast<int>((istart + nu - 1) / per)};
+    // the next copies (another proxy) write where the results were
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();
   }
 }
@@ -604,18 +697,35 @@ long long most_units(const KvAttnParams &p) {
   return p.B * p.kv.heads * rb * units;
 }
 
+// The kernel's shared memory, allowed once per device.
+template <int BITS, int D, int NT>
+bool allow_smem() {
+  static bool done[64] = {};
+  static std::mutex mu;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+  std::lock_guard<std::mutex> lock(mu);
+  if (!done[dev])
+    done[dev] = cudaFuncSetAttribute(kv_decode_kernel<BITS, D, NT>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     Plan<BITS, D, NT>::SMEM) == cudaSuccess;
+  return done[dev];
+}
+
 template <int BITS, int D, int NT>
 int launch_t(const KvAttnParams &p, cudaStream_t s) {
   using PL = Plan<BITS, D, NT>;
   const long long units = most_units<BITS, D, NT>(p);
   const long long room = kNumSMsGB300 * PL::BLOCKS;
   const int grid = static_cast<int>(units < room ? units : room);
+  if (!allow_smem<BITS, D, NT>()) return W8A8_ERR_CUDA;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = PL::SMEM;
   cfg.stream = s;
   cfg.attrs = at;
   cfg.numAttrs = 1;
@@ -626,6 +736,7 @@ int launch_t(const KvAttnParams &p, cudaStream_t s) {
   // no item can be cut when none has more than one unit
   if ((static_cast<long long>(p.table_w) << p.kv.page_shift) + 15 > PL::UNIT) {
     cfg.blockDim = dim3(512);
+    cfg.dynamicSmemBytes = 0;
     if (cudaLaunchKernelEx(&cfg, kv_decode_join_kernel<D, NT>, p, grid) != cudaSuccess) {
       cudaGetLastError();
       return W8A8_ERR_CUDA;
