@@ -92,17 +92,37 @@ __device__ __forceinline__ uint32_t h2_fma(uint32_t a, float m, float c) {
   return *reinterpret_cast<const uint32_t *>(&r);
 }
 
+// (w & MASK) ^ magic in one instruction.  One operand may be an immediate, so
+// the magic has to sit in a register: opaque() keeps the compiler from folding
+// it back, which would take two instructions (measured: a quarter of the
+// few-row attention kernel's integer work).
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t and_xor(uint32_t w, uint32_t magic) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(d) : "r"(w), "n"(MASK), "r"(magic));
+  return d;
+}
+__device__ __forceinline__ uint32_t opaque(uint32_t x) {
+  uint32_t d;
+  asm volatile("mov.b32 %0, %1;" : "=r"(d) : "r"(x));
+  return d;
+}
+
 // Two's-complement nibbles k and k + 4 of a word, k = 0 .. 3, as the fp16 pairs
 // o[k] = (nibble k, nibble k + 4): the nibble with its sign bit flipped (v + 8)
 // lands in the low bits of 1024 + (v + 8), or of 1024 + 16 (v + 8), which
 // one multiply-add brings back; every step is exact.
-__device__ __forceinline__ void nibbles_to_h(uint32_t w, uint32_t (&o)[4]) {
-  const uint32_t x = w >> 8;
-  o[0] = h2_add((w & 0x000f000fu) ^ 0x64086408u, -1032.f);
-  o[1] = h2_fma((w & 0x00f000f0u) ^ 0x64806480u, 0.0625f, -72.f);
-  o[2] = h2_add((x & 0x000f000fu) ^ 0x64086408u, -1032.f);
-  o[3] = h2_fma((x & 0x00f000f0u) ^ 0x64806480u, 0.0625f, -72.f);
-}
+struct Nibbles {
+  uint32_t lo, hi;  // the magics
+  __device__ __forceinline__ Nibbles() : lo(opaque(0x64086408u)), hi(opaque(0x64806480u)) {}
+  __device__ __forceinline__ void to_h(uint32_t w, uint32_t (&o)[4]) const {
+    const uint32_t x = w >> 8;
+    o[0] = h2_add(and_xor<0x000f000fu>(w, lo), -1032.f);
+    o[1] = h2_fma(and_xor<0x00f000f0u>(w, hi), 0.0625f, -72.f);
+    o[2] = h2_add(and_xor<0x000f000fu>(x, lo), -1032.f);
+    o[3] = h2_fma(and_xor<0x00f000f0u>(x, hi), 0.0625f, -72.f);
+  }
+};
 
 // Bytes 0, 1 and 2, 3 (two's complement) of a word as two fp16 pairs.
 __device__ __forceinline__ void bytes_to_h(uint32_t w, uint32_t &h01, uint32_t &h23) {

@@ -253,6 +253,7 @@ __global__ void __launch_bounds__(kThreads, Plan<BITS, D, NT>::BLOCKS)
   if (lane < S) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bars + 8 * lane));
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   __syncwarp();
+  const Nibbles nib;
   uint32_t phases = 0;  // bit s: parity of the next wait on stage s
   bool ok = true;
 
@@ -402,8 +403,8 @@ __global__ void __launch_bounds__(kThreads, Plan<BITS, D, NT>::BLOCKS)
         for (int w = 0; w < PL::KW; ++w) {
           if (BITS == 4) {
             uint32_t a[4], c[4];
-            nibbles_to_h(kraw[0][w], a);
-            nibbles_to_h(kraw[1][w], c);
+            nib.to_h(kraw[0][w], a);
+            nib.to_h(kraw[1][w], c);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
               mma16816(s[n][i], a[0], c[0], a[1], c[1], qf[n][2 * w][0], qf[n][2 * w][1]);
@@ -517,8 +518,8 @@ __global__ void __launch_bounds__(kThreads, Plan<BITS, D, NT>::BLOCKS)
             for (int half = 0; half < 2; ++half) {
               const int sel = half ? 0x7632 : 0x5410;
               uint32_t a[4], c[4];
-              nibbles_to_h(__byte_perm(x0, x1, sel), a);
-              nibbles_to_h(__byte_perm(x2, x3, sel), c);
+              nib.to_h(__byte_perm(x0, x1, sel), a);
+              nib.to_h(__byte_perm(x2, x3, sel), c);
 #pragma unroll
               for (int n = 0; n < NT; ++n) {
                 mma16816(o[n][4 * w + 2 * half], a[0], a[1], c[0], c[1], pf[n][i][0], pf[n][i][1]);
