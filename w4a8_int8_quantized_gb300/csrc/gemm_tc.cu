@@ -57,6 +57,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "tc_ptx.cuh"
 
 namespace w8a8 {
 namespace {
@@ -64,10 +65,9 @@ namespace {
 constexpr int BW = 128, BK = 64;  // weight rows (output channels) per tile, K block
 constexpr int NUM_THREADS = 512;
 constexpr int EPI_WARPS = 8, EPI_THREADS = EPI_WARPS * 32;
-// Limit of every bounded wait, in SM clock cycles (about 2 s at 2 GHz).  The
-// role waits take theirs from the launch (TcParams::wait_limit, this value
-// unless a test shortened it); the teardown waits always use this one.
-constexpr long long kTimeoutCycles = 4000000000LL;
+// The role waits take their limit from the launch (TcParams::wait_limit,
+// kTimeoutCycles unless a test shortened it); the teardown waits always use
+// kTimeoutCycles.
 
 // Shared-memory plan.  XH: activations arrive as fp16 codes (TMA straight
 // into the operand layout); BT: tokens per tile (activations as INT8 codes
@@ -149,99 +149,6 @@ struct TcParams {
   int skip_first_copy;   // test only: leave the first staging copy of each CTA unissued
 };
 
-// ---------------------------------------------------------------- PTX ----
-
-__device__ __forceinline__ uint32_t smem_u32(const void *p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count));
-}
-
-// HINT: the waiting thread re-checks at least every 100 ns instead of
-// after the system-dependent suspend time (measured on GB300: the per
-// channel kernels ~2 % faster, the per-group ones ~4 % slower, so only the
-// former pass it).
-template <bool HINT = false>
-__device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  if (HINT)
-    asm volatile(
-        "{\n.reg .pred p;\n"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
-        "selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(100)
-        : "memory");
-  else
-    asm volatile(
-        "{\n.reg .pred p;\n"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-        "selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-  return ok != 0;
-}
-
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-__device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar),
-               "r"(bytes)
-               : "memory");
-}
-
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map,
-                                            uint32_t bar, int x, int y) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
-      : "memory");
-}
-
-__device__ __forceinline__ void fence_proxy_async() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
-__device__ __forceinline__ void tc_fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-
-__device__ __forceinline__ void tc_fence_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-
-__device__ __forceinline__ void tc_commit(uint32_t bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-      : "memory");
-}
-
-__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t adesc, uint64_t bdesc,
-                                       uint32_t idesc, uint32_t accum) {
-  asm volatile(
-      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accum));
-}
-
-// shared-memory matrix descriptor: K-major, 128-byte swizzle, 8-row groups
-// 1024 bytes apart (rows are 128 bytes), descriptor version 1
-__device__ __forceinline__ uint64_t sw128_desc(uint32_t addr) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((addr & 0x3ffff) >> 4);      // start address
-  d |= static_cast<uint64_t>(1) << 16;                    // leading byte offset (unused)
-  d |= static_cast<uint64_t>(1024 >> 4) << 32;            // stride byte offset
-  d |= static_cast<uint64_t>(1) << 46;                    // version
-  d |= static_cast<uint64_t>(2) << 61;                    // 128-byte swizzle
-  return d;
-}
-
 // Ordered memory accesses for the epilogue: as volatile asm they keep their
 // program order, so a fully unrolled loop does not hoist all of its loads
 // ahead of its stores (which would need one register per load).
@@ -259,35 +166,6 @@ __device__ __forceinline__ void stg_b16(void *ptr, __half v) {
 
 __device__ __forceinline__ void stg_b32(void *ptr, int v) {
   asm volatile("st.global.b32 [%0], %1;" ::"l"(ptr), "r"(v) : "memory");
-}
-
-// Bounded wait.  Returns false if the CTA is aborting or the wait gave up
-// (then it records `code` and raises the abort flag).
-template <bool HINT = false>
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity,
-                                         volatile int *abort_flag, unsigned int code,
-                                         unsigned int *err, long long limit) {
-#pragma unroll 1
-  for (int i = 0; i < 32; ++i)
-    if (mbar_try_wait<HINT>(bar, parity)) return true;
-  const long long t0 = clock64();
-  while (true) {
-    if (mbar_try_wait<HINT>(bar, parity)) return true;
-    if (*abort_flag) return false;
-    if (clock64() - t0 > limit) {
-      if (err != nullptr) atomicCAS(err, 0u, code);
-      *abort_flag = 1;
-      return false;
-    }
-  }
-}
-
-// Bounded wait that ignores the abort flag (teardown: let own work land).
-__device__ __forceinline__ void wait_bar_teardown(uint32_t bar, uint32_t parity) {
-  const long long t0 = clock64();
-  while (!mbar_try_wait(bar, parity)) {
-    if (clock64() - t0 > kTimeoutCycles) return;
-  }
 }
 
 // 4 INT8 (one 32-bit word) -> 4 fp16, exactly: bytes b become halves with
@@ -404,35 +282,6 @@ __device__ __forceinline__ void convert_sub(const uint8_t *src, uint8_t *dst, in
       *reinterpret_cast<uint4 *>(row + (((2 * c4 + 1) ^ x) << 4)) = hi;
     }
   }
-}
-
-// 32 consecutive TMEM columns of this thread's lane
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]),
-        "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]),
-        "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]),
-        "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
-        "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]),
-        "=r"(v[30]), "=r"(v[31])
-      : "r"(taddr));
-}
-
-// Waits for this thread's TMEM loads; the loaded registers pass through the
-// statement, so no use of them can be scheduled before it.
-__device__ __forceinline__ void tmem_wait_ld32(uint32_t (&v)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]),
-                 "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]),
-                 "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]), "+r"(v[17]),
-                 "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]),
-                 "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]),
-                 "+r"(v[30]), "+r"(v[31])
-               :
-               : "memory");
 }
 
 // Epilogue of the tensor-core GEMM (warps 8-15): drains the TMEM
