@@ -13,7 +13,7 @@ int launch_kv_write(const KvView &kv, int bits, int D, const __half *k, long lon
 int launch_kv_read(const KvView &kv, int bits, int D, const long long *slots, int T, __half *k,
                    __half *v, cudaStream_t s);
 size_t kv_attn_workspace(int T, int Hq, int max_q, int B, long long max_len, const KvView &kv,
-                         int D);
+                         int bits, int D);
 int launch_kv_attn(const KvAttnParams &p, int bits, int D, cudaStream_t s);
 
 namespace {
@@ -125,7 +125,7 @@ size_t kv_cache_attention_workspace_bytes(int T, int q_heads, int B, int max_q, 
   if (T == 0 || B == 0) return 0;
   return kv_attn_workspace(T, q_heads, max_q < T ? max_q : T, B,
                            static_cast<long long>(table_width) * cache->page_size,
-                           view_of(cache), cache->head_dim);
+                           view_of(cache), cache->bits, cache->head_dim);
 }
 
 int kv_cache_attention(const w8a8_half *q, long long q_token_stride, long long q_head_stride,

@@ -81,9 +81,9 @@ __global__ void __launch_bounds__(128) kv_attn_row_kernel(const KvAttnParams p) 
 }  // namespace
 
 size_t kv_attn_workspace(int T, int Hq, int max_q, int B, long long max_len, const KvView &kv,
-                         int D) {
+                         int bits, int D) {
   const long long rows = static_cast<long long>(max_q) * (Hq / kv.heads);
-  return rows <= kFewRows ? kv_decode_workspace(D, static_cast<int>(rows)) : 0;
+  return rows <= kFewRows ? kv_decode_workspace(D, rows) : 0;
 }
 
 int launch_kv_attn(const KvAttnParams &p, int bits, int D, cudaStream_t s) {

@@ -25,7 +25,7 @@ __device__ __forceinline__ void store_row4(const KvAttnParams &p, long long row,
 // Rows per kv head and sequence up to which the few-row kernel runs.
 constexpr int kFewRows = 64;
 
-size_t kv_decode_workspace(int D, int rows);
+size_t kv_decode_workspace(int D, long long rows);
 int launch_kv_decode(const KvAttnParams &p, int bits, int D, cudaStream_t s);
 
 }  // namespace w8a8

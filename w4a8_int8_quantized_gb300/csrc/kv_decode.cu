@@ -12,18 +12,15 @@
 //
 // The contraction index of either product may be permuted freely as long as
 // both operands agree, which removes every shuffle between memory and the
-// tensor cores:
-//   S^T = K Q^T   lane (g, t) = (lane / 4, lane % 4) loads the same 16 bytes
-//                 (4 bits, D = 128) of the rows of tokens g and g + 8; its
-//                 codes are the operand of D / 16 products once converted, and
-//                 Q is laid out to match once per item;
-//   O^T = V^T P^T the lane loads the bytes of d = D/8 g .. of tokens 2t, 2t+1,
-//                 2t+8, 2t+9; two tokens' words are merged by a byte permute
-//                 so that one conversion gives pairs of tokens;
-//   P^T           the scores' accumulator holds (token g, rows 2t, 2t+1); one
-//                 8x8 transpose (movmatrix) per 8 tokens makes it the operand.
-// Codes go straight from global memory into registers, the next step's loads
-// issued as soon as the current ones are converted.
+// tensor cores (lane = 4 g + t throughout):
+//   S^T = K Q^T   the lane reads 16 bytes (4 bits, D = 128) of the rows of two
+//                 tokens per tile of 16; its codes are the operand of D / 16
+//                 products once converted, and Q is laid out to match once per
+//                 item;
+//   O^T = V^T P^T the lane reads its D / 8 values of the tokens of its columns;
+//                 tokens are merged into operand registers by byte permutes.
+// Codes arrive in a ring of shared-memory stages per warp, by bulk copies that
+// the warp itself issues two steps ahead, page by page.
 //
 // Softmax: u = S * scale * log2e * s_k + log2 s_v, weight p = 2^(u - M), so the
 // weight carries the value's scale: O = sum p code_v with exact codes, and the
@@ -69,23 +66,24 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+// BITS, D: the cache; NT: column tiles of 8 rows in an item.
 template <int BITS, int D, int NT>
 struct Plan {
   static constexpr int ROW = D * BITS / 8;           // bytes of a token's codes
-  static constexpr int MT = 16 / BITS * 64 / D;      // 16-token tiles per step: 32 registers of codes
+  static constexpr int MT = 16 / BITS * 64 / D;      // 16-token tiles per step: 2 KB of K
   static constexpr int STEP = 16 * MT;               // tokens of a warp's step
   static constexpr int UNIT = kWarps * STEP;         // tokens of a block's step
   static constexpr int KW = ROW / 16;                // K words per token and lane
   static constexpr int VW = ROW / 32;                // V words per token and lane
-  static constexpr int MMAS = D / 16;                // products along D
-  static constexpr int COLS = 8 * NT;
+  static constexpr int MMAS = D / 16;                // 16-row tiles of D
+  static constexpr int COLS = 8 * NT;  // rows of an item
   static constexpr int PAD = D + 4;                  // floats of a staged row
   static constexpr int BLOCKS = NT == 1 ? 4 : 3;     // resident per SM
   // a stage of a warp's ring: one step's K codes, V codes, K scales, V scales
   static constexpr int OFF_V = STEP * ROW, OFF_KS = 2 * STEP * ROW, OFF_VS = OFF_KS + STEP * 4;
   static constexpr int STAGE = OFF_VS + STEP * 4;
   static constexpr int TILE_BYTES = 2 * 16 * ROW + 2 * 16 * 4;  // of one 16-token tile
-  static constexpr int STAGES = 3;
+  static constexpr int STAGES = BLOCKS == 4 ? 3 : 4;
   static constexpr int RING = kWarps * STAGES * STAGE;
   static constexpr int JOIN = kWarps * COLS * PAD * 4;  // the warps' results, over the drained ring
   static constexpr int SMEM = (RING > JOIN ? RING : JOIN) + kWarps * STAGES * 8;
@@ -160,6 +158,284 @@ __device__ __forceinline__ void load_words(const uint8_t *p, uint32_t *o) {
   }
 }
 
+// What a warp knows of its item: which keys its rows see.
+struct Item {
+  int b, h, rb, R;             // sequence, kv head, row block, its rows
+  int q0, nq, len;             // queries, tokens of the sequence
+  int lo_max, hi_min, hi_max;  // keys [lo_max, hi_min) are seen by all rows, none from hi_max on
+  bool bad;                    // a page outside the cache was met
+
+  // output row of row c
+  __device__ __forceinline__ long long row(const KvAttnParams &p, int c, int cols) const {
+    const int ri = rb * cols + c;
+    return (static_cast<long long>(q0) + ri / p.group) * p.Hq + h * p.group + ri % p.group;
+  }
+  // its query
+  __device__ __forceinline__ const __half *query(const KvAttnParams &p, int c, int cols) const {
+    const int ri = rb * cols + c;
+    return p.q + (q0 + ri / p.group) * p.q_ts + static_cast<long long>(h * p.group + ri % p.group) * p.q_hs;
+  }
+  __device__ __forceinline__ void limits(const KvAttnParams &p, int c, int cols, int &lo, int &hi) const {
+    lo = hi = 0;
+    if (c < R) visible(p, len - nq + (rb * cols + c) / p.group, len, lo, hi);
+  }
+  // token a belongs to a page outside the cache
+  __device__ __forceinline__ bool gone(const KvAttnParams &p, int a) const {
+    return bad && a < hi_max && page_of(p, b, a >> p.kv.page_shift) < 0;
+  }
+};
+
+// A token's scales from a stage: s_k times `f`, log2 s_v and 1 / s_v.  s_v = 0
+// has all codes 0, so any scale will do.
+__device__ __forceinline__ void token_scales(uint32_t ks_at, uint32_t vs_at, float f, float &sk,
+                                             float &lv, float &rv) {
+  uint32_t x, y;
+  lds_words<1>(ks_at, &x);
+  lds_words<1>(vs_at, &y);
+  sk = __uint_as_float(x) * f;
+  const float sv = y == 0 ? 1.f : __uint_as_float(y);
+  lv = log2_fast(sv);
+  rv = rcp_fast(sv);
+}
+
+template <int BITS, int D, int NT>
+struct Math {
+  using PL = Plan<BITS, D, NT>;
+  static constexpr int MT = PL::MT, MMAS = PL::MMAS, ROW = PL::ROW, COLS = PL::COLS;
+  const KvAttnParams &p;
+  const int g, t;
+  const Nibbles nib;
+  const float f;
+  uint32_t k_at, v_at, v_row[2], s_at;
+  int tokg;
+  uint32_t qf[NT][MMAS][2];  // Q: column g of each n
+  float o[NT][MMAS][4];
+  float m[NT][2], l[NT][2];
+  int lo[NT][2], hi[NT][2];
+
+  __device__ __forceinline__ Math(const KvAttnParams &p, int lane)
+      : p(p), g(lane >> 2), t(lane & 3), f(p.scale * kLog2e) {
+    // Row r of a 16-token product stands for token tok(r) (+ 8 for the second
+    // half): rows 2t and 2t + 1 are tokens t and 4 + (t ^ 1), so that the lanes
+    // of a value load (rows 2t of four t) and of a key load (rows g, g + 1) read
+    // rows of both parities of 64 bytes, half of the bank conflicts of tokens
+    // in their own order.
+    tokg = (g & 1) ? 4 + ((g >> 1) ^ 1) : g >> 1;
+    k_at = tokg * ROW + t * (PL::KW >= 4 ? 16 : PL::KW * 4);
+    v_at = PL::OFF_V + g * (PL::VW * 4);
+    v_row[0] = t * ROW;
+    v_row[1] = (4 + (t ^ 1)) * ROW;
+    s_at = PL::OFF_KS + 4 * tokg;
+  }
+
+  __device__ __forceinline__ void begin(const Item &it) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int c = n * 8 + g;
+      const bool on = c < it.R;
+      const __half *qp = it.query(p, on ? c : 0, COLS);
+#pragma unroll
+      for (int w = 0; w < PL::KW; ++w) {
+        uint32_t x[4] = {0, 0, 0, 0};
+        if (BITS == 4) {
+          // word w holds d = 8 (t KW + w) .. + 7, in pairs (k, k + 4)
+          if (on) load_words<4>(reinterpret_cast<const uint8_t *>(qp + 8 * (t * PL::KW + w)), x);
+          qf[n][2 * w][0] = __byte_perm(x[0], x[2], 0x5410);
+          qf[n][2 * w][1] = __byte_perm(x[0], x[2], 0x7632);
+          qf[n][2 * w + 1][0] = __byte_perm(x[1], x[3], 0x5410);
+          qf[n][2 * w + 1][1] = __byte_perm(x[1], x[3], 0x7632);
+        } else {
+          // words 0-3: d = 16 t + 4 w .. + 3, words 4-7: 64 further on
+          const int d = (w & 4) * 16 + 16 * t + 4 * (w & 3);
+          if (on) load_words<2>(reinterpret_cast<const uint8_t *>(qp + d), x);
+          qf[n][w][0] = x[0];
+          qf[n][w][1] = x[1];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < MMAS; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[n][i][e] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        m[n][e] = kNoRef;
+        l[n][e] = 0.f;
+        it.limits(p, n * 8 + 2 * t + e, COLS, lo[n][e], hi[n][e]);
+      }
+    }
+  }
+
+  // The step whose codes are at `stage` and whose first token is j; `ends`:
+  // not every row sees every token.
+  __device__ __forceinline__ void step(const Item &it, uint32_t stage, int j, bool ends) {
+    float s[NT][MT][4];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      uint32_t kraw[2][PL::KW];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const uint32_t a = stage + k_at + (16 * i + 8 * r) * ROW;
+        lds_words<(PL::KW < 4 ? PL::KW : 4)>(a, kraw[r]);
+        if (PL::KW == 8) lds_words<4>(a + 64, &kraw[r][PL::KW - 4]);
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) s[n][i][0] = s[n][i][1] = s[n][i][2] = s[n][i][3] = 0.f;
+#pragma unroll
+      for (int w = 0; w < PL::KW; ++w) {
+        if (BITS == 4) {
+          uint32_t a[4], c[4];
+          nib.to_h(kraw[0][w], a);
+          nib.to_h(kraw[1][w], c);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma16816(s[n][i], a[0], c[0], a[1], c[1], qf[n][2 * w][0], qf[n][2 * w][1]);
+            mma16816(s[n][i], a[2], c[2], a[3], c[3], qf[n][2 * w + 1][0], qf[n][2 * w + 1][1]);
+          }
+        } else {
+          uint32_t a0, a1, a2, a3;
+          bytes_to_h(kraw[0][w], a0, a2);
+          bytes_to_h(kraw[1][w], a1, a3);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma16816(s[n][i], a0, a1, a2, a3, qf[n][w][0], qf[n][w][1]);
+        }
+      }
+    }
+    // exponents
+    float rv[MT][2];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const uint32_t a = stage + s_at + 4 * (16 * i + 8 * r);
+        float sk, lv;
+        token_scales(a, a + 4 * PL::STEP, f, sk, lv, rv[i][r]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) s[n][i][2 * r + e] = fmaf(s[n][i][2 * r + e], sk, lv);
+      }
+    if (ends) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int a = j + 16 * i + 8 * r + tokg;
+          const bool out = a >= it.len || it.gone(p, a);
+          if (out) rv[i][r] = 0.f;
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (out || a < lo[n][e] || a >= hi[n][e]) s[n][i][2 * r + e] = -CUDART_INF_F;
+        }
+    }
+    // reference
+    bool over = false;
+    float top[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        top[n][e] = -CUDART_INF_F;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) top[n][e] = fmaxf(top[n][e], fmaxf(s[n][i][e], s[n][i][2 + e]));
+        over |= top[n][e] > m[n][e] + kRoom;
+      }
+    if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = top[n][e];
+#pragma unroll
+          for (int q = 4; q < 32; q <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, q));
+          const float nm = x > m[n][e] + kRoom ? x - kHead : m[n][e];
+          const float a = exp2_fast(m[n][e] - nm);
+          m[n][e] = nm;
+          l[n][e] *= a;
+#pragma unroll
+          for (int i = 0; i < MMAS; ++i) {
+            o[n][i][e] *= a;
+            o[n][i][2 + e] *= a;
+          }
+        }
+    }
+    // weights
+    uint32_t pf[NT][MT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float w0 = exp2_fast(s[n][i][2 * r] - m[n][0]);
+          const float w1 = exp2_fast(s[n][i][2 * r + 1] - m[n][1]);
+          l[n][0] = fmaf(w0, rv[i][r], l[n][0]);
+          l[n][1] = fmaf(w1, rv[i][r], l[n][1]);
+          pf[n][i][r] = transpose8x8(pack_h2(w0, w1));
+        }
+    // values
+    uint32_t vraw[MT][4][PL::VW];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        lds_words<PL::VW>(stage + v_at + v_row[r & 1] + (16 * i + (r & 2) * 4) * ROW, vraw[i][r]);
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int w = 0; w < PL::VW; ++w) {
+        const uint32_t x0 = vraw[i][0][w], x1 = vraw[i][1][w];
+        const uint32_t x2 = vraw[i][2][w], x3 = vraw[i][3][w];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          if (BITS == 4) {
+            const int sel = half ? 0x7632 : 0x5410;
+            uint32_t a[4], c[4];
+            nib.to_h(__byte_perm(x0, x1, sel), a);
+            nib.to_h(__byte_perm(x2, x3, sel), c);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              mma16816(o[n][4 * w + 2 * half], a[0], a[1], c[0], c[1], pf[n][i][0], pf[n][i][1]);
+              mma16816(o[n][4 * w + 2 * half + 1], a[2], a[3], c[2], c[3], pf[n][i][0], pf[n][i][1]);
+            }
+          } else {
+            const int sel = half ? 0x7362 : 0x5140;
+            uint32_t a0, a1, a2, a3;
+            bytes_to_h(__byte_perm(x0, x1, sel), a0, a1);
+            bytes_to_h(__byte_perm(x2, x3, sel), a2, a3);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+              mma16816(o[n][2 * w + half], a0, a1, a2, a3, pf[n][i][0], pf[n][i][1]);
+          }
+        }
+      }
+  }
+
+  // This warp's sums of the item: o_sm [COLS][PAD], references and sums of weights.
+  __device__ __forceinline__ void finish(float (*o_sm)[PL::PAD], float *m_sm, float *l_sm) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int c = n * 8 + 2 * t + e;
+        float x = l[n][e];
+#pragma unroll
+        for (int q = 4; q < 32; q <<= 1) x += __shfl_xor_sync(0xffffffffu, x, q);
+        if (g == 0) {
+          m_sm[c] = m[n][e];
+          l_sm[c] = x;
+        }
+        // this lane's d: MMAS pairs (2 i, 2 i + 1) from 2 MMAS g on
+        float *dst = &o_sm[c][2 * MMAS * g];
+#pragma unroll
+        for (int i = 0; i < MMAS; i += 2)
+          *reinterpret_cast<float4 *>(dst + 2 * i) =
+              make_float4(o[n][i][e], o[n][i][2 + e], o[n][i + 1][e], o[n][i + 1][2 + e]);
+      }
+  }
+};
+
 // Keys that any query of sequence b sees: units of UNIT tokens from `first`
 // (a multiple of 16), at least one unit when there is a query to answer.
 template <int UNIT>
@@ -181,12 +457,12 @@ template <int BITS, int D, int NT>
 __global__ void __launch_bounds__(kThreads, Plan<BITS, D, NT>::BLOCKS)
     kv_decode_kernel(const KvAttnParams p) {
   using PL = Plan<BITS, D, NT>;
-  constexpr int MT = PL::MT, COLS = PL::COLS, MMAS = PL::MMAS, ROW = PL::ROW;
+  constexpr int MT = PL::MT, COLS = PL::COLS, ROW = PL::ROW;
   extern __shared__ __align__(128) uint8_t dyn[];
   float(*o_sm)[COLS][PL::PAD] = reinterpret_cast<float(*)[COLS][PL::PAD]>(dyn);
   __shared__ float m_sm[kWarps][COLS], l_sm[kWarps][COLS];
   __shared__ long long sums[kThreads];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
@@ -253,27 +529,20 @@ __global__ void __launch_bounds__(kThreads, Plan<BITS, D, NT>::BLOCKS)
   if (lane < S) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bars + 8 * lane));
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   __syncwarp();
-  const Nibbles nib;
   uint32_t phases = 0;  // bit s: parity of the next wait on stage s
   bool ok = true;
+  Math<BITS, D, NT> math(p, lane);
 
-  // Row r of a 16-token product stands for token tok(r) (+ 8 for the second
-  // half): rows 2t and 2t + 1 are tokens t and 4 + (t ^ 1), so that the lanes
-  // of a value load (rows 2t of four t) and of a key load (rows g, g + 1) read
-  // rows of both parities of 64 bytes, half of the bank conflicts of tokens
-  // in their own order.
-  const int tokg = (g & 1) ? 4 + ((g >> 1) ^ 1) : g >> 1;
-  const uint32_t k_at = ring + tokg * ROW + t * (PL::KW >= 4 ? 16 : PL::KW * 4);
-  const uint32_t v_at = ring + PL::OFF_V + g * (PL::VW * 4);
-  const uint32_t v_row[2] = {static_cast<uint32_t>(t) * ROW, static_cast<uint32_t>(4 + (t ^ 1)) * ROW};
-  // copies: lane i < 4 MT brings array i % 4 (K, V, K scales, V scales) of tile i / 4
-  const int ctile = lane >> 2, carr = lane & 3;
+  // copies: lane i < 4 MT brings array i % 4 (K, V, K scales, V scales) of tile
+  // i / 4; `page_bytes` from one page to the next
+  const int ctile = 16 * (lane >> 2), carr = lane & 3;
   const bool copier = lane < 4 * MT;
   const uint8_t *csrc = carr == 0 ? p.kv.kc : carr == 1 ? p.kv.vc
                         : reinterpret_cast<const uint8_t *>(carr == 2 ? p.kv.ks : p.kv.vs);
-  const int cbytes = carr < 2 ? ROW : 4;  // per token
-  const uint32_t cdst = (carr == 0 ? 0 : carr == 1 ? PL::OFF_V : carr == 2 ? PL::OFF_KS : PL::OFF_VS) +
-                        ctile * 16 * cbytes;
+  const uint32_t cbytes = carr < 2 ? ROW : 4;  // per token
+  const uint32_t page_bytes = (static_cast<uint32_t>(p.kv.heads) << p.kv.page_shift) * cbytes;
+  const uint32_t cdst = ring + ctile * cbytes +
+                        (carr == 0 ? 0 : carr == 1 ? PL::OFF_V : carr == 2 ? PL::OFF_KS : PL::OFF_VS);
   const int pmask = (1 << p.kv.page_shift) - 1;
 
   for (long long at = c0; at < c1;) {
@@ -284,274 +553,73 @@ __global__ void __launch_bounds__(kThreads, Plan<BITS, D, NT>::BLOCKS)
     // item: units [istart, istart + nu) of the line
     const int item = static_cast<int>((at - start) / nu);
     const long long istart = start + static_cast<long long>(item) * nu;
-    const int h = item / nrb, rb = item % nrb;
     const int u0 = static_cast<int>(at - istart);
     const int u1 = static_cast<int>(min(static_cast<long long>(nu), c1 - istart));
     at = istart + u1;
-    const int R = min(nq * p.group - rb * COLS, COLS);  // rows of this block
-
-    // limits of the rows
-    int lo[NT][2], hi[NT][2], lo_max, hi_min, hi_max;
+    Item it;
+    it.b = b;
+    it.h = item / nrb;
+    it.rb = item % nrb;
+    it.R = min(nq * p.group - it.rb * COLS, COLS);
+    it.q0 = q0;
+    it.nq = nq;
+    it.len = len;
+    it.bad = false;
     {
       int x;
-      visible(p, len - nq + rb * COLS / p.group, len, x, hi_min);
-      visible(p, len - nq + (rb * COLS + R - 1) / p.group, len, lo_max, hi_max);
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int c = n * 8 + 2 * t + e;
-          lo[n][e] = hi[n][e] = 0;
-          if (c < R) visible(p, len - nq + (rb * COLS + c) / p.group, len, lo[n][e], hi[n][e]);
-        }
-    }
-
-    // Q, as the second operand of the products over D: column g of each n
-    uint32_t qf[NT][MMAS][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int c = n * 8 + g;
-      const bool on = c < R;
-      const int ri = rb * COLS + (on ? c : 0);
-      const __half *qp = p.q + (q0 + ri / p.group) * p.q_ts +
-                         static_cast<long long>(h * p.group + ri % p.group) * p.q_hs;
-#pragma unroll
-      for (int w = 0; w < PL::KW; ++w) {
-        uint32_t x[4] = {0, 0, 0, 0};
-        if (BITS == 4) {
-          // word w holds d = 8 (t KW + w) .. + 7
-          if (on) load_words<4>(reinterpret_cast<const uint8_t *>(qp + 8 * (t * PL::KW + w)), x);
-          qf[n][2 * w][0] = __byte_perm(x[0], x[2], 0x5410);
-          qf[n][2 * w][1] = __byte_perm(x[0], x[2], 0x7632);
-          qf[n][2 * w + 1][0] = __byte_perm(x[1], x[3], 0x5410);
-          qf[n][2 * w + 1][1] = __byte_perm(x[1], x[3], 0x7632);
-        } else {
-          // words 0-3: d = 16 t + 4 w .. + 3, words 4-7: 64 further on
-          const int d = (w & 4) * 16 + 16 * t + 4 * (w & 3);
-          if (on) load_words<2>(reinterpret_cast<const uint8_t *>(qp + d), x);
-          qf[n][w][0] = x[0];
-          qf[n][w][1] = x[1];
-        }
-      }
-    }
-
-    float o[NT][MMAS][4];
-    float m[NT][2], l[NT][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-#pragma unroll
-      for (int i = 0; i < MMAS; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[n][i][e] = 0.f;
-      m[n][0] = m[n][1] = kNoRef;
-      l[n][0] = l[n][1] = 0.f;
+      visible(p, len - nq + it.rb * COLS / p.group, len, x, it.hi_min);
+      visible(p, len - nq + (it.rb * COLS + it.R - 1) / p.group, len, it.lo_max, it.hi_max);
     }
 
     // -- steps: this warp's tokens are j .. j + STEP - 1 of each unit ----------
-    // Page of the copier's tile of the step at token j (-1: left out, also
-    // past the last key); fetched a step before the copies that use it.
+    // Page of the copier's tile of the step at token j (-1: past the last key,
+    // -2: outside the cache); fetched a step before the copies that use it.
+    const uint8_t *hsrc = csrc + (static_cast<size_t>(it.h) << p.kv.page_shift) * cbytes;
     auto page_at = [&](int j) {
-      const int a = j + 16 * ctile;
-      return copier && a < hi_max ? page_of(p, b, a >> p.kv.page_shift) : -1;
+      const int a = j + ctile;
+      if (!copier || a >= it.hi_max) return -1;
+      const int e = page_of(p, b, a >> p.kv.page_shift);
+      return e < 0 ? -2 : e;
     };
-    // Issues the copies of a step; returns the tiles that are there, as bits.
     auto issue = [&](int page, int j, int st) {
       const uint32_t there = __ballot_sync(0xffffffffu, page >= 0);
       const uint32_t bar = bars + 8 * st;
+      if (__popc(there) != 4 * MT && __any_sync(0xffffffffu, page == -2)) it.bad = true;
       if (lane == 0)
         asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar),
                      "r"(__popc(there) / 4 * PL::TILE_BYTES)
                      : "memory");
       __syncwarp();
       if (page >= 0)
-        bulk_copy(ring + st * PL::STAGE + cdst,
-                  csrc + (p.kv.row(page, h) + ((j + 16 * ctile) & pmask)) * cbytes, 16 * cbytes, bar);
-      return there;
+        bulk_copy(cdst + st * PL::STAGE,
+                  hsrc + static_cast<size_t>(page) * page_bytes + ((j + ctile) & pmask) * cbytes,
+                  16 * cbytes, bar);
     };
     int j = first + u0 * PL::UNIT + warp * PL::STEP;
-    uint32_t there[S];
     int page[S + 1];  // pages of the first steps; the last one: of the next to be issued
 #pragma unroll
     for (int i = 0; i <= S; ++i) page[i] = u0 + i < u1 ? page_at(j + i * PL::UNIT) : -1;
 #pragma unroll
-    for (int i = 0; i < S; ++i) {
-      there[i] = 0;
-      if (u0 + i < u1) there[i] = issue(page[i], j + i * PL::UNIT, i);
-    }
+    for (int i = 0; i < S; ++i)
+      if (u0 + i < u1) issue(page[i], j + i * PL::UNIT, i);
     int next = page[S];
     int st = 0;
+    math.begin(it);
 
     for (int u = u0; u < u1; ++u, j += PL::UNIT) {
       ok = ok && wait_stage(bars + 8 * st, (phases >> st) & 1u);
       phases ^= 1u << st;
-      const uint32_t off = st * PL::STAGE;
-      const uint32_t now = there[0];  // this step's tiles
-      // scores
-      float s[NT][MT][4];
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        uint32_t kraw[2][PL::KW];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const uint32_t a = k_at + off + (16 * i + 8 * r) * ROW;
-          lds_words<(PL::KW < 4 ? PL::KW : 4)>(a, kraw[r]);
-          if (PL::KW == 8) lds_words<4>(a + 64, &kraw[r][PL::KW - 4]);
-        }
-#pragma unroll
-        for (int n = 0; n < NT; ++n) s[n][i][0] = s[n][i][1] = s[n][i][2] = s[n][i][3] = 0.f;
-#pragma unroll
-        for (int w = 0; w < PL::KW; ++w) {
-          if (BITS == 4) {
-            uint32_t a[4], c[4];
-            nib.to_h(kraw[0][w], a);
-            nib.to_h(kraw[1][w], c);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              mma16816(s[n][i], a[0], c[0], a[1], c[1], qf[n][2 * w][0], qf[n][2 * w][1]);
-              mma16816(s[n][i], a[2], c[2], a[3], c[3], qf[n][2 * w + 1][0], qf[n][2 * w + 1][1]);
-            }
-          } else {
-            uint32_t a0, a1, a2, a3;
-            bytes_to_h(kraw[0][w], a0, a2);
-            bytes_to_h(kraw[1][w], a1, a3);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) mma16816(s[n][i], a0, a1, a2, a3, qf[n][w][0], qf[n][w][1]);
-          }
-        }
-      }
-      // exponents, and per token 1 / s_v
-      float rv[MT][2];
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          uint32_t x, y;
-          lds_words<1>(ring + off + PL::OFF_KS + 4 * (16 * i + 8 * r + tokg), &x);
-          lds_words<1>(ring + off + PL::OFF_VS + 4 * (16 * i + 8 * r + tokg), &y);
-          const float sk = __uint_as_float(x) * (p.scale * kLog2e);
-          const float sv = y == 0 ? 1.f : __uint_as_float(y);
-          const float lv = log2_fast(sv);
-          rv[i][r] = rcp_fast(sv);
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) s[n][i][2 * r + e] = fmaf(s[n][i][2 * r + e], sk, lv);
-        }
-      const bool left_out = __popc(now) != 4 * MT;
-      if (j < lo_max || j + PL::STEP > hi_min || left_out) {
-        // a tile at an end of some row's keys (or with a page outside the cache)
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const int a = j + 16 * i + 8 * r + tokg;
-            const bool out = ((now >> (4 * i)) & 1u) == 0;
-            if (a >= len || out) rv[i][r] = 0.f;
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-                if (a < lo[n][e] || a >= hi[n][e] || out) s[n][i][2 * r + e] = -CUDART_INF_F;
-          }
-      }
-      // reference
-      bool over = false;
-      float top[NT][2];
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          top[n][e] = -CUDART_INF_F;
-#pragma unroll
-          for (int i = 0; i < MT; ++i)
-            top[n][e] = fmaxf(top[n][e], fmaxf(s[n][i][e], s[n][i][2 + e]));
-          over |= top[n][e] > m[n][e] + kRoom;
-        }
-      if (__any_sync(0xffffffffu, over)) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float x = top[n][e];
-#pragma unroll
-            for (int q = 4; q < 32; q <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, q));
-            const float nm = x > m[n][e] + kRoom ? x - kHead : m[n][e];
-            const float a = exp2_fast(m[n][e] - nm);
-            m[n][e] = nm;
-            l[n][e] *= a;
-#pragma unroll
-            for (int i = 0; i < MMAS; ++i) {
-              o[n][i][e] *= a;
-              o[n][i][2 + e] *= a;
-            }
-          }
-      }
-      // weights
-      uint32_t pf[NT][MT][2];
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const float w0 = exp2_fast(s[n][i][2 * r] - m[n][0]);
-            const float w1 = exp2_fast(s[n][i][2 * r + 1] - m[n][1]);
-            l[n][0] = fmaf(w0, rv[i][r], l[n][0]);
-            l[n][1] = fmaf(w1, rv[i][r], l[n][1]);
-            pf[n][i][r] = transpose8x8(pack_h2(w0, w1));
-          }
-      // values
-      uint32_t vraw[MT][4][PL::VW];
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          lds_words<PL::VW>(v_at + off + v_row[r & 1] + (16 * i + (r & 2) * 4) * ROW, vraw[i][r]);
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int w = 0; w < PL::VW; ++w) {
-          const uint32_t x0 = vraw[i][0][w], x1 = vraw[i][1][w];
-          const uint32_t x2 = vraw[i][2][w], x3 = vraw[i][3][w];
-          if (BITS == 4) {
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const int sel = half ? 0x7632 : 0x5410;
-              uint32_t a[4], c[4];
-              nib.to_h(__byte_perm(x0, x1, sel), a);
-              nib.to_h(__byte_perm(x2, x3, sel), c);
-#pragma unroll
-              for (int n = 0; n < NT; ++n) {
-                mma16816(o[n][4 * w + 2 * half], a[0], a[1], c[0], c[1], pf[n][i][0], pf[n][i][1]);
-                mma16816(o[n][4 * w + 2 * half + 1], a[2], a[3], c[2], c[3], pf[n][i][0], pf[n][i][1]);
-              }
-            }
-          } else {
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const int sel = half ? 0x7362 : 0x5140;
-              uint32_t a0, a1, a2, a3;
-              bytes_to_h(__byte_perm(x0, x1, sel), a0, a1);
-              bytes_to_h(__byte_perm(x2, x3, sel), a2, a3);
-#pragma unroll
-              for (int n = 0; n < NT; ++n)
-                mma16816(o[n][2 * w + half], a0, a1, a2, a3, pf[n][i][0], pf[n][i][1]);
-            }
-          }
-        }
+      math.step(it, ring + st * PL::STAGE, j, j < it.lo_max || j + PL::STEP > it.hi_min || it.bad);
       // refill the stage: every lane has its registers
       __syncwarp();
-#pragma unroll
-      for (int i = 0; i + 1 < S; ++i) there[i] = there[i + 1];
       if (u + S < u1 && ok) {
-        const int now_page = next;
+        issue(next, j + S * PL::UNIT, st);
         next = u + S + 1 < u1 ? page_at(j + (S + 1) * PL::UNIT) : -1;
-        there[S - 1] = issue(now_page, j + S * PL::UNIT, st);
       }
       st = st + 1 == S ? 0 : st + 1;
     }
 
-    if (!ok && u0 < u1) {
+    if (!ok) {
       // a copy did not land: report it, and let the others land (bounded)
       if (lane == 0) atomicCAS(p.kv.err, 0u, static_cast<unsigned>(kDevErrCacheCopy));
       for (int i = 0; i < S; ++i) wait_stage(bars + 8 * i, (phases >> i) & 1u);
@@ -559,31 +627,13 @@ __global__ void __launch_bounds__(kThreads, Plan<BITS, D, NT>::BLOCKS)
 
     // -- join the warps -----------------------------------------------------------
     __syncthreads();  // every ring is drained
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int c = n * 8 + 2 * t + e;
-        float x = l[n][e];
-#pragma unroll
-        for (int q = 4; q < 32; q <<= 1) x += __shfl_xor_sync(0xffffffffu, x, q);
-        if (g == 0) {
-          m_sm[warp][c] = m[n][e];
-          l_sm[warp][c] = x;
-        }
-        // this lane's d: MMAS pairs (2 i, 2 i + 1) from 2 MMAS g on
-        float *dst = &o_sm[warp][c][2 * MMAS * g];
-#pragma unroll
-        for (int i = 0; i < MMAS; i += 2)
-          *reinterpret_cast<float4 *>(dst + 2 * i) =
-              make_float4(o[n][i][e], o[n][i][2 + e], o[n][i + 1][e], o[n][i + 1][2 + e]);
-      }
+    math.finish(o_sm[warp], m_sm[warp], l_sm[warp]);
     __syncthreads();
     const bool whole = u0 == 0 && u1 == nu;
     // a block's first piece may go on from the block before: slot 0, else 1
     const int slot = u0 == 0 ? 1 : 0;
     float *part = parts + (static_cast<long long>(blockIdx.x) * 2 + slot) * COLS * (D + 2);
-    for (int i = threadIdx.x; i < R * (D / 4); i += kThreads) {
+    for (int i = threadIdx.x; i < it.R * (D / 4); i += kThreads) {
       const int c = i / (D / 4), d = i % (D / 4) * 4;
       float mm = m_sm[0][c];
 #pragma unroll
@@ -601,9 +651,7 @@ __global__ void __launch_bounds__(kThreads, Plan<BITS, D, NT>::BLOCKS)
         sum = fmaf(a, l_sm[w][c], sum);
       }
       if (whole) {
-        const int ri = rb * COLS + c;
-        const long long row = (static_cast<long long>(q0) + ri / p.group) * p.Hq +
-                              h * p.group + ri % p.group;
+        const long long row = it.row(p, c, COLS);
         store_row4<D>(p, row, d, x, mm, sum);
       } else {
         *reinterpret_cast<float4 *>(part + c * D + d) = x;
@@ -614,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, Plan<BITS, D, NT>::BLOCKS)
       }
     }
     if (!whole && u0 == 0 && threadIdx.x == 0)
-      descs[blockIdx.x] = Desc{b, h, rb, static_cast<int>((istart + nu - 1) / per)};
+      descs[blockIdx.x] = Desc{b, it.h, it.rb, static_cast<int>((istart + nu - 1) / per)};
     // the next copies (another proxy) write where the results were
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();
@@ -748,20 +796,24 @@ int launch_t(const KvAttnParams &p, cudaStream_t s) {
 
 }  // namespace
 
-size_t kv_decode_workspace(int D, int rows) {
-  const int cols = rows <= 8 ? 8 : 16;
-  const size_t grid = kNumSMsGB300 * (rows <= 8 ? 4 : 3);
+// Rows that a sequence's queries make per kv head: blocks of 8 or 16.
+static int column_tiles(long long rows) { return rows <= 8 ? 1 : 2; }
+
+size_t kv_decode_workspace(int D, long long rows) {
+  const int nt = column_tiles(rows);
+  const size_t cols = 8 * nt, grid = kNumSMsGB300 * (nt == 1 ? 4 : 3);
   return grid * (sizeof(Desc) + 2 * sizeof(float) * cols * (D + 2));
 }
 
 int launch_kv_decode(const KvAttnParams &p, int bits, int D, cudaStream_t s) {
-  const bool one = p.max_q * p.group <= 8;
+  const int nt = column_tiles(static_cast<long long>(p.max_q) * p.group);
   if (bits == 4) {
-    if (D == 64) return one ? launch_t<4, 64, 1>(p, s) : launch_t<4, 64, 2>(p, s);
-    return one ? launch_t<4, 128, 1>(p, s) : launch_t<4, 128, 2>(p, s);
+    if (D == 64)
+      return nt == 1 ? launch_t<4, 64, 1>(p, s) : launch_t<4, 64, 2>(p, s);
+    return nt == 1 ? launch_t<4, 128, 1>(p, s) : launch_t<4, 128, 2>(p, s);
   }
-  if (D == 64) return one ? launch_t<8, 64, 1>(p, s) : launch_t<8, 64, 2>(p, s);
-  return one ? launch_t<8, 128, 1>(p, s) : launch_t<8, 128, 2>(p, s);
+  if (D == 64) return nt == 1 ? launch_t<8, 64, 1>(p, s) : launch_t<8, 64, 2>(p, s);
+  return nt == 1 ? launch_t<8, 128, 1>(p, s) : launch_t<8, 128, 2>(p, s);
 }
 
 }  // namespace w8a8
