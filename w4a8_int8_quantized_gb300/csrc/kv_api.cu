@@ -3,6 +3,7 @@
 #include <math.h>
 
 #include "common.cuh"
+#include "kv_attn.cuh"
 #include "kv_common.cuh"
 
 namespace w8a8 {
@@ -12,10 +13,6 @@ int launch_kv_write(const KvView &kv, int bits, int D, const __half *k, long lon
                     const long long *slots, int T, cudaStream_t s);
 int launch_kv_read(const KvView &kv, int bits, int D, const long long *slots, int T, __half *k,
                    __half *v, cudaStream_t s);
-size_t kv_attn_workspace(int T, int Hq, int max_q, int B, long long max_len, const KvView &kv,
-                         int bits, int D);
-int launch_kv_attn(const KvAttnParams &p, int bits, int D, cudaStream_t s);
-
 namespace {
 
 bool aligned(const void *p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -123,9 +120,9 @@ size_t kv_cache_attention_workspace_bytes(int T, int q_heads, int B, int max_q, 
       table_width < 0 || q_heads % cache->kv_heads != 0)
     return 0;
   if (T == 0 || B == 0) return 0;
-  return kv_attn_workspace(T, q_heads, max_q < T ? max_q : T, B,
-                           static_cast<long long>(table_width) * cache->page_size,
-                           view_of(cache), cache->bits, cache->head_dim);
+  const long long rows = static_cast<long long>(max_q < T ? max_q : T) * (q_heads / cache->kv_heads);
+  return rows <= kFewRows ? kv_decode_workspace(cache->head_dim, rows)
+                          : kv_prefill_workspace(cache->head_dim);
 }
 
 int kv_cache_attention(const w8a8_half *q, long long q_token_stride, long long q_head_stride,
@@ -177,7 +174,9 @@ int kv_cache_attention(const w8a8_half *q, long long q_token_stride, long long q
   p.out = reinterpret_cast<__half *>(out);
   p.lse = lse;
   p.ws = static_cast<float *>(workspace);
-  return launch_kv_attn(p, cache->bits, cache->head_dim, static_cast<cudaStream_t>(stream));
+  const bool few = static_cast<long long>(max_q) * p.group <= kFewRows;
+  return (few ? launch_kv_decode : launch_kv_prefill)(p, cache->bits, cache->head_dim,
+                                                      static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

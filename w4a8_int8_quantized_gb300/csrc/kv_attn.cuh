@@ -22,10 +22,13 @@ __device__ __forceinline__ void store_row4(const KvAttnParams &p, long long row,
     p.lse[row] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * kLn2;
 }
 
-// Rows per kv head and sequence up to which the few-row kernel runs.
+// Rows per kv head and sequence up to which the few-row kernel runs, else the
+// tensor-memory one.
 constexpr int kFewRows = 64;
 
 size_t kv_decode_workspace(int D, long long rows);
 int launch_kv_decode(const KvAttnParams &p, int bits, int D, cudaStream_t s);
+size_t kv_prefill_workspace(int D);
+int launch_kv_prefill(const KvAttnParams &p, int bits, int D, cudaStream_t s);
 
 }  // namespace w8a8

@@ -1,0 +1,833 @@
+// Attention of many query rows (prompts, chunks) over the quantized cache, on
+// the 5th-generation tensor cores.
+//
+// Rows of one kv head share its keys: row r of a sequence is query r / group,
+// head r % group of the group, and an item is (sequence, 256 rows, kv head).
+// Per 128 keys an item needs S = Q K^T and O += P V, 4 * 256 * 128 * D flops
+// (2048 cycles of the tensor pipe at D = 128) against 17 KB of cache, so it is
+// bound by the tensor pipe, with the softmax (32768 exponentials) close behind.
+//
+// One CTA of 16 warps per SM:
+//   warps 0-3, 4-7   softmax of rows 0-127 and 128-255: a thread owns a row
+//                    (TMEM lane), reads its 128 scores, writes its weights P back
+//                    over them as fp16;
+//   warps 8-11       converters: a thread owns a token; codes to fp16 (exact)
+//                    into 128-byte-swizzled stages, and the token's scales;
+//   warp 12          issues the MMAs (one thread): S_0, S_1 of the next keys are
+//                    issued between the P V of the two row halves, so that one
+//                    half's softmax runs under the other half's products;
+//   warps 13, 14     bring the next item's Q rows while the current one finishes;
+//   warp 15          walks this block's range of work and publishes its pieces.
+// TMEM: S_0, S_1 (128 columns each, P in their first 64), O_0, O_1 (D columns).
+//
+// Operands: Q and K are K-major.  V keeps its token rows and is read as the
+// MN-major operand, so nothing is transposed.  At 4 bits the converter's pairs
+// (d, d + 4) permute the d of each 8; Q is stored with the same permutation and
+// the output undoes it for V.
+//
+// Softmax, with the codes exact and both scales in fp32: u = S (scale log2e s_k)
+// + log2 s_v, p = 2^(u - M), O = sum p code_v, l = sum p / s_v.  M is the lazy
+// reference of kv_common.cuh, a row's own: O is rescaled (TMEM to TMEM) only when
+// some row of the warp passes it.  Tokens past the length get s_k = 0,
+// log2 s_v = -inf, 1 / s_v = 0, so only tiles at a row's causal end or window
+// start test single keys.
+//
+// Split: as in the few-row kernel, the 128-key tiles of all items form one line
+// cut into equal ranges, one per SM, whatever the lengths, the causal triangle
+// and the number of items; an item cut by ranges leaves fp32 partials that a
+// second kernel joins in order.
+#include <math_constants.h>
+
+#include <mutex>
+
+#include "common.cuh"
+#include "kv_attn.cuh"
+#include "kv_common.cuh"
+#include "tc_ptx.cuh"
+
+namespace w8a8 {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kRows = 256;  // of an item
+constexpr int kKeys = 128;  // of a tile
+constexpr int kRing = 4;    // published pieces
+
+// A piece of an item: its tiles t0 .. t1 - 1 of nt.
+struct Piece {
+  int b, h, qt, R;     // R: rows of the item; 0: no more pieces
+  int q0, nq, len;     // of the sequence
+  int first, hi_max;   // token of tile 0; keys from hi_max on are seen by no row
+  int t0, t1, nt;
+  int last;            // range that holds the item's last tile
+};
+
+struct Desc {
+  int b, h, qt, last;
+};
+
+template <int D>
+struct Plan {
+  static constexpr int SUBS = D / 64;                  // 64-wide sub-tiles of 128-byte rows
+  static constexpr int SUB = 128 * 128;                // bytes of one
+  static constexpr int TILE = SUBS * SUB;              // a Q, K or V tile
+  static constexpr int OFF_Q = 0, OFF_K = 2 * TILE, OFF_V = 4 * TILE, OFF_S = 6 * TILE;
+  static constexpr int SLOTS = 3;                      // of token scales (see the converters)
+  static constexpr int OFF_BAR = OFF_S + SLOTS * 3 * kKeys * 4;
+  static constexpr int BARS = 18 + SLOTS + 2 * kRing + 1;
+  static constexpr int OFF_PIECE = OFF_BAR + BARS * 8;
+  static constexpr int OFF_MISC = OFF_PIECE + kRing * static_cast<int>(sizeof(Piece));
+  static constexpr int SMEM = OFF_MISC + 16 + 1024;    // 1024: aligned by hand
+  static constexpr uint32_t COL_S = 0, COL_O = 256;    // S_w at 128 w, O_w at 256 + 128 w
+};
+static_assert(Plan<128>::SMEM <= 232448, "shared memory plan too large");
+
+// D fp32, A and B fp16, M = 128; S: N = 128, both K-major; PV: N = D, B MN-major
+constexpr uint32_t kIdescS = (1u << 4) | (128u >> 3 << 17) | (128u >> 4 << 24);
+template <int D>
+__host__ __device__ constexpr uint32_t idesc_pv() {
+  return (1u << 4) | (1u << 16) | (static_cast<uint32_t>(D) >> 3 << 17) | (128u >> 4 << 24);
+}
+
+// V as MN-major operand, 128-byte swizzle: 64 d of 8 tokens per 1 KB atom, the
+// next 8 tokens 1 KB on (stride offset), the next 64 d a sub-tile on (leading offset)
+__device__ __forceinline__ uint64_t v_desc(uint32_t addr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((addr & 0x3ffff) >> 4);
+  d |= static_cast<uint64_t>((128 * 128) >> 4) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+
+// D += A B with A in tensor memory
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t accum) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(bdesc), "r"(idesc), "r"(accum));
+}
+
+#define W8A8_R8(v, i) "r"(v[i]), "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3]), "r"(v[i + 4]), "r"(v[i + 5]), "r"(v[i + 6]), "r"(v[i + 7])
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      W8A8_R8(v, 0), W8A8_R8(v, 8)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,"
+      "%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      W8A8_R8(v, 0), W8A8_R8(v, 8), W8A8_R8(v, 16), W8A8_R8(v, 24)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// paired fp32 arithmetic: each half an IEEE operation
+__device__ __forceinline__ void fma2(float &a, float &b, float x0, float x1, float y0, float y1,
+                                     float z0, float z1) {
+  asm("{\n.reg .b64 x, y, z, d;\n"
+      "mov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nmov.b64 z, {%6, %7};\n"
+      "fma.rn.f32x2 d, x, y, z;\nmov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(a), "=f"(b)
+      : "f"(x0), "f"(x1), "f"(y0), "f"(y1), "f"(z0), "f"(z1));
+}
+__device__ __forceinline__ void add2(float &a, float &b, float x0, float x1, float y) {
+  asm("{\n.reg .b64 x, y, d;\n"
+      "mov.b64 x, {%2, %3};\nmov.b64 y, {%4, %4};\n"
+      "add.rn.f32x2 d, x, y;\nmov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(a), "=f"(b)
+      : "f"(x0), "f"(x1), "f"(y));
+}
+
+__device__ __forceinline__ float4 lds4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void sts4(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ void sts1(uint32_t a, float v) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
+}
+
+// Rows and tiles of entity e = sequence * nqt + row block; 0 tiles: no rows.
+struct Entity {
+  int b, qt, R, q0, nq, len, first, hi_max, nt;
+};
+__device__ __forceinline__ Entity entity_of(const KvAttnParams &p, int nqt, int e) {
+  Entity x;
+  x.b = e / nqt;
+  x.qt = e - x.b * nqt;
+  seq_of(p, x.b, x.q0, x.nq, x.len);
+  const long long left = static_cast<long long>(x.nq) * p.group - static_cast<long long>(x.qt) * kRows;
+  x.R = static_cast<int>(min(left, static_cast<long long>(kRows)));
+  x.nt = 0;
+  x.first = x.hi_max = 0;
+  if (x.R > 0) {
+    int lo, hi, lo2;
+    visible(p, x.len - x.nq + (x.qt * kRows) / p.group, x.len, lo, hi);
+    visible(p, x.len - x.nq + (x.qt * kRows + x.R - 1) / p.group, x.len, lo2, x.hi_max);
+    x.hi_max = max(x.hi_max, 0);
+    x.first = min(lo, x.hi_max) & ~15;
+    x.nt = max((x.hi_max - x.first + kKeys - 1) / kKeys, 1);
+  }
+  return x;
+}
+
+// Token row i of a tile: byte offset of its 16-byte chunk c (8 d) in a swizzled tile
+__device__ __forceinline__ uint32_t chunk_at(int i, int c) {
+  return (c >> 3) * (128 * 128) + (i >> 3) * 1024 + (i & 7) * 128 + (((c & 7) ^ (i & 7)) << 4);
+}
+
+template <int BITS, int D>
+__global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnParams p) {
+  using PL = Plan<D>;
+  extern __shared__ uint8_t raw[];
+  __shared__ long long sums[kThreads];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  // -- this block's range of tiles --------------------------------------------
+  const int nqt = static_cast<int>((static_cast<long long>(p.max_q) * p.group + kRows - 1) / kRows);
+  const int entities = p.B * nqt, per_thread = (entities + kThreads - 1) / kThreads;
+  {
+    long long x = 0;
+    for (int i = 0; i < per_thread; ++i) {
+      const int e = threadIdx.x * per_thread + i;
+      if (e < entities) x += static_cast<long long>(entity_of(p, nqt, e).nt) * p.kv.heads;
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    sums[threadIdx.x] = x;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) x += sums[w * 32 + 31];
+    __syncthreads();
+    sums[threadIdx.x] = x;
+    __syncthreads();
+  }
+  const long long total = sums[kThreads - 1];
+  const long long per = (total + gridDim.x - 1) / gridDim.x;
+  const long long c0 = blockIdx.x * per, c1 = min(c0 + per, total);
+  Desc *descs = reinterpret_cast<Desc *>(p.ws);
+  float *parts = reinterpret_cast<float *>(descs + gridDim.x);
+  if (threadIdx.x == 0) descs[blockIdx.x].last = -1;
+  if (c0 >= c1) return;
+
+  const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+  uint8_t *sm = raw + (base - smem_u32(raw));
+  const uint32_t bar0 = base + PL::OFF_BAR;
+  auto q_full = [&](int w) { return bar0 + 8u * w; };
+  auto q_empty = [&](int w) { return bar0 + 8u * (2 + w); };
+  auto k_full = [&](int s) { return bar0 + 8u * (4 + s); };
+  auto k_empty = [&](int s) { return bar0 + 8u * (6 + s); };
+  auto v_full = [&](int s) { return bar0 + 8u * (8 + s); };
+  auto v_empty = [&](int s) { return bar0 + 8u * (10 + s); };
+  auto s_full = [&](int w) { return bar0 + 8u * (12 + w); };
+  auto p_full = [&](int w) { return bar0 + 8u * (14 + w); };
+  auto o_full = [&](int w) { return bar0 + 8u * (16 + w); };
+  auto sc_full = [&](int i) { return bar0 + 8u * (18 + i); };
+  auto piece_full = [&](int i) { return bar0 + 8u * (18 + PL::SLOTS + i); };
+  auto piece_empty = [&](int i) { return bar0 + 8u * (18 + PL::SLOTS + kRing + i); };
+  const uint32_t drain = bar0 + 8u * (PL::BARS - 1);
+  Piece *pieces = reinterpret_cast<Piece *>(sm + PL::OFF_PIECE);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + PL::OFF_MISC);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(q_full(i), 1);
+      mbar_init(q_empty(i), 1);
+      mbar_init(k_full(i), 4);
+      mbar_init(k_empty(i), 1);
+      mbar_init(v_full(i), 4);
+      mbar_init(v_empty(i), 1);
+      mbar_init(s_full(i), 1);
+      mbar_init(p_full(i), 4);
+      mbar_init(o_full(i), 1);
+    }
+    for (int i = 0; i < PL::SLOTS; ++i) mbar_init(sc_full(i), 4);
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(piece_full(i), 1);
+      mbar_init(piece_empty(i), 8 + 4 + 1 + 2);  // softmax, converter, MMA and Q warps
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 12) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot)));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  unsigned int *err = p.kv.err;
+  auto wait = [&](uint32_t bar, uint32_t parity) {
+    // the whole warp, in step
+    return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, kDevErrCacheCopy, err, kTimeoutCycles)) != 0;
+  };
+  // a warp's view of the published pieces
+  struct Reader {
+    int i = 0;
+    uint32_t phase = 0;
+  };
+  auto next_piece = [&](Reader &r, Piece &x) {
+    if (!wait(piece_full(r.i), r.phase)) return false;
+    x = pieces[r.i];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(piece_empty(r.i));
+    if (++r.i == kRing) {
+      r.i = 0;
+      r.phase ^= 1u;
+    }
+    return x.R > 0;
+  };
+  Reader reader;
+  Piece x;
+
+  // Registers: 2 * 192 + 72 + 56 = 4 * 128, the launch's share
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    // ------------------------------------------------------------ softmax ----
+    const int w = warp >> 2, r = w * 128 + (warp & 3) * 32 + lane;  // this thread's row of an item
+    const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t col_s = lanes + PL::COL_S + 128 * w, col_o = lanes + PL::COL_O + 128 * w;
+    uint32_t s_phase = 0, o_phase = 0;
+    uint32_t tiles = 0;  // so far
+    bool ok = true;
+    while (ok && next_piece(reader, x)) {
+      if (x.R <= w * 128) {  // this half has no rows; keep up with the scales' slots
+        tiles += x.t1 - x.t0;
+        continue;
+      }
+      const int ri = x.qt * kRows + r;
+      int lo = 0, hi = 0x7fffffff;
+      if (r < x.R) visible(p, x.len - x.nq + ri / p.group, x.len, lo, hi);
+      float m = kNoRef, l0 = 0.f, l1 = 0.f;
+      for (int i = x.t0; i < x.t1; ++i) {
+        const uint32_t slot = tiles % PL::SLOTS;
+        ok = wait(s_full(w), s_phase) && wait(sc_full(slot), (tiles / PL::SLOTS) & 1u);
+        if (!ok) break;
+        ++tiles;
+        s_phase ^= 1u;
+        tc_fence_after();
+        const uint32_t sc = base + PL::OFF_S + slot * (3 * kKeys * 4);
+        const int j = x.first + i * kKeys;
+        float u[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[32];
+          tmem_ld32(col_s + 32 * c, v);
+          tmem_wait_ld32(v);
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float4 k = lds4(sc + (32 * c + e) * 4), y = lds4(sc + (kKeys + 32 * c + e) * 4);
+            float *d = u + 32 * c + e;
+            fma2(d[0], d[1], __uint_as_float(v[e]), __uint_as_float(v[e + 1]), k.x, k.y, y.x, y.y);
+            fma2(d[2], d[3], __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]), k.z, k.w, y.z, y.w);
+          }
+        }
+        if (__any_sync(0xffffffffu, lo > j || hi < j + kKeys)) {
+          const int a = lo - j, z = hi - j;
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (c < a || c >= z) u[c] = -CUDART_INF_F;
+        }
+        float top = fmaxf(u[0], u[1]);
+#pragma unroll
+        for (int c = 2; c < 128; c += 2) top = fmaxf(fmaxf(top, u[c]), u[c + 1]);
+        if (__any_sync(0xffffffffu, top > m + kRoom)) {
+          const float nm = top > m + kRoom ? top - kHead : m;
+          const float a = exp2_fast(m - nm);
+          m = nm;
+          l0 *= a;
+          l1 *= a;
+          if (i > x.t0) {
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t v[32];
+              tmem_ld32(col_o + 32 * c, v);
+              tmem_wait_ld32(v);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * a);
+              tmem_st32(col_o + 32 * c, v);
+            }
+          }
+        }
+        // weights, 32 at a time over the scores that are already in registers
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            float *d = u + 32 * c + e;
+            add2(d[0], d[1], d[0], d[1], -m);
+            add2(d[2], d[3], d[2], d[3], -m);
+            const float w0 = exp2_fast(d[0]), w1 = exp2_fast(d[1]);
+            const float w2 = exp2_fast(d[2]), w3 = exp2_fast(d[3]);
+            const float4 rv = lds4(sc + (2 * kKeys + 32 * c + e) * 4);
+            fma2(l0, l1, w0, w1, rv.x, rv.y, l0, l1);
+            fma2(l0, l1, w2, w3, rv.z, rv.w, l0, l1);
+            const __half2 h0 = __floats2half2_rn(w0, w1), h1 = __floats2half2_rn(w2, w3);
+            v[e / 2] = *reinterpret_cast<const uint32_t *>(&h0);
+            v[e / 2 + 1] = *reinterpret_cast<const uint32_t *>(&h1);
+          }
+          tmem_st16(col_s + 16 * c, v);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full(w));
+      }
+      if (!ok) break;
+      // -- the item's (or piece's) end
+      ok = wait(o_full(w), o_phase);
+      if (!ok) break;
+      o_phase ^= 1u;
+      tc_fence_after();
+      const float l = l0 + l1;
+      const bool whole = x.t0 == 0 && x.t1 == x.nt;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const long long row = (static_cast<long long>(x.q0) + ri / p.group) * p.Hq + x.h * p.group + ri % p.group;
+      const long long part = static_cast<long long>(blockIdx.x) * 2 + (x.t0 == 0 ? 1 : 0);
+      float *dst = parts + part * kRows * (D + 2) + r * D;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t v[32];
+        tmem_ld32(col_o + 32 * c, v);
+        tmem_wait_ld32(v);
+        if (r < x.R) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            // columns e .. e + 7 are d 0, 4, 1, 5, 2, 6, 3, 7 of an 8 at 4 bits
+            float y[8];
+#pragma unroll
+            for (int z = 0; z < 8; ++z) {
+              const int from = BITS == 4 ? (z & 3) * 2 + (z >> 2) : z;
+              y[z] = __uint_as_float(v[e + from]);
+            }
+            if (whole) {
+              uint4 o;
+              const __half2 h0 = __floats2half2_rn(y[0] * inv, y[1] * inv), h1 = __floats2half2_rn(y[2] * inv, y[3] * inv);
+              const __half2 h2 = __floats2half2_rn(y[4] * inv, y[5] * inv), h3 = __floats2half2_rn(y[6] * inv, y[7] * inv);
+              o.x = *reinterpret_cast<const uint32_t *>(&h0);
+              o.y = *reinterpret_cast<const uint32_t *>(&h1);
+              o.z = *reinterpret_cast<const uint32_t *>(&h2);
+              o.w = *reinterpret_cast<const uint32_t *>(&h3);
+              *reinterpret_cast<uint4 *>(p.out + row * D + 32 * c + e) = o;
+            } else {
+              *reinterpret_cast<float4 *>(dst + 32 * c + e) = make_float4(y[0], y[1], y[2], y[3]);
+              *reinterpret_cast<float4 *>(dst + 32 * c + e + 4) = make_float4(y[4], y[5], y[6], y[7]);
+            }
+          }
+        }
+      }
+      if (r < x.R) {
+        if (!whole) {
+          float *ml = parts + part * kRows * (D + 2) + kRows * D + 2 * r;
+          ml[0] = m;
+          ml[1] = l;
+        } else if (p.lse != nullptr) {
+          p.lse[row] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * kLn2;
+        }
+      }
+      if (!whole && x.t0 == 0 && threadIdx.x == 0) descs[blockIdx.x] = Desc{x.b, x.h, x.qt, x.last};
+      tc_fence_before();
+    }
+  } else if (warp < 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    // --------------------------------------------------------- converters ----
+    // The scales have a third slot: a tile's are read until both halves' weights
+    // are written, and slot s is refilled for tile i + 3 only once the K stage
+    // of tile i + 1 is free, whose scores are issued after those weights.
+    constexpr int ROW = D * BITS / 8, NV = ROW / 16;  // 16-byte vectors of a token
+    const int tok = (warp - 8) * 32 + lane;
+    const Nibbles nib;
+    int st = 0, slot = 0;
+    uint32_t phase = 1;  // the first wait on an empty stage passes
+    const int pmask = (1 << p.kv.page_shift) - 1;
+    bool ok = true;
+    auto convert = [&](const uint4 (&v)[NV], uint32_t stage) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const uint32_t y[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        if (BITS == 4) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t o[4];
+            nib.to_h(y[e], o);
+            sts4(stage + chunk_at(tok, 4 * i + e), make_uint4(o[0], o[1], o[2], o[3]));
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; e += 2) {
+            uint4 o;
+            bytes_to_h(y[e], o.x, o.y);
+            bytes_to_h(y[e + 1], o.z, o.w);
+            sts4(stage + chunk_at(tok, 2 * i + e / 2), o);
+          }
+        }
+      }
+    };
+    while (ok && next_piece(reader, x)) {
+      const int end = min(x.hi_max, x.len);
+      for (int i = x.t0; i < x.t1; ++i) {
+        const int a = x.first + i * kKeys + tok;
+        const int page = a < end ? page_of(p, x.b, a >> p.kv.page_shift) : -1;
+        const long long row = p.kv.row(page < 0 ? 0 : page, x.h) + (a & pmask);
+        uint4 kv[NV], vv[NV];
+        float ks = 0.f, vs = 0.f;
+#pragma unroll
+        for (int e = 0; e < NV; ++e) kv[e] = vv[e] = make_uint4(0, 0, 0, 0);
+        if (page >= 0) {
+          const uint4 *kp = reinterpret_cast<const uint4 *>(p.kv.kc + row * ROW);
+#pragma unroll
+          for (int e = 0; e < NV; ++e) kv[e] = __ldg(kp + e);
+          ks = __ldg(p.kv.ks + row);
+          vs = __ldg(p.kv.vs + row);
+          const uint4 *vp = reinterpret_cast<const uint4 *>(p.kv.vc + row * ROW);
+#pragma unroll
+          for (int e = 0; e < NV; ++e) vv[e] = __ldg(vp + e);
+        }
+        ok = wait(k_empty(st), phase);
+        if (!ok) break;
+        convert(kv, base + PL::OFF_K + st * PL::TILE);
+        const uint32_t sc = base + PL::OFF_S + slot * (3 * kKeys * 4) + tok * 4;
+        const float sv = vs == 0.f ? 1.f : vs;  // s_v = 0: all codes 0, any scale will do
+        sts1(sc, page < 0 ? 0.f : ks * (p.scale * kLog2e));
+        sts1(sc + kKeys * 4, page < 0 ? -CUDART_INF_F : log2_fast(sv));
+        sts1(sc + 2 * kKeys * 4, page < 0 ? 0.f : 1.f / sv);
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(k_full(st));
+          mbar_arrive(sc_full(slot));
+        }
+        ok = wait(v_empty(st), phase);
+        if (!ok) break;
+        convert(vv, base + PL::OFF_V + st * PL::TILE);
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(v_full(st));
+        slot = slot + 1 == PL::SLOTS ? 0 : slot + 1;
+        st ^= 1;
+        if (st == 0) phase ^= 1u;
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 12) {
+      // ------------------------------------------------------------- MMAs ----
+      // (whole warp in step, one thread issues)
+      const bool issue = lane == 0;
+      int ks = 0, vs = 0;  // stages, and their phases
+      uint32_t kph = 0, vph = 0, qph[2] = {0, 0}, pph[2] = {0, 0};
+      auto scores = [&](int w) {
+        if (issue) {
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t at = (k >> 2) * PL::SUB + (k & 3) * 32;
+            tc_mma(tmem + PL::COL_S + 128 * w, sw128_desc(base + PL::OFF_Q + w * PL::TILE + at),
+                   sw128_desc(base + PL::OFF_K + ks * PL::TILE + at), kIdescS, k > 0);
+          }
+          tc_commit(s_full(w));
+        }
+        __syncwarp();
+      };
+      auto values = [&](int w, bool fresh) {
+        if (issue) {
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < kKeys / 16; ++k)
+            tc_mma_ts(tmem + PL::COL_O + 128 * w, tmem + PL::COL_S + 128 * w + 8 * k,
+                      v_desc(base + PL::OFF_V + vs * PL::TILE + k * 2048), idesc_pv<D>(), !(fresh && k == 0));
+        }
+        __syncwarp();
+      };
+      // the K stage whose scores are next: waited for once, released after the last half
+      auto open_k = [&]() { return wait(k_full(ks), kph); };
+      auto close_k = [&]() {
+        if (issue) tc_commit(k_empty(ks));
+        ks ^= 1;
+        if (ks == 0) kph ^= 1u;
+      };
+      bool ok = true, have = next_piece(reader, x);
+      if (have) {
+        ok = wait(q_full(0), qph[0]) && open_k();
+        qph[0] ^= 1u;
+        if (ok) scores(0);
+        if (ok && x.R > 128) {
+          ok = wait(q_full(1), qph[1]);
+          qph[1] ^= 1u;
+          if (ok) scores(1);
+        }
+        if (ok) {
+          if (issue && x.t1 - x.t0 == 1) {
+            tc_commit(q_empty(0));
+            if (x.R > 128) tc_commit(q_empty(1));
+          }
+          close_k();
+        }
+      }
+      while (ok && have) {
+        Piece y;
+        bool more = false;
+        for (int i = x.t0; i < x.t1 && ok; ++i) {
+          const bool last = i + 1 == x.t1;
+          if (last) {
+            more = next_piece(reader, y);
+            ok = *abort_flag == 0;
+            if (!ok) break;
+          }
+          const int R2 = last ? (more ? y.R : 0) : x.R;  // rows of the next tile's item
+          ok = wait(v_full(vs), vph);
+          if (!ok) break;
+          bool opened = false;
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            if (x.R > 128 * w) {
+              ok = ok && wait(p_full(w), pph[w]);
+              pph[w] ^= 1u;
+              if (!ok) break;
+              values(w, i == x.t0);
+              if (issue && last) tc_commit(o_full(w));
+            }
+            if (R2 > 128 * w) {
+              if (last) {
+                ok = wait(q_full(w), qph[w]);
+                qph[w] ^= 1u;
+              }
+              if (ok && !opened) ok = open_k();
+              opened = true;
+              if (!ok) break;
+              scores(w);
+              // the item's last scores: its Q rows may be replaced
+              const bool q_done = last ? y.t1 - y.t0 == 1 : i + 2 == x.t1;
+              if (issue && q_done) tc_commit(q_empty(w));
+            }
+          }
+          if (!ok) break;
+          if (issue) tc_commit(v_empty(vs));
+          vs ^= 1;
+          if (vs == 0) vph ^= 1u;
+          if (opened) close_k();
+        }
+        x = y;
+        have = more;
+      }
+      // every MMA has landed before TMEM is freed
+      if (issue) {
+        tc_commit(drain);
+        wait_bar_teardown(drain, 0);
+      }
+      __syncwarp();
+    } else if (warp < 15) {
+      // ---------------------------------------------------------- Q rows ----
+      const int w = warp - 13;
+      uint32_t phase = 1;
+      while (next_piece(reader, x)) {
+        if (x.R <= w * 128) continue;
+        if (!wait(q_empty(w), phase)) break;
+        phase ^= 1u;
+        // rows beyond the item's are zero; a lane takes chunk lane % (D / 8) of every row
+        constexpr int C = D / 8, RPS = 32 / C;  // rows per step of the warp
+        const int c = lane % C;
+        const uint32_t dst = base + PL::OFF_Q + w * PL::TILE;
+        for (int r0 = 0; r0 < 128; r0 += 8 * RPS) {
+          uint4 v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int rr = r0 + e * RPS + lane / C, ri = x.qt * kRows + w * 128 + rr;
+            v[e] = make_uint4(0, 0, 0, 0);
+            if (w * 128 + rr < x.R)
+              v[e] = __ldg(reinterpret_cast<const uint4 *>(
+                  p.q + (x.q0 + ri / p.group) * p.q_ts +
+                  static_cast<long long>(x.h * p.group + ri % p.group) * p.q_hs + 8 * c));
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int rr = r0 + e * RPS + lane / C;
+            uint4 o = v[e];
+            if (BITS == 4)  // d in the order 0, 4, 1, 5, 2, 6, 3, 7
+              o = make_uint4(__byte_perm(v[e].x, v[e].z, 0x5410), __byte_perm(v[e].x, v[e].z, 0x7632),
+                             __byte_perm(v[e].y, v[e].w, 0x5410), __byte_perm(v[e].y, v[e].w, 0x7632));
+            sts4(dst + chunk_at(rr, c), o);
+          }
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full(w));
+      }
+    } else {
+      // ---------------------------------------------------------- the walk ----
+      int lo = 0, hi = kThreads - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (sums[mid] > c0) hi = mid; else lo = mid + 1;
+      }
+      int e = lo * per_thread;
+      long long start = lo > 0 ? sums[lo - 1] : 0;  // first tile of entity e
+      Entity en = entity_of(p, nqt, e);
+      Reader slot;
+      uint32_t phase = 1;
+      bool ok = true;
+      for (long long at = c0; ok;) {
+        if (at < c1)
+          while (at >= start + static_cast<long long>(en.nt) * p.kv.heads) {
+            start += static_cast<long long>(en.nt) * p.kv.heads;
+            en = entity_of(p, nqt, ++e);
+          }
+        ok = wait(piece_empty(slot.i), phase);
+        if (!ok) break;
+        const bool end = at >= c1;
+        if (end) {
+          if (lane == 0) pieces[slot.i].R = 0;
+        } else {
+          const int h = static_cast<int>((at - start) / en.nt);
+          const long long istart = start + static_cast<long long>(h) * en.nt;
+          const int t0 = static_cast<int>(at - istart);
+          const int t1 = static_cast<int>(min(static_cast<long long>(en.nt), c1 - istart));
+          if (lane == 0)
+            pieces[slot.i] = Piece{en.b, h, en.qt, en.R, en.q0, en.nq, en.len, en.first, en.hi_max,
+                                   t0, t1, en.nt, static_cast<int>((istart + en.nt - 1) / per)};
+          at = istart + t1;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(piece_full(slot.i));
+        if (++slot.i == kRing) {
+          slot.i = 0;
+          phase ^= 1u;
+        }
+        if (end) break;
+      }
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 12)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+// Joins the partials of the items cut by the ranges: block (c, y) takes rows 32 y
+// .. + 31 of the item that starts in range c and ends in a later one, a warp a row.
+template <int D>
+__global__ void __launch_bounds__(256) kv_prefill_join_kernel(const KvAttnParams p, int ranges) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Desc *descs = reinterpret_cast<const Desc *>(p.ws);
+  const float *parts = reinterpret_cast<const float *>(descs + ranges);
+  const int c0 = blockIdx.x;
+  const Desc de = descs[c0];
+  if (de.last < 0) return;
+  int q0, nq, len;
+  seq_of(p, de.b, q0, nq, len);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr long long SIZE = static_cast<long long>(kRows) * (D + 2);
+  for (int r = blockIdx.y * 32 + warp; r < blockIdx.y * 32 + 32; r += 8) {
+    const int ri = de.qt * kRows + r;
+    if (ri >= nq * p.group) return;
+    float m = kNoRef;
+    for (int i = c0; i <= de.last; ++i)
+      m = fmaxf(m, parts[(i * 2 + (i == c0 ? 1 : 0)) * SIZE + kRows * D + 2 * r]);
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = c0; i <= de.last; ++i) {
+      const float *part = parts + (i * 2 + (i == c0 ? 1 : 0)) * SIZE;
+      const float a = exp2_fast(part[kRows * D + 2 * r] - m);
+      l = fmaf(a, part[kRows * D + 2 * r + 1], l);
+      if (lane * 4 < D) {
+        const float4 x = *reinterpret_cast<const float4 *>(part + r * D + lane * 4);
+        o.x = fmaf(a, x.x, o.x);
+        o.y = fmaf(a, x.y, o.y);
+        o.z = fmaf(a, x.z, o.z);
+        o.w = fmaf(a, x.w, o.w);
+      }
+    }
+    const long long row = (static_cast<long long>(q0) + ri / p.group) * p.Hq + de.h * p.group + ri % p.group;
+    if (lane * 4 < D) store_row4<D>(p, row, lane * 4, o, m, l);
+  }
+}
+
+template <int BITS, int D>
+bool allow_smem() {
+  static bool done[64] = {};
+  static std::mutex mu;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+  std::lock_guard<std::mutex> lock(mu);
+  if (!done[dev])
+    done[dev] = cudaFuncSetAttribute(kv_prefill_kernel<BITS, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     Plan<D>::SMEM) == cudaSuccess;
+  return done[dev];
+}
+
+template <int BITS, int D>
+int launch_t(const KvAttnParams &p, cudaStream_t s) {
+  if (!allow_smem<BITS, D>()) return W8A8_ERR_CUDA;
+  const long long nqt = (static_cast<long long>(p.max_q) * p.group + kRows - 1) / kRows;
+  if (nqt * p.B > 0x3fffffffLL) return W8A8_ERR_INVALID_ARG;
+  const long long tokens = static_cast<long long>(p.table_w) << p.kv.page_shift;
+  // + 15: the first tile starts on a multiple of 16 before the first key
+  const long long tiles = tokens > 0 ? (tokens + 15 + kKeys - 1) / kKeys : 1;
+  const long long most = nqt * p.B * p.kv.heads * tiles;
+  const int grid = static_cast<int>(most < kNumSMsGB300 ? most : kNumSMsGB300);
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Plan<D>::SMEM;
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kv_prefill_kernel<BITS, D>, p) != cudaSuccess) {
+    cudaGetLastError();
+    return W8A8_ERR_CUDA;
+  }
+  if (tiles > 1) {  // else no item can be cut
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), kRows / 32);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    if (cudaLaunchKernelEx(&cfg, kv_prefill_join_kernel<D>, p, grid) != cudaSuccess) {
+      cudaGetLastError();
+      return W8A8_ERR_CUDA;
+    }
+  }
+  return launch_status();
+}
+
+}  // namespace
+
+size_t kv_prefill_workspace(int D) {
+  return kNumSMsGB300 * (sizeof(Desc) + 2 * sizeof(float) * kRows * (D + 2));
+}
+
+int launch_kv_prefill(const KvAttnParams &p, int bits, int D, cudaStream_t s) {
+  if (bits == 4) return D == 64 ? launch_t<4, 64>(p, s) : launch_t<4, 128>(p, s);
+  return D == 64 ? launch_t<8, 64>(p, s) : launch_t<8, 128>(p, s);
+}
+
+}  // namespace w8a8
