@@ -52,6 +52,7 @@ constexpr int kThreads = 512;
 constexpr int kRows = 256;  // of an item
 constexpr int kKeys = 128;  // of a tile
 constexpr int kRing = 4;    // published pieces
+constexpr int kItemCost = 2;  // of an item beyond its tiles, in tiles: its start and end
 
 // A piece of an item: its tiles t0 .. t1 - 1 of nt.
 struct Piece {
@@ -101,30 +102,68 @@ __device__ __forceinline__ uint64_t v_desc(uint32_t addr) {
   return d;
 }
 
-// D += A B with A in tensor memory
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc,
-                                          uint32_t accum) {
+// MMAs and commits of one elected lane, as predicated instructions of a warp
+// that runs in step: the descriptors then stay in uniform registers.  (From
+// inside a one-lane branch a K = 16, N = 128 MMA took 96 to 108 cycles to
+// issue, this way 65 to 71; it executes in 64.)
+__device__ __forceinline__ uint32_t elect() {
+  uint32_t on;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(on));
+  return on;
+}
+__device__ __forceinline__ void mma_ss(uint32_t on, uint32_t d, uint64_t adesc, uint64_t bdesc,
+                                       uint32_t idesc, uint32_t accum) {
   asm volatile(
-      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(bdesc), "r"(idesc), "r"(accum));
+      "{\n.reg .pred p, q;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 q, %5, 0;\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accum), "r"(on));
+}
+// A in tensor memory
+__device__ __forceinline__ void mma_ts(uint32_t on, uint32_t d, uint32_t a, uint64_t bdesc,
+                                       uint32_t idesc, uint32_t accum) {
+  asm volatile(
+      "{\n.reg .pred p, q;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 q, %5, 0;\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(bdesc), "r"(idesc), "r"(accum), "r"(on));
+}
+__device__ __forceinline__ void commit_if(uint32_t on, uint32_t bar) {
+  asm volatile(
+      "{\n.reg .pred q;\nsetp.ne.b32 q, %1, 0;\n"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar),
+      "r"(on)
+      : "memory");
 }
 
-#define W8A8_R8(v, i) "r"(v[i]), "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3]), "r"(v[i + 4]), "r"(v[i + 5]), "r"(v[i + 6]), "r"(v[i + 7])
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *v) {
+// 16 TMEM lanes x 64 columns as fragments: register 4 n + e of lane 4 g + t is TMEM
+// lane g + 8 (e / 2), column 8 n + 2 t + (e & 1).
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t *v) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      W8A8_R8(v, 0), W8A8_R8(v, 8)
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t *v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x8.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
       : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *v) {
+// 16 lanes x 32 columns: register 2 n + e is TMEM lane g + 8 e, column 4 n + t.
+__device__ __forceinline__ void tmem_st_half_frag(uint32_t taddr, const uint32_t *v) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,"
-      "%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-      W8A8_R8(v, 0), W8A8_R8(v, 8), W8A8_R8(v, 16), W8A8_R8(v, 24)
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
+}
+// waits for this thread's TMEM loads; the registers pass through
+template <int N>
+__device__ __forceinline__ void tmem_wait_ld(uint32_t *v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(v[i]));
 }
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -147,13 +186,6 @@ __device__ __forceinline__ void add2(float &a, float &b, float x0, float x1, flo
       : "f"(x0), "f"(x1), "f"(y));
 }
 
-__device__ __forceinline__ float4 lds4(uint32_t a) {
-  float4 v;
-  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(a));
-  return v;
-}
 __device__ __forceinline__ void sts4(uint32_t a, uint4 v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z),
                "r"(v.w)
@@ -166,6 +198,8 @@ __device__ __forceinline__ void sts1(uint32_t a, float v) {
 // Rows and tiles of entity e = sequence * nqt + row block; 0 tiles: no rows.
 struct Entity {
   int b, qt, R, q0, nq, len, first, hi_max, nt;
+  // units of the line that one of its items takes: kItemCost, then its tiles
+  __device__ __forceinline__ long long cost() const { return nt > 0 ? nt + kItemCost : 0; }
 };
 __device__ __forceinline__ Entity entity_of(const KvAttnParams &p, int nqt, int e) {
   Entity x;
@@ -208,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
     long long x = 0;
     for (int i = 0; i < per_thread; ++i) {
       const int e = threadIdx.x * per_thread + i;
-      if (e < entities) x += static_cast<long long>(entity_of(p, nqt, e).nt) * p.kv.heads;
+      if (e < entities) x += entity_of(p, nqt, e).cost() * p.kv.heads;
     }
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -277,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = *tmem_slot;  // 0: all 512 columns are this block's
   unsigned int *err = p.kv.err;
   auto wait = [&](uint32_t bar, uint32_t parity) {
     // the whole warp, in step
@@ -288,108 +322,158 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
     int i = 0;
     uint32_t phase = 0;
   };
-  auto next_piece = [&](Reader &r, Piece &x) {
-    if (!wait(piece_full(r.i), r.phase)) return false;
-    x = pieces[r.i];
+  auto done_piece = [&](Reader &r) {
     __syncwarp();
     if (lane == 0) mbar_arrive(piece_empty(r.i));
     if (++r.i == kRing) {
       r.i = 0;
       r.phase ^= 1u;
     }
+  };
+  auto next_piece = [&](Reader &r, Piece &x) {
+    if (!wait(piece_full(r.i), r.phase)) return false;
+    x = pieces[r.i];
+    done_piece(r);
     return x.R > 0;
   };
   Reader reader;
-  Piece x;
 
   // Registers: 2 * 192 + 72 + 56 = 4 * 128, the launch's share
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     // ------------------------------------------------------------ softmax ----
-    const int w = warp >> 2, r = w * 128 + (warp & 3) * 32 + lane;  // this thread's row of an item
-    const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    // Scores come as fragments: a thread (lane 4 g + t) holds rows g + 8 y of its
+    // warp's 32 (y = 0 .. 3) and two of every 8 columns, so a token's scales,
+    // read from shared memory, serve four rows.  (One row a thread needs 96
+    // 16-byte broadcasts per row and tile, more than the 2048 cycles of MMAs.)
+    const int w = warp >> 2, g = lane >> 2, t = lane & 3;
+    const int r0 = w * 128 + (warp & 3) * 32;  // the warp's first row
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t col_s = lanes + PL::COL_S + 128 * w, col_o = lanes + PL::COL_O + 128 * w;
+    constexpr uint32_t kLane16 = 16u << 16;
     uint32_t s_phase = 0, o_phase = 0;
     uint32_t tiles = 0;  // so far
     bool ok = true;
-    while (ok && next_piece(reader, x)) {
+    while (ok && wait(piece_full(reader.i), reader.phase)) {
+      // the piece stays in shared memory until its end (registers are short)
+      const Piece &x = pieces[reader.i];
+      if (x.R == 0) break;
       if (x.R <= w * 128) {  // this half has no rows; keep up with the scales' slots
         tiles += x.t1 - x.t0;
+        done_piece(reader);
         continue;
       }
-      const int ri = x.qt * kRows + r;
-      int lo = 0, hi = 0x7fffffff;
-      if (r < x.R) visible(p, x.len - x.nq + ri / p.group, x.len, lo, hi);
-      float m = kNoRef, l0 = 0.f, l1 = 0.f;
-      for (int i = x.t0; i < x.t1; ++i) {
+      int lo[4], hi[4];
+      int lo_max = 0, hi_min = 0x7fffffff;
+      float m[4], l[4][2];
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const int r = r0 + 8 * y + g;
+        lo[y] = 0;
+        hi[y] = 0x7fffffff;
+        if (r < x.R) visible(p, x.len - x.nq + (x.qt * kRows + r) / p.group, x.len, lo[y], hi[y]);
+        lo_max = max(lo_max, lo[y]);
+        hi_min = min(hi_min, hi[y]);
+        m[y] = kNoRef;
+        l[y][0] = l[y][1] = 0.f;
+      }
+      int j = x.first + x.t0 * kKeys;
+      const int j_end = x.first + x.t1 * kKeys;
+      bool fresh = true;
+      for (; j < j_end; j += kKeys) {
         const uint32_t slot = tiles % PL::SLOTS;
         ok = wait(s_full(w), s_phase) && wait(sc_full(slot), (tiles / PL::SLOTS) & 1u);
         if (!ok) break;
         ++tiles;
         s_phase ^= 1u;
         tc_fence_after();
-        const uint32_t sc = base + PL::OFF_S + slot * (3 * kKeys * 4);
-        const int j = x.first + i * kKeys;
-        float u[128];
+        const float2 *sc = reinterpret_cast<const float2 *>(sm + PL::OFF_S + slot * (3 * kKeys * 4)) + t;
+        // u[y][c]: row y, columns 8 (c / 2) + 2 t + (c & 1)
+        float u[4][32];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t v[32];
-          tmem_ld32(col_s + 32 * c, v);
-          tmem_wait_ld32(v);
+        for (int c = 0; c < 2; ++c) {
+          uint32_t v[64];
+          tmem_ld_frag(col_s + 64 * c, v);
+          tmem_ld_frag(col_s + 64 * c + kLane16, v + 32);
+          tmem_wait_ld<64>(v);
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const float4 k = lds4(sc + (32 * c + e) * 4), y = lds4(sc + (kKeys + 32 * c + e) * 4);
-            float *d = u + 32 * c + e;
-            fma2(d[0], d[1], __uint_as_float(v[e]), __uint_as_float(v[e + 1]), k.x, k.y, y.x, y.y);
-            fma2(d[2], d[3], __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]), k.z, k.w, y.z, y.w);
-          }
-        }
-        if (__any_sync(0xffffffffu, lo > j || hi < j + kKeys)) {
-          const int a = lo - j, z = hi - j;
+          for (int n = 0; n < 8; ++n) {
+            const float2 k = sc[4 * (8 * c + n)], z = sc[kKeys / 2 + 4 * (8 * c + n)];
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (c < a || c >= z) u[c] = -CUDART_INF_F;
-        }
-        float top = fmaxf(u[0], u[1]);
-#pragma unroll
-        for (int c = 2; c < 128; c += 2) top = fmaxf(fmaxf(top, u[c]), u[c + 1]);
-        if (__any_sync(0xffffffffu, top > m + kRoom)) {
-          const float nm = top > m + kRoom ? top - kHead : m;
-          const float a = exp2_fast(m - nm);
-          m = nm;
-          l0 *= a;
-          l1 *= a;
-          if (i > x.t0) {
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t v[32];
-              tmem_ld32(col_o + 32 * c, v);
-              tmem_wait_ld32(v);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * a);
-              tmem_st32(col_o + 32 * c, v);
+            for (int y = 0; y < 4; ++y) {
+              float *d = u[y] + 16 * c + 2 * n;
+              const uint32_t *f = v + 32 * (y >> 1) + 4 * n + 2 * (y & 1);
+              fma2(d[0], d[1], __uint_as_float(f[0]), __uint_as_float(f[1]), k.x, k.y, z.x, z.y);
             }
           }
         }
-        // weights, 32 at a time over the scores that are already in registers
+        if (__any_sync(0xffffffffu, lo_max > j || hi_min < j + kKeys)) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t v[16];
+          for (int y = 0; y < 4; ++y) {
+            const int a = lo[y] - j - 2 * t, z = hi[y] - j - 2 * t;
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            float *d = u + 32 * c + e;
-            add2(d[0], d[1], d[0], d[1], -m);
-            add2(d[2], d[3], d[2], d[3], -m);
-            const float w0 = exp2_fast(d[0]), w1 = exp2_fast(d[1]);
-            const float w2 = exp2_fast(d[2]), w3 = exp2_fast(d[3]);
-            const float4 rv = lds4(sc + (2 * kKeys + 32 * c + e) * 4);
-            fma2(l0, l1, w0, w1, rv.x, rv.y, l0, l1);
-            fma2(l0, l1, w2, w3, rv.z, rv.w, l0, l1);
-            const __half2 h0 = __floats2half2_rn(w0, w1), h1 = __floats2half2_rn(w2, w3);
-            v[e / 2] = *reinterpret_cast<const uint32_t *>(&h0);
-            v[e / 2 + 1] = *reinterpret_cast<const uint32_t *>(&h1);
+            for (int c = 0; c < 32; ++c) {
+              const int col = 8 * (c / 2) + (c & 1);
+              if (col < a || col >= z) u[y][c] = -CUDART_INF_F;
+            }
           }
-          tmem_st16(col_s + 16 * c, v);
+        }
+        bool over = false;
+        float top[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          top[y] = fmaxf(u[y][0], u[y][1]);
+#pragma unroll
+          for (int c = 2; c < 32; c += 2) top[y] = fmaxf(fmaxf(top[y], u[y][c]), u[y][c + 1]);
+          over |= top[y] > m[y] + kRoom;
+        }
+        if (__any_sync(0xffffffffu, over)) {
+          float a[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            top[y] = fmaxf(top[y], __shfl_xor_sync(0xffffffffu, top[y], 1));
+            top[y] = fmaxf(top[y], __shfl_xor_sync(0xffffffffu, top[y], 2));
+            const float nm = top[y] > m[y] + kRoom ? top[y] - kHead : m[y];
+            a[y] = exp2_fast(m[y] - nm);
+            m[y] = nm;
+            l[y][0] *= a[y];
+            l[y][1] *= a[y];
+          }
+          if (!fresh) {
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+              for (int z = 0; z < 2; ++z) {
+                uint32_t v[32];
+                tmem_ld_frag(col_o + 64 * c + z * kLane16, v);
+                tmem_wait_ld<32>(v);
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  v[e] = __float_as_uint(__uint_as_float(v[e]) * a[2 * z + ((e >> 1) & 1)]);
+                tmem_st_frag(col_o + 64 * c + z * kLane16, v);
+              }
+          }
+        }
+        fresh = false;
+        // weights; 8 scores become 4 columns of fp16 pairs
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t v[32];
+#pragma unroll
+          for (int n = 0; n < 8; ++n) {
+            const float2 rv = sc[kKeys + 4 * (8 * c + n)];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              float *d = u[y] + 16 * c + 2 * n;
+              add2(d[0], d[1], d[0], d[1], -m[y]);
+              const float w0 = exp2_fast(d[0]), w1 = exp2_fast(d[1]);
+              fma2(l[y][0], l[y][1], w0, w1, rv.x, rv.y, l[y][0], l[y][1]);
+              const __half2 h = __floats2half2_rn(w0, w1);
+              v[16 * (y >> 1) + 2 * n + (y & 1)] = *reinterpret_cast<const uint32_t *>(&h);
+            }
+          }
+          tmem_st_half_frag(col_s + 32 * c, v);
+          tmem_st_half_frag(col_s + 32 * c + kLane16, v + 16);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -397,14 +481,27 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
         if (lane == 0) mbar_arrive(p_full(w));
       }
       if (!ok) break;
-      // -- the item's (or piece's) end
+      // -- the item's (or piece's) end: a thread takes the row of its lane
+      float sum = 0.f, ref = 0.f;
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        float z = l[y][0] + l[y][1];
+        z += __shfl_xor_sync(0xffffffffu, z, 1);
+        z += __shfl_xor_sync(0xffffffffu, z, 2);
+        const float a = __shfl_sync(0xffffffffu, z, 4 * (lane & 7));
+        const float c = __shfl_sync(0xffffffffu, m[y], 4 * (lane & 7));
+        if (lane >> 3 == y) {
+          sum = a;
+          ref = c;
+        }
+      }
       ok = wait(o_full(w), o_phase);
       if (!ok) break;
       o_phase ^= 1u;
       tc_fence_after();
-      const float l = l0 + l1;
+      const int r = r0 + lane, ri = x.qt * kRows + r;
       const bool whole = x.t0 == 0 && x.t1 == x.nt;
-      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
       const long long row = (static_cast<long long>(x.q0) + ri / p.group) * p.Hq + x.h * p.group + ri % p.group;
       const long long part = static_cast<long long>(blockIdx.x) * 2 + (x.t0 == 0 ? 1 : 0);
       float *dst = parts + part * kRows * (D + 2) + r * D;
@@ -442,14 +539,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
       if (r < x.R) {
         if (!whole) {
           float *ml = parts + part * kRows * (D + 2) + kRows * D + 2 * r;
-          ml[0] = m;
-          ml[1] = l;
+          ml[0] = ref;
+          ml[1] = sum;
         } else if (p.lse != nullptr) {
-          p.lse[row] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * kLn2;
+          p.lse[row] = sum == 0.f ? -CUDART_INF_F : (ref + log2f(sum)) * kLn2;
         }
       }
       if (!whole && x.t0 == 0 && threadIdx.x == 0) descs[blockIdx.x] = Desc{x.b, x.h, x.qt, x.last};
       tc_fence_before();
+      done_piece(reader);
     }
   } else if (warp < 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
@@ -486,6 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
         }
       }
     };
+    Piece x;
     while (ok && next_piece(reader, x)) {
       const int end = min(x.hi_max, x.len);
       for (int i = x.t0; i < x.t1; ++i) {
@@ -535,40 +634,37 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 12) {
       // ------------------------------------------------------------- MMAs ----
-      // (whole warp in step, one thread issues)
-      const bool issue = lane == 0;
+      const uint32_t on = elect();
       int ks = 0, vs = 0;  // stages, and their phases
       uint32_t kph = 0, vph = 0, qph[2] = {0, 0}, pph[2] = {0, 0};
+      const uint64_t q_desc = sw128_desc(base + PL::OFF_Q), k_desc = sw128_desc(base + PL::OFF_K);
+      const uint64_t v_desc0 = v_desc(base + PL::OFF_V);
       auto scores = [&](int w) {
-        if (issue) {
-          tc_fence_after();
+        tc_fence_after();
+        const uint64_t a = q_desc + w * (PL::TILE >> 4), b = k_desc + ks * (PL::TILE >> 4);
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t at = (k >> 2) * PL::SUB + (k & 3) * 32;
-            tc_mma(tmem + PL::COL_S + 128 * w, sw128_desc(base + PL::OFF_Q + w * PL::TILE + at),
-                   sw128_desc(base + PL::OFF_K + ks * PL::TILE + at), kIdescS, k > 0);
-          }
-          tc_commit(s_full(w));
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t at = ((k >> 2) * PL::SUB + (k & 3) * 32) >> 4;
+          mma_ss(on, PL::COL_S + 128 * w, a + at, b + at, kIdescS, k > 0);
         }
-        __syncwarp();
+        commit_if(on, s_full(w));
       };
       auto values = [&](int w, bool fresh) {
-        if (issue) {
-          tc_fence_after();
+        tc_fence_after();
+        const uint64_t b = v_desc0 + vs * (PL::TILE >> 4);
 #pragma unroll
-          for (int k = 0; k < kKeys / 16; ++k)
-            tc_mma_ts(tmem + PL::COL_O + 128 * w, tmem + PL::COL_S + 128 * w + 8 * k,
-                      v_desc(base + PL::OFF_V + vs * PL::TILE + k * 2048), idesc_pv<D>(), !(fresh && k == 0));
-        }
-        __syncwarp();
+        for (int k = 0; k < kKeys / 16; ++k)
+          mma_ts(on, PL::COL_O + 128 * w, PL::COL_S + 128 * w + 8 * k, b + k * (2048 >> 4),
+                 idesc_pv<D>(), !(fresh && k == 0));
       };
       // the K stage whose scores are next: waited for once, released after the last half
       auto open_k = [&]() { return wait(k_full(ks), kph); };
       auto close_k = [&]() {
-        if (issue) tc_commit(k_empty(ks));
+        commit_if(on, k_empty(ks));
         ks ^= 1;
         if (ks == 0) kph ^= 1u;
       };
+      Piece x;
       bool ok = true, have = next_piece(reader, x);
       if (have) {
         ok = wait(q_full(0), qph[0]) && open_k();
@@ -580,9 +676,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
           if (ok) scores(1);
         }
         if (ok) {
-          if (issue && x.t1 - x.t0 == 1) {
-            tc_commit(q_empty(0));
-            if (x.R > 128) tc_commit(q_empty(1));
+          if (x.t1 - x.t0 == 1) {
+            commit_if(on, q_empty(0));
+            if (x.R > 128) commit_if(on, q_empty(1));
           }
           close_k();
         }
@@ -608,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
               pph[w] ^= 1u;
               if (!ok) break;
               values(w, i == x.t0);
-              if (issue && last) tc_commit(o_full(w));
+              if (last) commit_if(on, o_full(w));
             }
             if (R2 > 128 * w) {
               if (last) {
@@ -621,11 +717,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
               scores(w);
               // the item's last scores: its Q rows may be replaced
               const bool q_done = last ? y.t1 - y.t0 == 1 : i + 2 == x.t1;
-              if (issue && q_done) tc_commit(q_empty(w));
+              if (q_done) commit_if(on, q_empty(w));
             }
           }
           if (!ok) break;
-          if (issue) tc_commit(v_empty(vs));
+          commit_if(on, v_empty(vs));
           vs ^= 1;
           if (vs == 0) vph ^= 1u;
           if (opened) close_k();
@@ -634,15 +730,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
         have = more;
       }
       // every MMA has landed before TMEM is freed
-      if (issue) {
-        tc_commit(drain);
-        wait_bar_teardown(drain, 0);
-      }
+      commit_if(on, drain);
+      wait_bar_teardown(drain, 0);
       __syncwarp();
     } else if (warp < 15) {
       // ---------------------------------------------------------- Q rows ----
       const int w = warp - 13;
       uint32_t phase = 1;
+      Piece x;
       while (next_piece(reader, x)) {
         if (x.R <= w * 128) continue;
         if (!wait(q_empty(w), phase)) break;
@@ -690,25 +785,29 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
       uint32_t phase = 1;
       bool ok = true;
       for (long long at = c0; ok;) {
-        if (at < c1)
-          while (at >= start + static_cast<long long>(en.nt) * p.kv.heads) {
-            start += static_cast<long long>(en.nt) * p.kv.heads;
+        // the next piece that has a tile in the range
+        int t0 = 0, t1 = 0, h = 0;
+        long long istart = 0;
+        while (at < c1 && t0 == t1) {
+          while (at >= start + en.cost() * p.kv.heads) {
+            start += en.cost() * p.kv.heads;
             en = entity_of(p, nqt, ++e);
           }
+          h = static_cast<int>((at - start) / en.cost());
+          istart = start + h * en.cost();
+          t0 = static_cast<int>(max(at - istart - kItemCost, 0LL));
+          t1 = static_cast<int>(max(min(en.cost(), c1 - istart) - kItemCost, 0LL));
+          at = istart + kItemCost + t1;
+        }
+        const bool end = t0 == t1;
         ok = wait(piece_empty(slot.i), phase);
         if (!ok) break;
-        const bool end = at >= c1;
         if (end) {
           if (lane == 0) pieces[slot.i].R = 0;
         } else {
-          const int h = static_cast<int>((at - start) / en.nt);
-          const long long istart = start + static_cast<long long>(h) * en.nt;
-          const int t0 = static_cast<int>(at - istart);
-          const int t1 = static_cast<int>(min(static_cast<long long>(en.nt), c1 - istart));
           if (lane == 0)
             pieces[slot.i] = Piece{en.b, h, en.qt, en.R, en.q0, en.nq, en.len, en.first, en.hi_max,
-                                   t0, t1, en.nt, static_cast<int>((istart + en.nt - 1) / per)};
-          at = istart + t1;
+                                   t0, t1, en.nt, static_cast<int>((istart + en.cost() - 1) / per)};
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(piece_full(slot.i));
@@ -791,7 +890,7 @@ int launch_t(const KvAttnParams &p, cudaStream_t s) {
   const long long tokens = static_cast<long long>(p.table_w) << p.kv.page_shift;
   // + 15: the first tile starts on a multiple of 16 before the first key
   const long long tiles = tokens > 0 ? (tokens + 15 + kKeys - 1) / kKeys : 1;
-  const long long most = nqt * p.B * p.kv.heads * tiles;
+  const long long most = nqt * p.B * p.kv.heads * (tiles + kItemCost);
   const int grid = static_cast<int>(most < kNumSMsGB300 ? most : kNumSMsGB300);
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
