@@ -75,7 +75,7 @@ struct Plan {
   static constexpr int OFF_Q = 0, OFF_K = 2 * TILE, OFF_V = 4 * TILE, OFF_S = 6 * TILE;
   static constexpr int SLOTS = 3;                      // of token scales (see the converters)
   static constexpr int OFF_BAR = OFF_S + SLOTS * 3 * kKeys * 4;
-  static constexpr int BARS = 18 + SLOTS + 2 * kRing + 1;
+  static constexpr int BARS = 22 + SLOTS + 2 * kRing + 1;
   static constexpr int OFF_PIECE = OFF_BAR + BARS * 8;
   static constexpr int OFF_MISC = OFF_PIECE + kRing * static_cast<int>(sizeof(Piece));
   static constexpr int SMEM = OFF_MISC + 16 + 1024;    // 1024: aligned by hand
@@ -150,13 +150,17 @@ __device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t *v) 
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
       : "memory");
 }
-// 16 lanes x 32 columns: register 2 n + e is TMEM lane g + 8 e, column 4 n + t.
+// 16 lanes x 16 columns: register 2 n + e is TMEM lane g + 8 e, column 4 n + t.
 __device__ __forceinline__ void tmem_st_half_frag(uint32_t taddr, const uint32_t *v) {
   asm volatile(
-      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      "tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
       : "memory");
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 // waits for this thread's TMEM loads; the registers pass through
 template <int N>
@@ -274,11 +278,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
   auto v_full = [&](int s) { return bar0 + 8u * (8 + s); };
   auto v_empty = [&](int s) { return bar0 + 8u * (10 + s); };
   auto s_full = [&](int w) { return bar0 + 8u * (12 + w); };
-  auto p_full = [&](int w) { return bar0 + 8u * (14 + w); };
-  auto o_full = [&](int w) { return bar0 + 8u * (16 + w); };
-  auto sc_full = [&](int i) { return bar0 + 8u * (18 + i); };
-  auto piece_full = [&](int i) { return bar0 + 8u * (18 + PL::SLOTS + i); };
-  auto piece_empty = [&](int i) { return bar0 + 8u * (18 + PL::SLOTS + kRing + i); };
+  auto p_full = [&](int w, int c) { return bar0 + 8u * (14 + 2 * w + c); };  // keys 64 c .. + 63
+  auto o_full = [&](int w) { return bar0 + 8u * (18 + w); };
+  auto a_done = [&](int w) { return bar0 + 8u * (20 + w); };  // products of a tile's first 64 keys
+  auto sc_full = [&](int i) { return bar0 + 8u * (22 + i); };
+  auto piece_full = [&](int i) { return bar0 + 8u * (22 + PL::SLOTS + i); };
+  auto piece_empty = [&](int i) { return bar0 + 8u * (22 + PL::SLOTS + kRing + i); };
   const uint32_t drain = bar0 + 8u * (PL::BARS - 1);
   Piece *pieces = reinterpret_cast<Piece *>(sm + PL::OFF_PIECE);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + PL::OFF_MISC);
@@ -292,8 +297,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
       mbar_init(v_full(i), 4);
       mbar_init(v_empty(i), 1);
       mbar_init(s_full(i), 1);
-      mbar_init(p_full(i), 4);
+      mbar_init(p_full(i, 0), 4);
+      mbar_init(p_full(i, 1), 4);
       mbar_init(o_full(i), 1);
+      mbar_init(a_done(i), 1);
     }
     for (int i = 0; i < PL::SLOTS; ++i) mbar_init(sc_full(i), 4);
     for (int i = 0; i < kRing; ++i) {
@@ -338,9 +345,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
   };
   Reader reader;
 
-  // Registers: 2 * 192 + 72 + 56 = 4 * 128, the launch's share
+  // Registers: 2 * 160 + 104 + 88 = 4 * 128, the launch's share
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
     // ------------------------------------------------------------ softmax ----
     // Scores come as fragments: a thread (lane 4 g + t) holds rows g + 8 y of its
     // warp's 32 (y = 0 .. 3) and two of every 8 columns, so a token's scales,
@@ -363,17 +370,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
         done_piece(reader);
         continue;
       }
-      int lo[4], hi[4];
+      // keys that row g + 8 y sees; rows past the item's: all
+      auto limits = [&](int y, int &lo, int &hi) {
+        const int r = r0 + 8 * y + g;
+        lo = 0;
+        hi = 0x7fffffff;
+        if (r < x.R) visible(p, x.len - x.nq + (x.qt * kRows + r) / p.group, x.len, lo, hi);
+      };
       int lo_max = 0, hi_min = 0x7fffffff;
       float m[4], l[4][2];
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
-        const int r = r0 + 8 * y + g;
-        lo[y] = 0;
-        hi[y] = 0x7fffffff;
-        if (r < x.R) visible(p, x.len - x.nq + (x.qt * kRows + r) / p.group, x.len, lo[y], hi[y]);
-        lo_max = max(lo_max, lo[y]);
-        hi_min = min(hi_min, hi[y]);
+        int lo, hi;
+        limits(y, lo, hi);
+        lo_max = max(lo_max, lo);
+        hi_min = min(hi_min, hi);
         m[y] = kNoRef;
         l[y][0] = l[y][1] = 0.f;
       }
@@ -388,97 +399,107 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
         s_phase ^= 1u;
         tc_fence_after();
         const float2 *sc = reinterpret_cast<const float2 *>(sm + PL::OFF_S + slot * (3 * kKeys * 4)) + t;
-        // u[y][c]: row y, columns 8 (c / 2) + 2 t + (c & 1)
-        float u[4][32];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t v[64];
-          tmem_ld_frag(col_s + 64 * c, v);
-          tmem_ld_frag(col_s + 64 * c + kLane16, v + 32);
-          tmem_wait_ld<64>(v);
+        // 64 keys at a time: their weights are handed over, and multiplied, while
+        // the others are being made (and half the registers do)
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c, sc += kKeys / 4) {
+          // u[32 z + 4 n + 2 f + e]: row y = 2 z + f, column 64 c + 8 n + 2 t + e
+          uint32_t s[64];
+          tmem_ld_frag(col_s + 64 * c, s);
+          tmem_ld_frag(col_s + 64 * c + kLane16, s + 32);
+          tmem_wait_ld<64>(s);
+          float *u = reinterpret_cast<float *>(s);
 #pragma unroll
           for (int n = 0; n < 8; ++n) {
-            const float2 k = sc[4 * (8 * c + n)], z = sc[kKeys / 2 + 4 * (8 * c + n)];
+            const float2 k = sc[4 * n], z = sc[kKeys / 2 + 4 * n];
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
-              float *d = u[y] + 16 * c + 2 * n;
-              const uint32_t *f = v + 32 * (y >> 1) + 4 * n + 2 * (y & 1);
-              fma2(d[0], d[1], __uint_as_float(f[0]), __uint_as_float(f[1]), k.x, k.y, z.x, z.y);
+              float *d = u + 32 * (y >> 1) + 4 * n + 2 * (y & 1);
+              fma2(d[0], d[1], d[0], d[1], k.x, k.y, z.x, z.y);
             }
           }
-        }
-        if (__any_sync(0xffffffffu, lo_max > j || hi_min < j + kKeys)) {
+          const int jc = j + 64 * c;
+          if (__any_sync(0xffffffffu, lo_max > jc || hi_min < jc + 64)) {
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const int a = lo[y] - j - 2 * t, z = hi[y] - j - 2 * t;
+            for (int y = 0; y < 4; ++y) {
+              int lo, hi;
+              limits(y, lo, hi);
+              lo -= jc + 2 * t;
+              hi -= jc + 2 * t;
 #pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              const int col = 8 * (c / 2) + (c & 1);
-              if (col < a || col >= z) u[y][c] = -CUDART_INF_F;
+              for (int n = 0; n < 8; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  if (8 * n + e < lo || 8 * n + e >= hi) u[32 * (y >> 1) + 4 * n + 2 * (y & 1) + e] = -CUDART_INF_F;
             }
           }
-        }
-        bool over = false;
-        float top[4];
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          top[y] = fmaxf(u[y][0], u[y][1]);
-#pragma unroll
-          for (int c = 2; c < 32; c += 2) top[y] = fmaxf(fmaxf(top[y], u[y][c]), u[y][c + 1]);
-          over |= top[y] > m[y] + kRoom;
-        }
-        if (__any_sync(0xffffffffu, over)) {
-          float a[4];
+          bool over = false;
+          float top[4];
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
-            top[y] = fmaxf(top[y], __shfl_xor_sync(0xffffffffu, top[y], 1));
-            top[y] = fmaxf(top[y], __shfl_xor_sync(0xffffffffu, top[y], 2));
-            const float nm = top[y] > m[y] + kRoom ? top[y] - kHead : m[y];
-            a[y] = exp2_fast(m[y] - nm);
-            m[y] = nm;
-            l[y][0] *= a[y];
-            l[y][1] *= a[y];
+            const float *d = u + 32 * (y >> 1) + 2 * (y & 1);
+            top[y] = fmaxf(d[0], d[1]);
+#pragma unroll
+            for (int n = 1; n < 8; ++n) top[y] = max3(top[y], d[4 * n], d[4 * n + 1]);
+            over |= top[y] > m[y] + kRoom;
           }
-          if (!fresh) {
+          if (__any_sync(0xffffffffu, over)) {
+            float a[4];
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c)
+            for (int y = 0; y < 4; ++y) {
+              top[y] = fmaxf(top[y], __shfl_xor_sync(0xffffffffu, top[y], 1));
+              top[y] = fmaxf(top[y], __shfl_xor_sync(0xffffffffu, top[y], 2));
+              const float nm = top[y] > m[y] + kRoom ? top[y] - kHead : m[y];
+              a[y] = exp2_fast(m[y] - nm);
+              m[y] = nm;
+              l[y][0] *= a[y];
+              l[y][1] *= a[y];
+            }
+            // O is this warp's to change once the products so far are in: those of
+            // the tile's first 64 keys have a barrier of their own
+            if (c == 1) ok = ok && wait(a_done(w), s_phase ^ 1u);
+            if (!fresh || c == 1) {
+              tc_fence_after();
 #pragma unroll
-              for (int z = 0; z < 2; ++z) {
-                uint32_t v[32];
-                tmem_ld_frag(col_o + 64 * c + z * kLane16, v);
-                tmem_wait_ld<32>(v);
+              for (int q = 0; q < D / 64; ++q)
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  v[e] = __float_as_uint(__uint_as_float(v[e]) * a[2 * z + ((e >> 1) & 1)]);
-                tmem_st_frag(col_o + 64 * c + z * kLane16, v);
+                for (int z = 0; z < 2; ++z) {
+                  uint32_t v[32];
+                  tmem_ld_frag(col_o + 64 * q + z * kLane16, v);
+                  tmem_wait_ld<32>(v);
+#pragma unroll
+                  for (int e = 0; e < 32; ++e)
+                    v[e] = __float_as_uint(__uint_as_float(v[e]) * a[2 * z + ((e >> 1) & 1)]);
+                  tmem_st_frag(col_o + 64 * q + z * kLane16, v);
+                }
+            }
+          }
+          // 8 scores become 4 columns of fp16 pairs
+#pragma unroll
+          for (int n0 = 0; n0 < 8; n0 += 4) {
+            uint32_t v[16];
+#pragma unroll
+            for (int n = n0; n < n0 + 4; ++n) {
+              const float2 rv = sc[kKeys + 4 * n];
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                float *d = u + 32 * (y >> 1) + 4 * n + 2 * (y & 1);
+                add2(d[0], d[1], d[0], d[1], -m[y]);
+                const float w0 = exp2_fast(d[0]), w1 = exp2_fast(d[1]);
+                fma2(l[y][0], l[y][1], w0, w1, rv.x, rv.y, l[y][0], l[y][1]);
+                const __half2 h = __floats2half2_rn(w0, w1);
+                v[8 * (y >> 1) + 2 * (n - n0) + (y & 1)] = *reinterpret_cast<const uint32_t *>(&h);
               }
+            }
+            tmem_st_half_frag(col_s + 32 * c + 4 * n0, v);
+            tmem_st_half_frag(col_s + 32 * c + 4 * n0 + kLane16, v + 8);
           }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full(w, c));
         }
         fresh = false;
-        // weights; 8 scores become 4 columns of fp16 pairs
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t v[32];
-#pragma unroll
-          for (int n = 0; n < 8; ++n) {
-            const float2 rv = sc[kKeys + 4 * (8 * c + n)];
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              float *d = u[y] + 16 * c + 2 * n;
-              add2(d[0], d[1], d[0], d[1], -m[y]);
-              const float w0 = exp2_fast(d[0]), w1 = exp2_fast(d[1]);
-              fma2(l[y][0], l[y][1], w0, w1, rv.x, rv.y, l[y][0], l[y][1]);
-              const __half2 h = __floats2half2_rn(w0, w1);
-              v[16 * (y >> 1) + 2 * n + (y & 1)] = *reinterpret_cast<const uint32_t *>(&h);
-            }
-          }
-          tmem_st_half_frag(col_s + 32 * c, v);
-          tmem_st_half_frag(col_s + 32 * c + kLane16, v + 16);
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full(w));
       }
       if (!ok) break;
       // -- the item's (or piece's) end: a thread takes the row of its lane
@@ -550,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
       done_piece(reader);
     }
   } else if (warp < 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     // --------------------------------------------------------- converters ----
     // The scales have a third slot: a tile's are read until both halves' weights
     // are written, and slot s is refilled for tile i + 3 only once the K stage
@@ -631,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
       }
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 12) {
       // ------------------------------------------------------------- MMAs ----
       const uint32_t on = elect();
@@ -649,11 +670,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
         }
         commit_if(on, s_full(w));
       };
-      auto values = [&](int w, bool fresh) {
+      // O_w += P V over keys 64 c .. + 63
+      auto values = [&](int w, int c, bool fresh) {
         tc_fence_after();
         const uint64_t b = v_desc0 + vs * (PL::TILE >> 4);
 #pragma unroll
-        for (int k = 0; k < kKeys / 16; ++k)
+        for (int k = 4 * c; k < 4 * c + 4; ++k)
           mma_ts(on, PL::COL_O + 128 * w, PL::COL_S + 128 * w + 8 * k, b + k * (2048 >> 4),
                  idesc_pv<D>(), !(fresh && k == 0));
       };
@@ -700,10 +722,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
             if (x.R > 128 * w) {
-              ok = ok && wait(p_full(w), pph[w]);
+              ok = ok && wait(p_full(w, 0), pph[w]);
+              if (!ok) break;
+              values(w, 0, i == x.t0);
+              commit_if(on, a_done(w));
+              ok = wait(p_full(w, 1), pph[w]);
               pph[w] ^= 1u;
               if (!ok) break;
-              values(w, i == x.t0);
+              values(w, 1, false);
               if (last) commit_if(on, o_full(w));
             }
             if (R2 > 128 * w) {
