@@ -374,6 +374,7 @@ class KVCache:
         if not 16 <= self.page_size <= 1024 or self.page_size & (self.page_size - 1):
             raise ValueError(f"page_size must be a power of two from 16 to 1024, got {self.page_size}")
         self.device = k_codes.device
+        self.index = self.device.index
         self._struct = _CacheStruct(k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(),
                                     v_scale.data_ptr(), self.num_pages, self.kv_heads,
                                     self.page_size, self.head_dim, self.bits)
@@ -392,69 +393,93 @@ class KVCache:
                              for _ in range(2)))
 
 
-def _on(cache: KVCache, t: torch.Tensor, dtype, name: str):
-    """t is a tensor of this type on the cache's device."""
+# A decoding step's kernels take a few microseconds, so these calls keep their
+# checks short: plain comparisons first, the words only when one fails.
+
+_HALF, _INT, _LONG, _FLOAT = torch.float16, torch.int32, torch.int64, torch.float32
+# the current stream's handle and the current device, without building objects
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _refuse(cache: KVCache, t, dtype, name: str, shape):
+    """Says what is wrong with a tensor that failed its checks."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype is not dtype:
+    if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != cache.device:
         raise ValueError(f"{name} must be on the cache's device {cache.device}, got {t.device}")
+    if len(t.shape) != len(shape) or any(a is not None and a != b for a, b in zip(shape, t.shape)):
+        raise ValueError(f"{name} must have shape {tuple(shape)} (None: any), got {tuple(t.shape)}")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _rows(cache: KVCache, t: torch.Tensor, name: str, shape):
-    """t is an fp16 [tokens, heads, D] of this shape (None: any) with contiguous rows."""
-    _on(cache, t, torch.float16, name)
-    if t.dim() != 3 or any(a is not None and a != b for a, b in zip(shape, t.shape)):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+def _vector(cache: KVCache, t: torch.Tensor, dtype, name: str, shape):
+    """t is a contiguous tensor of this type and shape on the cache's device."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.device == cache.device and t.is_contiguous()):
+        _refuse(cache, t, dtype, name, shape)
+
+
+def _rows(cache: KVCache, t: torch.Tensor, name: str, heads: int | None, T: int | None):
+    """Token and head strides of t, an fp16 [tokens, heads, D] with contiguous rows
+    (heads, T: None for any)."""
+    D = cache.head_dim
+    if not (isinstance(t, torch.Tensor) and t.dtype is _HALF and t.device == cache.device
+            and t.dim() == 3):
+        _refuse(cache, t, _HALF, name, (T, heads, D))
+    n, h, d = t.shape
+    if d != D or (heads is not None and h != heads) or (T is not None and n != T):
+        _refuse(cache, t, _HALF, name, (T, heads, D))
     ts, hs, ds = t.stride()
     if ds != 1:
         raise ValueError(f"{name} must be contiguous along the head dimension")
     # the stride of a dimension of one element says nothing
-    return (ts if t.shape[0] > 1 else 0), (hs if t.shape[1] > 1 else 0)
-
-
-def _vector(cache: KVCache, t: torch.Tensor, dtype, name: str, shape):
-    _on(cache, t, dtype, name)
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    return (ts if n > 1 else 0), (hs if h > 1 else 0), n, h
 
 
 def _stream_of(cache: KVCache) -> int:
     """The current stream of the cache's device, which has to be the current device."""
-    index = cache.device.index
-    if torch.cuda.current_device() != index:
+    index = cache.index
+    if _current_device() != index:
         raise ValueError(f"the cache is on {cache.device}, which is not the current device")
-    return torch.cuda.current_stream(index).cuda_stream
+    return _raw_stream(index)
 
 
 def kv_cache_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache: KVCache) -> None:
     """Quantizes fp16 k, v [T, kv_heads, D] (any token and head strides that are
     multiples of 8) into the cache's slots, int64 [T] (page * page_size +
     offset; negative: not stored)."""
-    ks = _rows(cache, k, "k", (None, cache.kv_heads, cache.head_dim))
-    vs = _rows(cache, v, "v", k.shape)
-    T = k.shape[0]
-    _vector(cache, slots, torch.int64, "slots", (T,))
-    _check(load().kv_cache_write(k.data_ptr(), *ks, v.data_ptr(), *vs, slots.data_ptr(), T,
-                                 cache._at, _stream_of(cache)), "kv_cache_write")
+    kts, khs, T, heads = _rows(cache, k, "k", cache.kv_heads, None)
+    vts, vhs, _, _ = _rows(cache, v, "v", heads, T)
+    _vector(cache, slots, _LONG, "slots", (T,))
+    status = (_lib or load()).kv_cache_write(k.data_ptr(), kts, khs, v.data_ptr(), vts, vhs,
+                                             slots.data_ptr(), T, cache._at, _stream_of(cache))
+    if status:
+        _check(status, "kv_cache_write")
 
 
 def kv_cache_read(slots: torch.Tensor, cache: KVCache, k=None, v=None):
     """The dequantized fp16 (k, v) [T, kv_heads, D] of the slots, int64 [T]
     (negative: zeros)."""
-    _on(cache, slots, torch.int64, "slots")
-    T = slots.numel()
-    _vector(cache, slots, torch.int64, "slots", (T,))
+    T = slots.shape[0] if isinstance(slots, torch.Tensor) and slots.dim() == 1 else None
+    _vector(cache, slots, _LONG, "slots", (T,))
     shape = (T, cache.kv_heads, cache.head_dim)
-    k = torch.empty(shape, dtype=torch.float16, device=cache.device) if k is None else k
-    v = torch.empty(shape, dtype=torch.float16, device=cache.device) if v is None else v
-    _vector(cache, k, torch.float16, "k", shape)
-    _vector(cache, v, torch.float16, "v", shape)
-    _check(load().kv_cache_read(slots.data_ptr(), T, cache._at, k.data_ptr(), v.data_ptr(),
-                                _stream_of(cache)), "kv_cache_read")
+    device = cache.device
+    if k is None:
+        k = torch.empty(shape, dtype=_HALF, device=device)
+    else:
+        _vector(cache, k, _HALF, "k", shape)
+    if v is None:
+        v = torch.empty(shape, dtype=_HALF, device=device)
+    else:
+        _vector(cache, v, _HALF, "v", shape)
+    status = (_lib or load()).kv_cache_read(slots.data_ptr(), T, cache._at, k.data_ptr(),
+                                            v.data_ptr(), _stream_of(cache))
+    if status:
+        _check(status, "kv_cache_read")
     return k, v
 
 
@@ -476,38 +501,45 @@ def kv_cache_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tenso
     (None: one query per sequence); max_q: upper bound of one sequence's
     queries (default T).  causal, window: which keys a query sees.  Returns out
     fp16 [T, q_heads, D], or (out, lse fp32 [T, q_heads]) with return_lse."""
-    ts, hs = _rows(cache, q, "q", (None, None, cache.head_dim))
-    T, heads, D = q.shape
-    _on(cache, block_table, torch.int32, "block_table")
-    if block_table.dim() != 2 or not block_table.is_contiguous():
-        raise ValueError("block_table must be a contiguous [sequences, pages]")
+    ts, hs, T, heads = _rows(cache, q, "q", None, None)
+    device = cache.device
+    if not (isinstance(block_table, torch.Tensor) and block_table.dtype is _INT
+            and block_table.dim() == 2 and block_table.device == device
+            and block_table.is_contiguous()):
+        _refuse(cache, block_table, _INT, "block_table", (None, None))
     B, width = block_table.shape
-    _vector(cache, seq_lens, torch.int32, "seq_lens", (B,))
-    offsets_at = 0
-    if q_offsets is not None:
-        _vector(cache, q_offsets, torch.int32, "q_offsets", (B + 1,))
+    _vector(cache, seq_lens, _INT, "seq_lens", (B,))
+    if q_offsets is None:
+        offsets_at, max_q = 0, 1
+    else:
+        _vector(cache, q_offsets, _INT, "q_offsets", (B + 1,))
         offsets_at = q_offsets.data_ptr()
-        max_q = max(T, 1) if max_q is None else max_q
-    else:
-        max_q = 1
-    lib = load()
-    need = lib.kv_cache_attention_workspace_bytes(T, heads, B, max_q, width, cache._at)
+        if max_q is None:
+            max_q = T or 1
+    lib = _lib or load()
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=cache.device)
-    elif workspace.dtype is not torch.uint8 or not workspace.is_contiguous() or workspace.device != cache.device:
+        need = lib.kv_cache_attention_workspace_bytes(T, heads, B, max_q, width, cache._at)
+        workspace = torch.empty(need or 1, dtype=torch.uint8, device=device)
+    elif not (workspace.dtype is torch.uint8 and workspace.device == device
+              and workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous torch.uint8 tensor on the cache's device")
+    D = cache.head_dim
     if out is None:
-        out = torch.empty((T, heads, D), dtype=torch.float16, device=cache.device)
+        out = torch.empty((T, heads, D), dtype=_HALF, device=device)
     else:
-        _vector(cache, out, torch.float16, "out", (T, heads, D))
+        _vector(cache, out, _HALF, "out", (T, heads, D))
+    lse_at = 0
     if return_lse:
         if lse is None:
-            lse = torch.empty((T, heads), dtype=torch.float32, device=cache.device)
+            lse = torch.empty((T, heads), dtype=_FLOAT, device=device)
         else:
-            _vector(cache, lse, torch.float32, "lse", (T, heads))
-    _check(lib.kv_cache_attention(
+            _vector(cache, lse, _FLOAT, "lse", (T, heads))
+        lse_at = lse.data_ptr()
+    status = lib.kv_cache_attention(
         q.data_ptr(), ts, hs, T, heads, offsets_at, B, max_q, block_table.data_ptr(), width,
         seq_lens.data_ptr(), cache._at, D ** -0.5 if softmax_scale is None else softmax_scale,
-        int(causal), window, workspace.data_ptr(), workspace.numel(), out.data_ptr(),
-        lse.data_ptr() if return_lse else 0, _stream_of(cache)), "kv_cache_attention")
+        1 if causal else 0, window, workspace.data_ptr(), workspace.numel(), out.data_ptr(),
+        lse_at, _stream_of(cache))
+    if status:
+        _check(status, "kv_cache_attention")
     return (out, lse) if return_lse else out
