@@ -7,17 +7,16 @@
 // (2048 cycles of the tensor pipe at D = 128) against 17 KB of cache, so it is
 // bound by the tensor pipe, with the softmax (32768 exponentials) close behind.
 //
-// One CTA of 16 warps per SM:
-//   warps 0-3, 4-7   softmax of rows 0-127 and 128-255: a thread owns a row
-//                    (TMEM lane), reads its 128 scores, writes its weights P back
-//                    over them as fp16;
-//   warps 8-11       converters: a thread owns a token; codes to fp16 (exact)
+// One CTA of 24 warps per SM:
+//   warps 0-7, 8-15  softmax of rows 0-127 and 128-255, 16 rows a warp: scores
+//                    from TMEM, weights P back over them as fp16;
+//   warps 16-19      converters: a thread owns a token; codes to fp16 (exact)
 //                    into 128-byte-swizzled stages, and the token's scales;
-//   warp 12          issues the MMAs (one thread): S_0, S_1 of the next keys are
-//                    issued between the P V of the two row halves, so that one
-//                    half's softmax runs under the other half's products;
-//   warps 13, 14     bring the next item's Q rows while the current one finishes;
-//   warp 15          walks this block's range of work and publishes its pieces.
+//   warp 20          issues the MMAs: S_0, S_1 of the next keys go between the
+//                    P V of the two row halves, so that one half's softmax runs
+//                    under the other half's products;
+//   warps 21, 22     bring the next item's Q rows while the current one finishes;
+//   warp 23          walks this block's range of work and publishes its pieces.
 // TMEM: S_0, S_1 (128 columns each, P in their first 64), O_0, O_1 (D columns).
 //
 // Operands: Q and K are K-major.  V keeps its token rows and is read as the
@@ -48,7 +47,7 @@
 namespace w8a8 {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kSoftWarps = 16, kWarps = kSoftWarps + 8, kThreads = 32 * kWarps;
 constexpr int kRows = 256;  // of an item
 constexpr int kKeys = 128;  // of a tile
 constexpr int kRing = 4;    // published pieces
@@ -75,9 +74,10 @@ struct Plan {
   static constexpr int OFF_Q = 0, OFF_K = 2 * TILE, OFF_V = 4 * TILE, OFF_S = 6 * TILE;
   static constexpr int SLOTS = 3;                      // of token scales (see the converters)
   static constexpr int OFF_BAR = OFF_S + SLOTS * 3 * kKeys * 4;
-  static constexpr int BARS = 22 + SLOTS + 2 * kRing + 1;
+  static constexpr int BARS = 30 + SLOTS + 2 * kRing + 1;
   static constexpr int OFF_PIECE = OFF_BAR + BARS * 8;
-  static constexpr int OFF_MISC = OFF_PIECE + kRing * static_cast<int>(sizeof(Piece));
+  static constexpr int OFF_STAT = OFF_PIECE + kRing * static_cast<int>(sizeof(Piece));  // M, l of the rows
+  static constexpr int OFF_MISC = OFF_STAT + kRows * 8;
   static constexpr int SMEM = OFF_MISC + 16 + 1024;    // 1024: aligned by hand
   static constexpr uint32_t COL_S = 0, COL_O = 256;    // S_w at 128 w, O_w at 256 + 128 w
 };
@@ -143,18 +143,24 @@ __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t *v) {
       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
       : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t *v) {
+// the same for 32 columns
+__device__ __forceinline__ void tmem_ld_frag4(uint32_t taddr, uint32_t *v) {
   asm volatile(
-      "tcgen05.st.sync.aligned.16x256b.x8.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_frag4(uint32_t taddr, const uint32_t *v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
-// 16 lanes x 16 columns: register 2 n + e is TMEM lane g + 8 e, column 4 n + t.
+// 16 lanes x 32 columns: register 2 n + e is TMEM lane g + 8 e, column 4 n + t.
 __device__ __forceinline__ void tmem_st_half_frag(uint32_t taddr, const uint32_t *v) {
   asm volatile(
-      "tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -281,9 +287,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
   auto p_full = [&](int w, int c) { return bar0 + 8u * (14 + 2 * w + c); };  // keys 64 c .. + 63
   auto o_full = [&](int w) { return bar0 + 8u * (18 + w); };
   auto a_done = [&](int w) { return bar0 + 8u * (20 + w); };  // products of a tile's first 64 keys
-  auto sc_full = [&](int i) { return bar0 + 8u * (22 + i); };
-  auto piece_full = [&](int i) { return bar0 + 8u * (22 + PL::SLOTS + i); };
-  auto piece_empty = [&](int i) { return bar0 + 8u * (22 + PL::SLOTS + kRing + i); };
+  auto pair = [&](int i) { return bar0 + 8u * (22 + i); };   // the two softmax warps of 32 rows
+  auto sc_full = [&](int i) { return bar0 + 8u * (30 + i); };
+  auto piece_full = [&](int i) { return bar0 + 8u * (30 + PL::SLOTS + i); };
+  auto piece_empty = [&](int i) { return bar0 + 8u * (30 + PL::SLOTS + kRing + i); };
   const uint32_t drain = bar0 + 8u * (PL::BARS - 1);
   Piece *pieces = reinterpret_cast<Piece *>(sm + PL::OFF_PIECE);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + PL::OFF_MISC);
@@ -297,21 +304,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
       mbar_init(v_full(i), 4);
       mbar_init(v_empty(i), 1);
       mbar_init(s_full(i), 1);
-      mbar_init(p_full(i, 0), 4);
-      mbar_init(p_full(i, 1), 4);
+      mbar_init(p_full(i, 0), kSoftWarps / 2);
+      mbar_init(p_full(i, 1), kSoftWarps / 2);
       mbar_init(o_full(i), 1);
       mbar_init(a_done(i), 1);
     }
+    for (int i = 0; i < 8; ++i) mbar_init(pair(i), 2);
     for (int i = 0; i < PL::SLOTS; ++i) mbar_init(sc_full(i), 4);
     for (int i = 0; i < kRing; ++i) {
       mbar_init(piece_full(i), 1);
-      mbar_init(piece_empty(i), 8 + 4 + 1 + 2);  // softmax, converter, MMA and Q warps
+      mbar_init(piece_empty(i), kSoftWarps + 4 + 1 + 2);  // softmax, converter, MMA and Q warps
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 12) {
+  if (warp == kSoftWarps + 4) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot)));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
@@ -345,20 +353,31 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
   };
   Reader reader;
 
-  // Registers: 2 * 160 + 104 + 88 = 4 * 128, the launch's share
-  if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
+  // Registers per warpgroup: 4 * 88 + 72 + 56 = 6 * 80, the launch's share (launch_t
+  // checks that the kernel was built with 80)
+  if (warp < kSoftWarps) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
     // ------------------------------------------------------------ softmax ----
-    // Scores come as fragments: a thread (lane 4 g + t) holds rows g + 8 y of its
-    // warp's 32 (y = 0 .. 3) and two of every 8 columns, so a token's scales,
-    // read from shared memory, serve four rows.  (One row a thread needs 96
-    // 16-byte broadcasts per row and tile, more than the 2048 cycles of MMAs.)
-    const int w = warp >> 2, g = lane >> 2, t = lane & 3;
-    const int r0 = w * 128 + (warp & 3) * 32;  // the warp's first row
-    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    // Scores come as fragments: a thread (lane 4 g + t) holds rows g and g + 8 of
+    // its warp's 16 and two of every 8 columns, so a token's scales, read from
+    // shared memory, serve two rows.  (One row a thread needs 96 16-byte
+    // broadcasts per row and tile, more than the 2048 cycles of MMAs; four rows a
+    // thread leave two warps a scheduler, too few to cover the latencies: a
+    // prompt of 4516 tokens took 426 us.)
+    const int w = warp >> 3, quad = warp & 3, sub = (warp >> 2) & 1, g = lane >> 2, t = lane & 3;
+    const int r0 = w * 128 + quad * 32 + sub * 16;  // the warp's first row
+    const uint32_t quad_lanes = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t lanes = quad_lanes + (static_cast<uint32_t>(sub * 16) << 16);
     const uint32_t col_s = lanes + PL::COL_S + 128 * w, col_o = lanes + PL::COL_O + 128 * w;
-    constexpr uint32_t kLane16 = 16u << 16;
-    uint32_t s_phase = 0, o_phase = 0;
+    float2 *stat = reinterpret_cast<float2 *>(sm + PL::OFF_STAT);
+    uint32_t s_phase = 0, o_phase = 0, pair_phase = 0;
+    auto meet = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(pair(4 * w + quad));
+      const bool met = wait(pair(4 * w + quad), pair_phase);
+      pair_phase ^= 1u;
+      return met;
+    };
     uint32_t tiles = 0;  // so far
     bool ok = true;
     while (ok && wait(piece_full(reader.i), reader.phase)) {
@@ -378,9 +397,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
         if (r < x.R) visible(p, x.len - x.nq + (x.qt * kRows + r) / p.group, x.len, lo, hi);
       };
       int lo_max = 0, hi_min = 0x7fffffff;
-      float m[4], l[4][2];
+      float m[2], l[2][2];
 #pragma unroll
-      for (int y = 0; y < 4; ++y) {
+      for (int y = 0; y < 2; ++y) {
         int lo, hi;
         limits(y, lo, hi);
         lo_max = max(lo_max, lo);
@@ -403,25 +422,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
         // the others are being made (and half the registers do)
 #pragma unroll 1
         for (int c = 0; c < 2; ++c, sc += kKeys / 4) {
-          // u[32 z + 4 n + 2 f + e]: row y = 2 z + f, column 64 c + 8 n + 2 t + e
-          uint32_t s[64];
+          // u[4 n + 2 y + e]: row y, column 64 c + 8 n + 2 t + e
+          uint32_t s[32];
           tmem_ld_frag(col_s + 64 * c, s);
-          tmem_ld_frag(col_s + 64 * c + kLane16, s + 32);
-          tmem_wait_ld<64>(s);
+          tmem_wait_ld<32>(s);
           float *u = reinterpret_cast<float *>(s);
 #pragma unroll
           for (int n = 0; n < 8; ++n) {
             const float2 k = sc[4 * n], z = sc[kKeys / 2 + 4 * n];
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              float *d = u + 32 * (y >> 1) + 4 * n + 2 * (y & 1);
-              fma2(d[0], d[1], d[0], d[1], k.x, k.y, z.x, z.y);
-            }
+            fma2(u[4 * n], u[4 * n + 1], u[4 * n], u[4 * n + 1], k.x, k.y, z.x, z.y);
+            fma2(u[4 * n + 2], u[4 * n + 3], u[4 * n + 2], u[4 * n + 3], k.x, k.y, z.x, z.y);
           }
           const int jc = j + 64 * c;
           if (__any_sync(0xffffffffu, lo_max > jc || hi_min < jc + 64)) {
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
+            for (int y = 0; y < 2; ++y) {
               int lo, hi;
               limits(y, lo, hi);
               lo -= jc + 2 * t;
@@ -430,23 +445,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
               for (int n = 0; n < 8; ++n)
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
-                  if (8 * n + e < lo || 8 * n + e >= hi) u[32 * (y >> 1) + 4 * n + 2 * (y & 1) + e] = -CUDART_INF_F;
+                  if (8 * n + e < lo || 8 * n + e >= hi) u[4 * n + 2 * y + e] = -CUDART_INF_F;
             }
           }
-          bool over = false;
-          float top[4];
+          float top[2];
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const float *d = u + 32 * (y >> 1) + 2 * (y & 1);
+          for (int y = 0; y < 2; ++y) {
+            const float *d = u + 2 * y;
             top[y] = fmaxf(d[0], d[1]);
 #pragma unroll
             for (int n = 1; n < 8; ++n) top[y] = max3(top[y], d[4 * n], d[4 * n + 1]);
-            over |= top[y] > m[y] + kRoom;
           }
-          if (__any_sync(0xffffffffu, over)) {
-            float a[4];
+          if (__any_sync(0xffffffffu, top[0] > m[0] + kRoom || top[1] > m[1] + kRoom)) {
+            float a[2];
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
+            for (int y = 0; y < 2; ++y) {
               top[y] = fmaxf(top[y], __shfl_xor_sync(0xffffffffu, top[y], 1));
               top[y] = fmaxf(top[y], __shfl_xor_sync(0xffffffffu, top[y], 2));
               const float nm = top[y] > m[y] + kRoom ? top[y] - kHead : m[y];
@@ -460,40 +473,34 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
             if (c == 1) ok = ok && wait(a_done(w), s_phase ^ 1u);
             if (!fresh || c == 1) {
               tc_fence_after();
+#pragma unroll 1
+              for (int q = 0; q < D / 32; ++q) {
+                uint32_t v[16];
+                tmem_ld_frag4(col_o + 32 * q, v);
+                tmem_wait_ld<16>(v);
 #pragma unroll
-              for (int q = 0; q < D / 64; ++q)
-#pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                  uint32_t v[32];
-                  tmem_ld_frag(col_o + 64 * q + z * kLane16, v);
-                  tmem_wait_ld<32>(v);
-#pragma unroll
-                  for (int e = 0; e < 32; ++e)
-                    v[e] = __float_as_uint(__uint_as_float(v[e]) * a[2 * z + ((e >> 1) & 1)]);
-                  tmem_st_frag(col_o + 64 * q + z * kLane16, v);
-                }
+                for (int e = 0; e < 16; ++e)
+                  v[e] = __float_as_uint(__uint_as_float(v[e]) * a[(e >> 1) & 1]);
+                tmem_st_frag4(col_o + 32 * q, v);
+              }
             }
           }
           // 8 scores become 4 columns of fp16 pairs
+          uint32_t v[16];
 #pragma unroll
-          for (int n0 = 0; n0 < 8; n0 += 4) {
-            uint32_t v[16];
+          for (int n = 0; n < 8; ++n) {
+            const float2 rv = sc[kKeys + 4 * n];
 #pragma unroll
-            for (int n = n0; n < n0 + 4; ++n) {
-              const float2 rv = sc[kKeys + 4 * n];
-#pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                float *d = u + 32 * (y >> 1) + 4 * n + 2 * (y & 1);
-                add2(d[0], d[1], d[0], d[1], -m[y]);
-                const float w0 = exp2_fast(d[0]), w1 = exp2_fast(d[1]);
-                fma2(l[y][0], l[y][1], w0, w1, rv.x, rv.y, l[y][0], l[y][1]);
-                const __half2 h = __floats2half2_rn(w0, w1);
-                v[8 * (y >> 1) + 2 * (n - n0) + (y & 1)] = *reinterpret_cast<const uint32_t *>(&h);
-              }
+            for (int y = 0; y < 2; ++y) {
+              float *d = u + 4 * n + 2 * y;
+              add2(d[0], d[1], d[0], d[1], -m[y]);
+              const float w0 = exp2_fast(d[0]), w1 = exp2_fast(d[1]);
+              fma2(l[y][0], l[y][1], w0, w1, rv.x, rv.y, l[y][0], l[y][1]);
+              const __half2 h = __floats2half2_rn(w0, w1);
+              v[2 * n + y] = *reinterpret_cast<const uint32_t *>(&h);
             }
-            tmem_st_half_frag(col_s + 32 * c + 4 * n0, v);
-            tmem_st_half_frag(col_s + 32 * c + 4 * n0 + kLane16, v + 8);
           }
+          tmem_st_half_frag(col_s + 32 * c, v);
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
@@ -502,34 +509,33 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
         fresh = false;
       }
       if (!ok) break;
-      // -- the item's (or piece's) end: a thread takes the row of its lane
-      float sum = 0.f, ref = 0.f;
+      // -- the item's (or piece's) end: the two warps of 32 rows exchange their
+      // rows' references and sums, and write half of the columns of all 32 each, a
+      // thread the row of its lane
 #pragma unroll
-      for (int y = 0; y < 4; ++y) {
+      for (int y = 0; y < 2; ++y) {
         float z = l[y][0] + l[y][1];
         z += __shfl_xor_sync(0xffffffffu, z, 1);
         z += __shfl_xor_sync(0xffffffffu, z, 2);
-        const float a = __shfl_sync(0xffffffffu, z, 4 * (lane & 7));
-        const float c = __shfl_sync(0xffffffffu, m[y], 4 * (lane & 7));
-        if (lane >> 3 == y) {
-          sum = a;
-          ref = c;
-        }
+        if (t == 0) stat[r0 + 8 * y + g] = make_float2(m[y], z);
       }
+      ok = meet();
+      if (!ok) break;
+      const int r = w * 128 + quad * 32 + lane, ri = x.qt * kRows + r;
+      const float ref = stat[r].x, sum = stat[r].y;
       ok = wait(o_full(w), o_phase);
       if (!ok) break;
       o_phase ^= 1u;
       tc_fence_after();
-      const int r = r0 + lane, ri = x.qt * kRows + r;
       const bool whole = x.t0 == 0 && x.t1 == x.nt;
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
       const long long row = (static_cast<long long>(x.q0) + ri / p.group) * p.Hq + x.h * p.group + ri % p.group;
       const long long part = static_cast<long long>(blockIdx.x) * 2 + (x.t0 == 0 ? 1 : 0);
       float *dst = parts + part * kRows * (D + 2) + r * D;
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
+#pragma unroll 1
+      for (int c = sub * (D / 64); c < (sub + 1) * (D / 64); ++c) {
         uint32_t v[32];
-        tmem_ld32(col_o + 32 * c, v);
+        tmem_ld32(quad_lanes + PL::COL_O + 128 * w + 32 * c, v);
         tmem_wait_ld32(v);
         if (r < x.R) {
 #pragma unroll
@@ -557,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
           }
         }
       }
-      if (r < x.R) {
+      if (sub == 0 && r < x.R) {
         if (!whole) {
           float *ml = parts + part * kRows * (D + 2) + kRows * D + 2 * r;
           ml[0] = ref;
@@ -568,16 +574,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
       }
       if (!whole && x.t0 == 0 && threadIdx.x == 0) descs[blockIdx.x] = Desc{x.b, x.h, x.qt, x.last};
       tc_fence_before();
+      // both have read the exchange (and TMEM) before either goes on
+      ok = meet();
       done_piece(reader);
     }
-  } else if (warp < 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+  } else if (warp < kSoftWarps + 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     // --------------------------------------------------------- converters ----
     // The scales have a third slot: a tile's are read until both halves' weights
     // are written, and slot s is refilled for tile i + 3 only once the K stage
     // of tile i + 1 is free, whose scores are issued after those weights.
     constexpr int ROW = D * BITS / 8, NV = ROW / 16;  // 16-byte vectors of a token
-    const int tok = (warp - 8) * 32 + lane;
+    const int tok = (warp - kSoftWarps) * 32 + lane;
     const Nibbles nib;
     int st = 0, slot = 0;
     uint32_t phase = 1;  // the first wait on an empty stage passes
@@ -652,8 +660,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
       }
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    if (warp == 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == kSoftWarps + 4) {
       // ------------------------------------------------------------- MMAs ----
       const uint32_t on = elect();
       int ks = 0, vs = 0;  // stages, and their phases
@@ -759,9 +767,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
       commit_if(on, drain);
       wait_bar_teardown(drain, 0);
       __syncwarp();
-    } else if (warp < 15) {
+    } else if (warp < kSoftWarps + 7) {
       // ---------------------------------------------------------- Q rows ----
-      const int w = warp - 13;
+      const int w = warp - (kSoftWarps + 5);
       uint32_t phase = 1;
       Piece x;
       while (next_piece(reader, x)) {
@@ -850,7 +858,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 12)
+  if (warp == kSoftWarps + 4)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
@@ -905,6 +913,10 @@ bool allow_smem() {
   if (!done[dev])
     done[dev] = cudaFuncSetAttribute(kv_prefill_kernel<BITS, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      Plan<D>::SMEM) == cudaSuccess;
+  // the warpgroups' register shares add up to what a launch with 80 brings
+  cudaFuncAttributes a;
+  if (done[dev] && (cudaFuncGetAttributes(&a, kv_prefill_kernel<BITS, D>) != cudaSuccess || a.numRegs != 80))
+    done[dev] = false;
   return done[dev];
 }
 
