@@ -51,7 +51,7 @@ constexpr int kSoftWarps = 16, kWarps = kSoftWarps + 8, kThreads = 32 * kWarps;
 constexpr int kRows = 256;  // of an item
 constexpr int kKeys = 128;  // of a tile
 constexpr int kRing = 4;    // published pieces
-constexpr int kItemCost = 2;  // of an item beyond its tiles, in tiles: its start and end
+constexpr int kItemCost = 3;  // of an item beyond its tiles, in tiles: its start and end
 
 // A piece of an item: its tiles t0 .. t1 - 1 of nt.
 struct Piece {
@@ -74,10 +74,9 @@ struct Plan {
   static constexpr int OFF_Q = 0, OFF_K = 2 * TILE, OFF_V = 4 * TILE, OFF_S = 6 * TILE;
   static constexpr int SLOTS = 3;                      // of token scales (see the converters)
   static constexpr int OFF_BAR = OFF_S + SLOTS * 3 * kKeys * 4;
-  static constexpr int BARS = 30 + SLOTS + 2 * kRing + 1;
+  static constexpr int BARS = 22 + SLOTS + 2 * kRing + 1;
   static constexpr int OFF_PIECE = OFF_BAR + BARS * 8;
-  static constexpr int OFF_STAT = OFF_PIECE + kRing * static_cast<int>(sizeof(Piece));  // M, l of the rows
-  static constexpr int OFF_MISC = OFF_STAT + kRows * 8;
+  static constexpr int OFF_MISC = OFF_PIECE + kRing * static_cast<int>(sizeof(Piece));
   static constexpr int SMEM = OFF_MISC + 16 + 1024;    // 1024: aligned by hand
   static constexpr uint32_t COL_S = 0, COL_O = 256;    // S_w at 128 w, O_w at 256 + 128 w
 };
@@ -319,10 +318,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
   auto p_full = [&](int w, int c) { return bar0 + 8u * (14 + 2 * w + c); };  // keys 64 c .. + 63
   auto o_full = [&](int w) { return bar0 + 8u * (18 + w); };
   auto a_done = [&](int w) { return bar0 + 8u * (20 + w); };  // products of a tile's first 64 keys
-  auto pair = [&](int i) { return bar0 + 8u * (22 + i); };   // the two softmax warps of 32 rows
-  auto sc_full = [&](int i) { return bar0 + 8u * (30 + i); };
-  auto piece_full = [&](int i) { return bar0 + 8u * (30 + PL::SLOTS + i); };
-  auto piece_empty = [&](int i) { return bar0 + 8u * (30 + PL::SLOTS + kRing + i); };
+  auto sc_full = [&](int i) { return bar0 + 8u * (22 + i); };
+  auto piece_full = [&](int i) { return bar0 + 8u * (22 + PL::SLOTS + i); };
+  auto piece_empty = [&](int i) { return bar0 + 8u * (22 + PL::SLOTS + kRing + i); };
   const uint32_t drain = bar0 + 8u * (PL::BARS - 1);
   Piece *pieces = reinterpret_cast<Piece *>(sm + PL::OFF_PIECE);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + PL::OFF_MISC);
@@ -341,7 +339,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
       mbar_init(o_full(i), 1);
       mbar_init(a_done(i), 1);
     }
-    for (int i = 0; i < 8; ++i) mbar_init(pair(i), 2);
     for (int i = 0; i < PL::SLOTS; ++i) mbar_init(sc_full(i), 4);
     for (int i = 0; i < kRing; ++i) {
       mbar_init(piece_full(i), 1);
@@ -397,18 +394,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
     // prompt of 4516 tokens took 426 us.)
     const int w = warp >> 3, quad = warp & 3, sub = (warp >> 2) & 1, g = lane >> 2, t = lane & 3;
     const int r0 = w * 128 + quad * 32 + sub * 16;  // the warp's first row
-    const uint32_t quad_lanes = static_cast<uint32_t>(quad * 32) << 16;
-    const uint32_t lanes = quad_lanes + (static_cast<uint32_t>(sub * 16) << 16);
+    const uint32_t lanes = static_cast<uint32_t>(quad * 32 + sub * 16) << 16;
     const uint32_t col_s = lanes + PL::COL_S + 128 * w, col_o = lanes + PL::COL_O + 128 * w;
-    float2 *stat = reinterpret_cast<float2 *>(sm + PL::OFF_STAT);
-    uint32_t s_phase = 0, o_phase = 0, pair_phase = 0;
-    auto meet = [&]() {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(pair(4 * w + quad));
-      const bool met = wait(pair(4 * w + quad), pair_phase);
-      pair_phase ^= 1u;
-      return met;
-    };
+    uint32_t s_phase = 0, o_phase = 0;
     uint32_t tiles = 0;  // so far
     bool ok = true;
     while (ok && wait(piece_full(reader.i), reader.phase)) {
@@ -540,73 +528,79 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
         fresh = false;
       }
       if (!ok) break;
-      // -- the item's (or piece's) end: the two warps of 32 rows exchange their
-      // rows' references and sums, and write half of the columns of all 32 each, a
-      // thread the row of its lane
+      // -- the item's (or piece's) end
+      float inv[2], sum[2];
+      long long row[2];  // of the output; -1: past the item's rows
+      const bool whole = x.t0 == 0 && x.t1 == x.nt;
+      const long long part = static_cast<long long>(blockIdx.x) * 2 + (x.t0 == 0 ? 1 : 0);
+      float *part_at = parts + part * kRows * (D + 2);
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         float z = l[y][0] + l[y][1];
         z += __shfl_xor_sync(0xffffffffu, z, 1);
         z += __shfl_xor_sync(0xffffffffu, z, 2);
-        if (t == 0) stat[r0 + 8 * y + g] = make_float2(m[y], z);
+        sum[y] = z;
+        inv[y] = z == 0.f ? 0.f : 1.f / z;
+        const int r = r0 + 8 * y + g, ri = x.qt * kRows + r;
+        row[y] = r < x.R ? (static_cast<long long>(x.q0) + ri / p.group) * p.Hq + x.h * p.group + ri % p.group : -1;
+        if (t == 0 && r < x.R) {
+          if (!whole)
+            *reinterpret_cast<float2 *>(part_at + kRows * D + 2 * r) = make_float2(m[y], z);
+          else if (p.lse != nullptr)
+            p.lse[row[y]] = z == 0.f ? -CUDART_INF_F : (m[y] + log2f(z)) * kLn2;
+        }
       }
-      ok = meet();
-      if (!ok) break;
-      const int r = w * 128 + quad * 32 + lane, ri = x.qt * kRows + r;
-      const float ref = stat[r].x, sum = stat[r].y;
+      if (!whole && x.t0 == 0 && threadIdx.x == 0) descs[blockIdx.x] = Desc{x.b, x.h, x.qt, x.last};
       ok = wait(o_full(w), o_phase);
       if (!ok) break;
       o_phase ^= 1u;
       tc_fence_after();
-      const bool whole = x.t0 == 0 && x.t1 == x.nt;
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      const long long row = (static_cast<long long>(x.q0) + ri / p.group) * p.Hq + x.h * p.group + ri % p.group;
-      const long long part = static_cast<long long>(blockIdx.x) * 2 + (x.t0 == 0 ? 1 : 0);
-      float *dst = parts + part * kRows * (D + 2) + r * D;
 #pragma unroll 1
-      for (int c = sub * (D / 64); c < (sub + 1) * (D / 64); ++c) {
-        uint32_t v[32];
-        tmem_ld32(quad_lanes + PL::COL_O + 128 * w + 32 * c, v);
-        tmem_wait_ld32(v);
-        if (r < x.R) {
+      for (int q = 0; q < D / 32; ++q) {
+        // v[4 n + 2 y + e]: row y, column 32 q + 8 n + 2 t + e
+        uint32_t v[16];
+        tmem_ld_frag4(col_o + 32 * q, v);
+        tmem_wait_ld<16>(v);
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            // columns e .. e + 7 are d 0, 4, 1, 5, 2, 6, 3, 7 of an 8 at 4 bits
-            float y[8];
+        for (int y = 0; y < 2; ++y) {
+          if (!whole) {
+            // columns stay as they are (the join knows their order): a row's 32 bytes
+            // from four lanes
+            float *dst = part_at + (r0 + 8 * y + g) * D + 32 * q + 2 * t;
+            if (row[y] >= 0) {
 #pragma unroll
-            for (int z = 0; z < 8; ++z) {
-              const int from = BITS == 4 ? (z & 3) * 2 + (z >> 2) : z;
-              y[z] = __uint_as_float(v[e + from]);
+              for (int n = 0; n < 4; ++n)
+                *reinterpret_cast<float2 *>(dst + 8 * n) =
+                    make_float2(__uint_as_float(v[4 * n + 2 * y]), __uint_as_float(v[4 * n + 2 * y + 1]));
             }
-            if (whole) {
-              uint4 o;
-              const __half2 h0 = __floats2half2_rn(y[0] * inv, y[1] * inv), h1 = __floats2half2_rn(y[2] * inv, y[3] * inv);
-              const __half2 h2 = __floats2half2_rn(y[4] * inv, y[5] * inv), h3 = __floats2half2_rn(y[6] * inv, y[7] * inv);
-              o.x = *reinterpret_cast<const uint32_t *>(&h0);
-              o.y = *reinterpret_cast<const uint32_t *>(&h1);
-              o.z = *reinterpret_cast<const uint32_t *>(&h2);
-              o.w = *reinterpret_cast<const uint32_t *>(&h3);
-              *reinterpret_cast<uint4 *>(p.out + row * D + 32 * c + e) = o;
-            } else {
-              *reinterpret_cast<float4 *>(dst + 32 * c + e) = make_float4(y[0], y[1], y[2], y[3]);
-              *reinterpret_cast<float4 *>(dst + 32 * c + e + 4) = make_float4(y[4], y[5], y[6], y[7]);
+          } else {
+            // the four lanes of a row exchange pairs, so that lane t has the 8 columns
+            // of n = t: 64 contiguous bytes a row
+            uint32_t h[4], o[4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+              const __half2 z = __floats2half2_rn(__uint_as_float(v[4 * n + 2 * y]) * inv[y],
+                                                  __uint_as_float(v[4 * n + 2 * y + 1]) * inv[y]);
+              h[n] = *reinterpret_cast<const uint32_t *>(&z);
             }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int n = t ^ k;  // what lane t ^ k is to have
+              const uint32_t z = n & 2 ? (n & 1 ? h[3] : h[2]) : (n & 1 ? h[1] : h[0]);
+              const uint32_t got = k ? __shfl_xor_sync(0xffffffffu, z, k) : z;
+#pragma unroll
+              for (int s = 0; s < 4; ++s)
+                if (s == n) o[s] = got;  // lane s's pair of columns 2 s, 2 s + 1
+            }
+            uint4 z = make_uint4(o[0], o[1], o[2], o[3]);
+            if (BITS == 4)  // columns 2 s, 2 s + 1 are d = s and s + 4
+              z = make_uint4(__byte_perm(o[0], o[1], 0x5410), __byte_perm(o[2], o[3], 0x5410),
+                             __byte_perm(o[0], o[1], 0x7632), __byte_perm(o[2], o[3], 0x7632));
+            if (row[y] >= 0) *reinterpret_cast<uint4 *>(p.out + row[y] * D + 32 * q + 8 * t) = z;
           }
         }
       }
-      if (sub == 0 && r < x.R) {
-        if (!whole) {
-          float *ml = parts + part * kRows * (D + 2) + kRows * D + 2 * r;
-          ml[0] = ref;
-          ml[1] = sum;
-        } else if (p.lse != nullptr) {
-          p.lse[row] = sum == 0.f ? -CUDART_INF_F : (ref + log2f(sum)) * kLn2;
-        }
-      }
-      if (!whole && x.t0 == 0 && threadIdx.x == 0) descs[blockIdx.x] = Desc{x.b, x.h, x.qt, x.last};
       tc_fence_before();
-      // both have read the exchange (and TMEM) before either goes on
-      ok = meet();
       done_piece(reader);
     }
   } else if (warp < kSoftWarps + 4) {
@@ -895,7 +889,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
 
 // Joins the partials of the items cut by the ranges: block (c, y) takes rows 32 y
 // .. + 31 of the item that starts in range c and ends in a later one, a warp a row.
-template <int D>
+template <int BITS, int D>
 __global__ void __launch_bounds__(256) kv_prefill_join_kernel(const KvAttnParams p, int ranges) {
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -930,6 +924,14 @@ __global__ void __launch_bounds__(256) kv_prefill_join_kernel(const KvAttnParams
       }
     }
     const long long row = (static_cast<long long>(q0) + ri / p.group) * p.Hq + de.h * p.group + ri % p.group;
+    if (BITS == 4) {
+      // columns 0 .. 7 of an 8 are d = 0, 4, 1, 5, 2, 6, 3, 7: the lane of the first four
+      // gives d 4, 5 for d 2, 3
+      const bool odd = lane & 1;
+      const float a = __shfl_xor_sync(0xffffffffu, odd ? o.x : o.y, 1);
+      const float b = __shfl_xor_sync(0xffffffffu, odd ? o.z : o.w, 1);
+      o = odd ? make_float4(a, b, o.y, o.w) : make_float4(o.x, o.z, a, b);
+    }
     if (lane * 4 < D) store_row4<D>(p, row, lane * 4, o, m, l);
   }
 }
@@ -979,7 +981,7 @@ int launch_t(const KvAttnParams &p, cudaStream_t s) {
     cfg.gridDim = dim3(static_cast<unsigned>(grid), kRows / 32);
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
-    if (cudaLaunchKernelEx(&cfg, kv_prefill_join_kernel<D>, p, grid) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, kv_prefill_join_kernel<BITS, D>, p, grid) != cudaSuccess) {
       cudaGetLastError();
       return W8A8_ERR_CUDA;
     }
