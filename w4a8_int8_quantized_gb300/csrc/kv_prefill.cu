@@ -720,24 +720,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
         if (ks == 0) kph ^= 1u;
       };
       Piece x;
+      // the first scores of a piece
+      auto start = [&](const Piece &z) {
+        if (!open_k()) return false;
+        for (int w = 0; w < 2 && z.R > 128 * w; ++w) {
+          if (!wait(q_full(w), qph[w])) return false;
+          qph[w] ^= 1u;
+          scores(w);
+          if (z.t1 - z.t0 == 1) commit_if(on, q_empty(w));
+        }
+        close_k();
+        return true;
+      };
       bool ok = true, have = next_piece(reader, x);
-      if (have) {
-        ok = wait(q_full(0), qph[0]) && open_k();
-        qph[0] ^= 1u;
-        if (ok) scores(0);
-        if (ok && x.R > 128) {
-          ok = wait(q_full(1), qph[1]);
-          qph[1] ^= 1u;
-          if (ok) scores(1);
-        }
-        if (ok) {
-          if (x.t1 - x.t0 == 1) {
-            commit_if(on, q_empty(0));
-            if (x.R > 128) commit_if(on, q_empty(1));
-          }
-          close_k();
-        }
-      }
+      if (have) ok = start(x);
       while (ok && have) {
         Piece y;
         bool more = false;
@@ -745,45 +741,48 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
           const bool last = i + 1 == x.t1;
           if (last) {
             more = next_piece(reader, y);
-            ok = *abort_flag == 0;
+            ok = !__any_sync(0xffffffffu, *abort_flag != 0);
             if (!ok) break;
           }
-          const int R2 = last ? (more ? y.R : 0) : x.R;  // rows of the next tile's item
           ok = wait(v_full(vs), vph);
           if (!ok) break;
-          bool opened = false;
-#pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            if (x.R > 128 * w) {
-              ok = ok && wait(p_full(w, 0), pph[w]);
-              if (!ok) break;
-              values(w, 0, i == x.t0);
-              commit_if(on, a_done(w));
-              ok = wait(p_full(w, 1), pph[w]);
-              pph[w] ^= 1u;
-              if (!ok) break;
-              values(w, 1, false);
-              if (last) commit_if(on, o_full(w));
+          auto finish = [&](int w) {  // O_w += P_w V of tile i
+            if (x.R <= 128 * w) return true;
+            if (!wait(p_full(w, 0), pph[w])) return false;
+            values(w, 0, i == x.t0);
+            commit_if(on, a_done(w));
+            if (!wait(p_full(w, 1), pph[w])) return false;
+            pph[w] ^= 1u;
+            values(w, 1, false);
+            if (last) commit_if(on, o_full(w));
+            return true;
+          };
+          if (!last) {
+            ok = finish(0) && open_k();
+            if (!ok) break;
+            scores(0);
+            // the item's last scores: its Q rows may be replaced
+            if (i + 2 == x.t1) commit_if(on, q_empty(0));
+            ok = finish(1);
+            if (!ok) break;
+            commit_if(on, v_empty(vs));
+            if (x.R > 128) {
+              scores(1);
+              if (i + 2 == x.t1) commit_if(on, q_empty(1));
             }
-            if (R2 > 128 * w) {
-              if (last) {
-                ok = wait(q_full(w), qph[w]);
-                qph[w] ^= 1u;
-              }
-              if (ok && !opened) ok = open_k();
-              opened = true;
+            close_k();
+          } else {
+            // nothing of this item waits for the next one's rows
+            ok = finish(0) && finish(1);
+            if (!ok) break;
+            commit_if(on, v_empty(vs));
+            if (more) {
+              ok = start(y);
               if (!ok) break;
-              scores(w);
-              // the item's last scores: its Q rows may be replaced
-              const bool q_done = last ? y.t1 - y.t0 == 1 : i + 2 == x.t1;
-              if (q_done) commit_if(on, q_empty(w));
             }
           }
-          if (!ok) break;
-          commit_if(on, v_empty(vs));
           vs ^= 1;
           if (vs == 0) vph ^= 1u;
-          if (opened) close_k();
         }
         x = y;
         have = more;
@@ -801,29 +800,30 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
         if (x.R <= w * 128) continue;
         if (!wait(q_empty(w), phase)) break;
         phase ^= 1u;
+        // all rows in flight at once (by way of registers it took 8 round trips);
         // rows beyond the item's are zero; a lane takes chunk lane % (D / 8) of every row
         constexpr int C = D / 8, RPS = 32 / C;  // rows per step of the warp
         const int c = lane % C;
         const uint32_t dst = base + PL::OFF_Q + w * PL::TILE;
-        for (int r0 = 0; r0 < 128; r0 += 8 * RPS) {
-          uint4 v[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int rr = r0 + e * RPS + lane / C, ri = x.qt * kRows + w * 128 + rr;
-            v[e] = make_uint4(0, 0, 0, 0);
-            if (w * 128 + rr < x.R)
-              v[e] = __ldg(reinterpret_cast<const uint4 *>(
-                  p.q + (x.q0 + ri / p.group) * p.q_ts +
-                  static_cast<long long>(x.h * p.group + ri % p.group) * p.q_hs + 8 * c));
-          }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int rr = r0 + e * RPS + lane / C;
-            uint4 o = v[e];
-            if (BITS == 4)  // d in the order 0, 4, 1, 5, 2, 6, 3, 7
-              o = make_uint4(__byte_perm(v[e].x, v[e].z, 0x5410), __byte_perm(v[e].x, v[e].z, 0x7632),
-                             __byte_perm(v[e].y, v[e].w, 0x5410), __byte_perm(v[e].y, v[e].w, 0x7632));
-            sts4(dst + chunk_at(rr, c), o);
+#pragma unroll 4
+        for (int rr = lane / C; rr < 128; rr += RPS) {
+          const bool in = w * 128 + rr < x.R;
+          const int ri = x.qt * kRows + (in ? w * 128 + rr : 0);
+          const __half *src = p.q + (x.q0 + ri / p.group) * p.q_ts +
+                              static_cast<long long>(x.h * p.group + ri % p.group) * p.q_hs + 8 * c;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + chunk_at(rr, c)), "l"(src),
+                       "r"(in ? 16 : 0)
+                       : "memory");
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        if (BITS == 4) {  // this lane's own chunks, d in the order 0, 4, 1, 5, 2, 6, 3, 7
+#pragma unroll 4
+          for (int rr = lane / C; rr < 128; rr += RPS) {
+            const uint32_t a = dst + chunk_at(rr, c);
+            uint4 v;
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+            sts4(a, make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
+                               __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632)));
           }
         }
         fence_proxy_async();
