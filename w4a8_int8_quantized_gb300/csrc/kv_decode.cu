@@ -70,7 +70,10 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
 template <int BITS, int D, int NT>
 struct Plan {
   static constexpr int ROW = D * BITS / 8;           // bytes of a token's codes
-  static constexpr int MT = 16 / BITS * 64 / D;      // 16-token tiles per step: 2 KB of K
+  // 16-token tiles per step: 4 KB of K (2 KB for two column tiles, whose sums
+  // take the registers; 64 tokens at most).  Half as much cost a tenth more time
+  // (64 sequences of 512..8192 tokens: 87 us against 81): the step's fixed work.
+  static constexpr int MT = NT == 2 ? 16 / BITS * 64 / D : BITS == 4 && D == 64 ? 4 : 32 / BITS * 64 / D;
   static constexpr int STEP = 16 * MT;               // tokens of a warp's step
   static constexpr int UNIT = kWarps * STEP;         // tokens of a block's step
   static constexpr int KW = ROW / 16;                // K words per token and lane
@@ -78,22 +81,25 @@ struct Plan {
   static constexpr int MMAS = D / 16;                // 16-row tiles of D
   static constexpr int COLS = 8 * NT;  // rows of an item
   static constexpr int PAD = D + 4;                  // floats of a staged row
-  static constexpr int BLOCKS = NT == 1 ? 4 : 3;     // resident per SM
+  static constexpr int BLOCKS = 3;                   // resident per SM
   // a stage of a warp's ring: one step's K codes, V codes, K scales, V scales
   static constexpr int OFF_V = STEP * ROW, OFF_KS = 2 * STEP * ROW, OFF_VS = OFF_KS + STEP * 4;
   static constexpr int STAGE = OFF_VS + STEP * 4;
   static constexpr int TILE_BYTES = 2 * 16 * ROW + 2 * 16 * 4;  // of one 16-token tile
-  static constexpr int STAGES = BLOCKS == 4 ? 3 : 4;
+  static constexpr int STAGES = NT == 2 ? 4 : 2;
   static constexpr int RING = kWarps * STAGES * STAGE;
   static constexpr int JOIN = kWarps * COLS * PAD * 4;  // the warps' results, over the drained ring
-  static constexpr int SMEM = (RING > JOIN ? RING : JOIN) + kWarps * STAGES * 8;
+  static constexpr int OFF_SCALES = RING > JOIN ? RING : JOIN;  // a warp's step: 16 bytes a token
+  static constexpr int OFF_BAR = OFF_SCALES + kWarps * STEP * 16;
+  static constexpr int SMEM = OFF_BAR + kWarps * STAGES * 8;
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
-// Waits for a phase of an mbarrier; false if it gave up after about 2 s.
+// Waits for a phase of an mbarrier, the whole warp together; false if it gave up
+// after about 2 s.
 __device__ __forceinline__ bool wait_stage(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   long long t0 = 0;
@@ -101,13 +107,14 @@ __device__ __forceinline__ bool wait_stage(uint32_t bar, uint32_t parity) {
     asm volatile(
         "{\n.reg .pred p;\n"
         "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        "vote.sync.all.pred p, p, 0xffffffff;\n"
         "selp.u32 %0, 1, 0, p;\n}\n"
         : "=r"(ok)
         : "r"(bar), "r"(parity)
         : "memory");
     if (ok) return true;
     if (i == 64) t0 = clock64();
-    if (i > 64 && clock64() - t0 > 4000000000LL) return false;
+    if (i > 64 && __any_sync(0xffffffffu, clock64() - t0 > 4000000000LL)) return false;
   }
 }
 
@@ -206,6 +213,7 @@ struct Math {
   const int g, t;
   const Nibbles nib;
   const float f;
+  const uint32_t scales;  // the step's (s_k f, log2 s_v, 1 / s_v) per token, in shared memory
   uint32_t k_at, v_at, v_row[2], s_at;
   int tokg;
   uint32_t qf[NT][MMAS][2];  // Q: column g of each n
@@ -213,8 +221,8 @@ struct Math {
   float m[NT][2], l[NT][2];
   int lo[NT][2], hi[NT][2];
 
-  __device__ __forceinline__ Math(const KvAttnParams &p, int lane)
-      : p(p), g(lane >> 2), t(lane & 3), f(p.scale * kLog2e) {
+  __device__ __forceinline__ Math(const KvAttnParams &p, int lane, uint32_t scales)
+      : p(p), g(lane >> 2), t(lane & 3), f(p.scale * kLog2e), scales(scales) {
     // Row r of a 16-token product stands for token tok(r) (+ 8 for the second
     // half): rows 2t and 2t + 1 are tokens t and 4 + (t ^ 1), so that the lanes
     // of a value load (rows 2t of four t) and of a key load (rows g, g + 1) read
@@ -225,7 +233,7 @@ struct Math {
     v_at = PL::OFF_V + g * (PL::VW * 4);
     v_row[0] = t * ROW;
     v_row[1] = (4 + (t ^ 1)) * ROW;
-    s_at = PL::OFF_KS + 4 * tokg;
+    s_at = scales + 16 * tokg;
   }
 
   __device__ __forceinline__ void begin(const Item &it) {
@@ -268,6 +276,17 @@ struct Math {
   // The step whose codes are at `stage` and whose first token is j; `ends`:
   // not every row sees every token.
   __device__ __forceinline__ void step(const Item &it, uint32_t stage, int j, bool ends) {
+    // scales, once per token
+#pragma unroll
+    for (int k = 0; k < PL::STEP; k += 32) {
+      const int tok = k + 4 * g + t;
+      if (PL::STEP >= 32 || tok < PL::STEP) {
+        float sk, lv, rv;
+        token_scales(stage + PL::OFF_KS + 4 * tok, stage + PL::OFF_VS + 4 * tok, f, sk, lv, rv);
+        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %3};" ::"r"(scales + 16 * tok), "f"(sk), "f"(lv), "f"(rv) : "memory");
+      }
+    }
+    __syncwarp();
     float s[NT][MT][4];
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
@@ -306,9 +325,10 @@ struct Math {
     for (int i = 0; i < MT; ++i)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const uint32_t a = stage + s_at + 4 * (16 * i + 8 * r);
-        float sk, lv;
-        token_scales(a, a + 4 * PL::STEP, f, sk, lv, rv[i][r]);
+        uint32_t x[4];
+        lds_words<4>(s_at + 16 * (16 * i + 8 * r), x);
+        const float sk = __uint_as_float(x[0]), lv = __uint_as_float(x[1]);
+        rv[i][r] = __uint_as_float(x[2]);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -525,13 +545,13 @@ __global__ void __launch_bounds__(kThreads, Plan<BITS, D, NT>::BLOCKS)
   // the warp's ring, and its barriers (one arrival a phase: lane 0)
   constexpr int S = PL::STAGES;
   const uint32_t ring = smem_u32(dyn) + warp * (S * PL::STAGE);
-  const uint32_t bars = smem_u32(dyn) + PL::SMEM - kWarps * S * 8 + warp * (S * 8);
+  const uint32_t bars = smem_u32(dyn) + PL::OFF_BAR + warp * (S * 8);
   if (lane < S) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bars + 8 * lane));
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   __syncwarp();
   uint32_t phases = 0;  // bit s: parity of the next wait on stage s
   bool ok = true;
-  Math<BITS, D, NT> math(p, lane);
+  Math<BITS, D, NT> math(p, lane, smem_u32(dyn) + PL::OFF_SCALES + warp * PL::STEP * 16);
 
   // copies: lane i < 4 MT brings array i % 4 (K, V, K scales, V scales) of tile
   // i / 4; `page_bytes` from one page to the next
@@ -801,7 +821,7 @@ static int column_tiles(long long rows) { return rows <= 8 ? 1 : 2; }
 
 size_t kv_decode_workspace(int D, long long rows) {
   const int nt = column_tiles(rows);
-  const size_t cols = 8 * nt, grid = kNumSMsGB300 * (nt == 1 ? 4 : 3);
+  const size_t cols = 8 * nt, grid = kNumSMsGB300 * 3;
   return grid * (sizeof(Desc) + 2 * sizeof(float) * cols * (D + 2));
 }
 
