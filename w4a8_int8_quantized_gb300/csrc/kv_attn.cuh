@@ -22,6 +22,61 @@ __device__ __forceinline__ void store_row4(const KvAttnParams &p, long long row,
     p.lse[row] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * kLn2;
 }
 
+// Partial results of an item cut by ranges: block i of the line left two slots of
+// ROWS rows, D sums each, then (reference, sum of weights) per row; its item's
+// first piece is in slot 1, any other in slot 0.
+template <int D, int ROWS>
+struct Partials {
+  static constexpr long long SIZE = static_cast<long long>(ROWS) * (D + 2);
+  const float *parts;
+  int first;  // range of the item's first piece
+  __device__ __forceinline__ const float *slot(int i) const {
+    return parts + (static_cast<long long>(i) * 2 + (i == first ? 1 : 0)) * SIZE;
+  }
+};
+
+// A warp joins row r of the pieces i0, i0 + step, ... up to `last`, in that order:
+// lane's four elements (from 4 lane on, if D reaches there), the reference and
+// the sum.  U pieces are fetched at a time, so that the few there are cost one
+// round trip.
+template <int D, int ROWS, int U>
+__device__ __forceinline__ void join_row(const Partials<D, ROWS> &ps, int r, int i0, int step, int last,
+                                         int lane, float4 &o, float &m, float &l) {
+  o = make_float4(0.f, 0.f, 0.f, 0.f);
+  m = kNoRef;
+  l = 0.f;
+  for (int i = i0; i <= last; i += U * step) {
+    float4 x[U];
+    float2 s[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      s[u] = make_float2(kNoRef, 0.f);
+      if (i + u * step <= last) {
+        const float *p = ps.slot(i + u * step);
+        s[u] = *reinterpret_cast<const float2 *>(p + ROWS * D + 2 * r);
+        if (lane * 4 < D) x[u] = *reinterpret_cast<const float4 *>(p + r * D + lane * 4);
+      }
+    }
+    float top = m;
+#pragma unroll
+    for (int u = 0; u < U; ++u) top = fmaxf(top, s[u].x);
+    const float a = exp2_fast(m - top);
+    o = make_float4(o.x * a, o.y * a, o.z * a, o.w * a);
+    l *= a;
+    m = top;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float b = exp2_fast(s[u].x - m);
+      l = fmaf(b, s[u].y, l);
+      o.x = fmaf(b, x[u].x, o.x);
+      o.y = fmaf(b, x[u].y, o.y);
+      o.z = fmaf(b, x[u].z, o.z);
+      o.w = fmaf(b, x[u].w, o.w);
+    }
+  }
+}
+
 // Rows per kv head and sequence up to which the few-row kernel runs, else the
 // tensor-memory one.
 constexpr int kFewRows = 64;

@@ -689,71 +689,48 @@ __global__ void __launch_bounds__(kThreads, Plan<BITS, D, NT>::BLOCKS)
   }
 }
 
-// Joins the partials of the items cut by the ranges: block c takes the item
-// that starts in range c and ends in a later one.  A warp takes every 4th
-// piece of a row (16 warps: 4 rows at once), and the sums of the 4 are added
-// in order.
+// Joins the partials of the items cut by the ranges: block (c, r) takes row r of
+// the item that starts in range c and ends in a later one; warp w takes every
+// 4th piece from the w-th on, and the four are added in order.
 template <int D, int NT>
-__global__ void __launch_bounds__(512) kv_decode_join_kernel(const KvAttnParams p, int ranges) {
-  constexpr int COLS = 8 * NT, WPR = 4, V = D / 32;
-  __shared__ float sh[16][D + 2];
+__global__ void __launch_bounds__(128) kv_decode_join_kernel(const KvAttnParams p, int ranges) {
+  constexpr int COLS = 8 * NT, W = 4;
+  __shared__ float4 o_sm[W][32];
+  __shared__ float2 s_sm[W];
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Desc *descs = reinterpret_cast<const Desc *>(p.ws);
-  const float *parts = reinterpret_cast<const float *>(descs + ranges);
-  const int c0 = blockIdx.x;
-  const Desc de = descs[c0];
+  const Desc de = reinterpret_cast<const Desc *>(p.ws)[blockIdx.x];
   if (de.last < 0) return;
   int q0, nq, len;
   seq_of(p, de.b, q0, nq, len);
-  const int R = min(nq * p.group - de.rb * COLS, COLS);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wp = warp % WPR;
-  for (int base = 0; base < R; base += 16 / WPR) {
-    const int c = base + warp / WPR;
-    float m = kNoRef, l = 0.f, o[V] = {};
-    if (c < R) {
-      // the largest reference first, then the sums against it
-      for (int i = c0 + lane; i <= de.last; i += 32) {
-        const float *part = parts + (static_cast<long long>(i) * 2 + (i == c0 ? 1 : 0)) * COLS * (D + 2);
-        m = fmaxf(m, part[COLS * D + 2 * c]);
-      }
+  const int r = blockIdx.y, ri = de.rb * COLS + r;
+  if (ri >= nq * p.group) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Partials<D, COLS> ps{reinterpret_cast<const float *>(reinterpret_cast<const Desc *>(p.ws) + ranges),
+                             static_cast<int>(blockIdx.x)};
+  float4 o;
+  float m, l;
+  join_row<D, COLS, 8>(ps, r, blockIdx.x + warp, W, de.last, lane, o, m, l);
+  o_sm[warp][lane] = o;
+  if (lane == 0) s_sm[warp] = make_float2(m, l);
+  __syncthreads();
+  if (warp != 0 || lane * 4 >= D) return;
 #pragma unroll
-      for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-#pragma unroll 4
-      for (int i = c0 + wp; i <= de.last; i += WPR) {
-        const float *part = parts + (static_cast<long long>(i) * 2 + (i == c0 ? 1 : 0)) * COLS * (D + 2);
-        const float a = exp2_fast(part[COLS * D + 2 * c] - m);
-        l = fmaf(a, part[COLS * D + 2 * c + 1], l);
-        const float *x = part + c * D + lane * V;
+  for (int w = 1; w < W; ++w) m = fmaxf(m, s_sm[w].x);
+  o = make_float4(0.f, 0.f, 0.f, 0.f);
+  l = 0.f;
 #pragma unroll
-        for (int v = 0; v < V; ++v) o[v] = fmaf(a, x[v], o[v]);
-      }
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) sh[warp][lane * V + v] = o[v];
-    if (lane == 0) sh[warp][D] = l;
-    __syncthreads();
-    if (c < R && wp == 0) {
-      float sum = 0.f;
-#pragma unroll
-      for (int w = 0; w < WPR; ++w) sum += sh[warp + w][D];
-      const int ri = de.rb * COLS + c;
-      const long long row = (static_cast<long long>(q0) + ri / p.group) * p.Hq +
-                            de.h * p.group + ri % p.group;
-      for (int d = lane * 4; d < D; d += 128) {
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < WPR; ++w) {
-          x.x += sh[warp + w][d];
-          x.y += sh[warp + w][d + 1];
-          x.z += sh[warp + w][d + 2];
-          x.w += sh[warp + w][d + 3];
-        }
-        store_row4<D>(p, row, d, x, m, sum);
-      }
-    }
-    __syncthreads();
+  for (int w = 0; w < W; ++w) {
+    const float a = exp2_fast(s_sm[w].x - m);
+    const float4 x = o_sm[w][lane];
+    l = fmaf(a, s_sm[w].y, l);
+    o.x = fmaf(a, x.x, o.x);
+    o.y = fmaf(a, x.y, o.y);
+    o.z = fmaf(a, x.z, o.z);
+    o.w = fmaf(a, x.w, o.w);
   }
+  const long long row = (static_cast<long long>(q0) + ri / p.group) * p.Hq + de.h * p.group + ri % p.group;
+  store_row4<D>(p, row, lane * 4, o, m, l);
 }
 
 template <int BITS, int D, int NT>
@@ -804,7 +781,9 @@ int launch_t(const KvAttnParams &p, cudaStream_t s) {
   }
   // no item can be cut when none has more than one unit
   if ((static_cast<long long>(p.table_w) << p.kv.page_shift) + 15 > PL::UNIT) {
-    cfg.blockDim = dim3(512);
+    const long long most = static_cast<long long>(p.max_q) * p.group;
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), static_cast<unsigned>(most < PL::COLS ? most : PL::COLS));
+    cfg.blockDim = dim3(128);
     cfg.dynamicSmemBytes = 0;
     if (cudaLaunchKernelEx(&cfg, kv_decode_join_kernel<D, NT>, p, grid) != cudaSuccess) {
       cudaGetLastError();

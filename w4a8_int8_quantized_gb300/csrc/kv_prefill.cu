@@ -887,53 +887,33 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
-// Joins the partials of the items cut by the ranges: block (c, y) takes rows 32 y
-// .. + 31 of the item that starts in range c and ends in a later one, a warp a row.
+// Joins the partials of the items cut by the ranges: block (c, y) takes rows 8 y
+// .. + 7 of the item that starts in range c and ends in a later one, a warp a row.
 template <int BITS, int D>
 __global__ void __launch_bounds__(256) kv_prefill_join_kernel(const KvAttnParams p, int ranges) {
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Desc *descs = reinterpret_cast<const Desc *>(p.ws);
-  const float *parts = reinterpret_cast<const float *>(descs + ranges);
-  const int c0 = blockIdx.x;
-  const Desc de = descs[c0];
+  const Desc de = reinterpret_cast<const Desc *>(p.ws)[blockIdx.x];
   if (de.last < 0) return;
   int q0, nq, len;
   seq_of(p, de.b, q0, nq, len);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr long long SIZE = static_cast<long long>(kRows) * (D + 2);
-  for (int r = blockIdx.y * 32 + warp; r < blockIdx.y * 32 + 32; r += 8) {
-    const int ri = de.qt * kRows + r;
-    if (ri >= nq * p.group) return;
-    float m = kNoRef;
-    for (int i = c0; i <= de.last; ++i)
-      m = fmaxf(m, parts[(i * 2 + (i == c0 ? 1 : 0)) * SIZE + kRows * D + 2 * r]);
-    float l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = c0; i <= de.last; ++i) {
-      const float *part = parts + (i * 2 + (i == c0 ? 1 : 0)) * SIZE;
-      const float a = exp2_fast(part[kRows * D + 2 * r] - m);
-      l = fmaf(a, part[kRows * D + 2 * r + 1], l);
-      if (lane * 4 < D) {
-        const float4 x = *reinterpret_cast<const float4 *>(part + r * D + lane * 4);
-        o.x = fmaf(a, x.x, o.x);
-        o.y = fmaf(a, x.y, o.y);
-        o.z = fmaf(a, x.z, o.z);
-        o.w = fmaf(a, x.w, o.w);
-      }
-    }
-    const long long row = (static_cast<long long>(q0) + ri / p.group) * p.Hq + de.h * p.group + ri % p.group;
-    if (BITS == 4) {
-      // columns 0 .. 7 of an 8 are d = 0, 4, 1, 5, 2, 6, 3, 7: the lane of the first four
-      // gives d 4, 5 for d 2, 3
-      const bool odd = lane & 1;
-      const float a = __shfl_xor_sync(0xffffffffu, odd ? o.x : o.y, 1);
-      const float b = __shfl_xor_sync(0xffffffffu, odd ? o.z : o.w, 1);
-      o = odd ? make_float4(a, b, o.y, o.w) : make_float4(o.x, o.z, a, b);
-    }
-    if (lane * 4 < D) store_row4<D>(p, row, lane * 4, o, m, l);
+  const int lane = threadIdx.x & 31, r = blockIdx.y * 8 + (threadIdx.x >> 5), ri = de.qt * kRows + r;
+  if (ri >= nq * p.group) return;
+  const Partials<D, kRows> ps{reinterpret_cast<const float *>(reinterpret_cast<const Desc *>(p.ws) + ranges),
+                              static_cast<int>(blockIdx.x)};
+  float4 o;
+  float m, l;
+  join_row<D, kRows, 4>(ps, r, blockIdx.x, 1, de.last, lane, o, m, l);
+  if (BITS == 4) {
+    // columns 0 .. 7 of an 8 are d = 0, 4, 1, 5, 2, 6, 3, 7: the lane of the first four
+    // gives d 4, 5 for d 2, 3
+    const bool odd = lane & 1;
+    const float a = __shfl_xor_sync(0xffffffffu, odd ? o.x : o.y, 1);
+    const float b = __shfl_xor_sync(0xffffffffu, odd ? o.z : o.w, 1);
+    o = odd ? make_float4(a, b, o.y, o.w) : make_float4(o.x, o.z, a, b);
   }
+  const long long row = (static_cast<long long>(q0) + ri / p.group) * p.Hq + de.h * p.group + ri % p.group;
+  if (lane * 4 < D) store_row4<D>(p, row, lane * 4, o, m, l);
 }
 
 template <int BITS, int D>
@@ -978,7 +958,7 @@ int launch_t(const KvAttnParams &p, cudaStream_t s) {
     return W8A8_ERR_CUDA;
   }
   if (tiles > 1) {  // else no item can be cut
-    cfg.gridDim = dim3(static_cast<unsigned>(grid), kRows / 32);
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), kRows / 8);
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
     if (cudaLaunchKernelEx(&cfg, kv_prefill_join_kernel<BITS, D>, p, grid) != cudaSuccess) {
