@@ -487,46 +487,54 @@ __global__ void __launch_bounds__(kThreads, Plan<BITS, D, NT>::BLOCKS)
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // -- this block's range of units -------------------------------------------
-  // prefix sums over the sequences, `chunk` of them per thread
-  const int chunk = (p.B + kThreads - 1) / kThreads;
   auto work_of = [&](int b, int &q0, int &nq, int &len, int &first, int &nu, int &nrb) {
     seq_of(p, b, q0, nq, len);
     nu = units_of<PL::UNIT>(p, nq, len, first);
     nrb = (nq * p.group + COLS - 1) / COLS;
     return static_cast<long long>(nu) * nrb * p.kv.heads;
   };
-  {
-    long long mine = 0;
-    for (int i = 0; i < chunk; ++i) {
-      const int b = threadIdx.x * chunk + i;
-      int q0, nq, len, first, nu, nrb;
-      if (b < p.B) mine += work_of(b, q0, nq, len, first, nu, nrb);
-    }
-    long long x = mine;
+  auto inclusive = [&](long long x) {  // over the warp's lanes
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long y = __shfl_up_sync(0xffffffffu, x, o);
       if (lane >= o) x += y;
     }
-    sums[threadIdx.x] = x;  // inclusive within the warp
+    return x;
+  };
+  // The sequence in which this block's range starts, its first unit, and the range:
+  // prefix sums over the sequences, a lane each while they fit a warp (every
+  // warp for itself), else `chunk` of them a thread.
+  int b;
+  long long start, per, c0, c1;
+  auto range = [&](long long total) {
+    per = total < 0x7fffffff ? (static_cast<unsigned>(total) + gridDim.x - 1) / gridDim.x
+                             : (total + gridDim.x - 1) / gridDim.x;
+    c0 = blockIdx.x * per;
+    c1 = min(c0 + per, total);
+  };
+  if (p.B <= 32) {
+    int q0, nq, len, first, nu, nrb;
+    const long long mine = lane < p.B ? work_of(lane, q0, nq, len, first, nu, nrb) : 0;
+    const long long x = inclusive(mine);
+    range(__shfl_sync(0xffffffffu, x, 31));
+    b = __popc(__ballot_sync(0xffffffffu, x <= c0));  // sequences that end before c0
+    start = __shfl_sync(0xffffffffu, x - mine, b & 31);
+  } else {
+    const int chunk = (p.B + kThreads - 1) / kThreads;
+    long long x = 0;
+    for (int i = 0; i < chunk; ++i) {
+      const int e = threadIdx.x * chunk + i;
+      int q0, nq, len, first, nu, nrb;
+      if (e < p.B) x += work_of(e, q0, nq, len, first, nu, nrb);
+    }
+    x = inclusive(x);
+    sums[threadIdx.x] = x;
     __syncthreads();
     for (int w = 0; w < warp; ++w) x += sums[w * 32 + 31];
     __syncthreads();
     sums[threadIdx.x] = x;
     __syncthreads();
-  }
-  const long long total = sums[kThreads - 1];
-  const long long per = (total + gridDim.x - 1) / gridDim.x;
-  const long long c0 = blockIdx.x * per, c1 = min(c0 + per, total);
-  Desc *descs = reinterpret_cast<Desc *>(p.ws);
-  float *parts = reinterpret_cast<float *>(descs + gridDim.x);
-  if (threadIdx.x == 0) descs[blockIdx.x].last = -1;
-  if (c0 >= c1) return;
-
-  // first sequence: binary search over the threads' sums, then along the chunk
-  int b;
-  long long start;  // first unit of sequence b
-  {
+    range(sums[kThreads - 1]);
     int lo = 0, hi = kThreads - 1;
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
@@ -535,6 +543,11 @@ __global__ void __launch_bounds__(kThreads, Plan<BITS, D, NT>::BLOCKS)
     b = lo * chunk;
     start = lo > 0 ? sums[lo - 1] : 0;
   }
+  Desc *descs = reinterpret_cast<Desc *>(p.ws);
+  float *parts = reinterpret_cast<float *>(descs + gridDim.x);
+  if (threadIdx.x == 0) descs[blockIdx.x].last = -1;
+  if (c0 >= c1) return;
+
   int q0, nq, len, first, nu, nrb;
   long long work = work_of(b, q0, nq, len, first, nu, nrb);
   while (start + work <= c0) {
@@ -564,6 +577,7 @@ __global__ void __launch_bounds__(kThreads, Plan<BITS, D, NT>::BLOCKS)
   const uint32_t cdst = ring + ctile * cbytes +
                         (carr == 0 ? 0 : carr == 1 ? PL::OFF_V : carr == 2 ? PL::OFF_KS : PL::OFF_VS);
   const int pmask = (1 << p.kv.page_shift) - 1;
+  const int run_tokens = min(pmask + 1, PL::STEP);
 
   for (long long at = c0; at < c1;) {
     while (at >= start + work) {
@@ -571,7 +585,8 @@ __global__ void __launch_bounds__(kThreads, Plan<BITS, D, NT>::BLOCKS)
       work = work_of(++b, q0, nq, len, first, nu, nrb);
     }
     // item: units [istart, istart + nu) of the line
-    const int item = static_cast<int>((at - start) / nu);
+    const int item = at - start < 0x7fffffff ? static_cast<int>(at - start) / nu
+                                             : static_cast<int>((at - start) / nu);
     const long long istart = start + static_cast<long long>(item) * nu;
     const int u0 = static_cast<int>(at - istart);
     const int u1 = static_cast<int>(min(static_cast<long long>(nu), c1 - istart));
@@ -602,18 +617,21 @@ __global__ void __launch_bounds__(kThreads, Plan<BITS, D, NT>::BLOCKS)
       return e < 0 ? -2 : e;
     };
     auto issue = [&](int page, int j, int st) {
-      const uint32_t there = __ballot_sync(0xffffffffu, page >= 0);
+      if (__any_sync(0xffffffffu, page == -2)) it.bad = true;
+      // tiles that follow one another in a page come in one copy
+      const int run = (j & (run_tokens - 1)) == 0 ? run_tokens : 16;
+      const bool copies = page >= 0 && (ctile & (run - 1)) == 0;
+      const uint32_t there = __ballot_sync(0xffffffffu, copies);
       const uint32_t bar = bars + 8 * st;
-      if (__popc(there) != 4 * MT && __any_sync(0xffffffffu, page == -2)) it.bad = true;
       if (lane == 0)
         asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar),
-                     "r"(__popc(there) / 4 * PL::TILE_BYTES)
+                     "r"(__popc(there) / 4 * (run >> 4) * PL::TILE_BYTES)
                      : "memory");
       __syncwarp();
-      if (page >= 0)
+      if (copies)
         bulk_copy(cdst + st * PL::STAGE,
                   hsrc + static_cast<size_t>(page) * page_bytes + ((j + ctile) & pmask) * cbytes,
-                  16 * cbytes, bar);
+                  run * cbytes, bar);
     };
     int j = first + u0 * PL::UNIT + warp * PL::STEP;
     int page[S + 1];  // pages of the first steps; the last one: of the next to be issued
@@ -691,10 +709,10 @@ __global__ void __launch_bounds__(kThreads, Plan<BITS, D, NT>::BLOCKS)
 
 // Joins the partials of the items cut by the ranges: block (c, r) takes row r of
 // the item that starts in range c and ends in a later one; warp w takes every
-// 4th piece from the w-th on, and the four are added in order.
-template <int D, int NT>
-__global__ void __launch_bounds__(128) kv_decode_join_kernel(const KvAttnParams p, int ranges) {
-  constexpr int COLS = 8 * NT, W = 4;
+// W-th piece from the w-th on, and the warps are added in order.
+template <int D, int NT, int W>
+__global__ void __launch_bounds__(32 * W) kv_decode_join_kernel(const KvAttnParams p, int ranges) {
+  constexpr int COLS = 8 * NT;
   __shared__ float4 o_sm[W][32];
   __shared__ float2 s_sm[W];
   asm volatile("griddepcontrol.launch_dependents;");
@@ -783,9 +801,13 @@ int launch_t(const KvAttnParams &p, cudaStream_t s) {
   if ((static_cast<long long>(p.table_w) << p.kv.page_shift) + 15 > PL::UNIT) {
     const long long most = static_cast<long long>(p.max_q) * p.group;
     cfg.gridDim = dim3(static_cast<unsigned>(grid), static_cast<unsigned>(most < PL::COLS ? most : PL::COLS));
-    cfg.blockDim = dim3(128);
+    // items of many pieces: more warps fetch them (131072 tokens, 57 pieces: 4 warps
+    // 40 us in all, 8 warps 38; 64 sequences, 2 pieces: 82 and 84)
+    const bool many = grid / (p.B * p.kv.heads) >= 32;
+    cfg.blockDim = dim3(many ? 256 : 128);
     cfg.dynamicSmemBytes = 0;
-    if (cudaLaunchKernelEx(&cfg, kv_decode_join_kernel<D, NT>, p, grid) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, many ? kv_decode_join_kernel<D, NT, 8> : kv_decode_join_kernel<D, NT, 4>,
+                           p, grid) != cudaSuccess) {
       cudaGetLastError();
       return W8A8_ERR_CUDA;
     }
