@@ -17,7 +17,8 @@
 //                    under the other half's products;
 //   warps 21, 22     bring the next item's Q rows while the current one finishes;
 //   warp 23          walks this block's range of work and publishes its pieces.
-// TMEM: S_0, S_1 (128 columns each, P in their first 64), O_0, O_1 (D columns).
+// TMEM: S_0, S_1 (two buffers of 64 keys each, P in the first half of its buffer's
+// columns), O_0, O_1 (D columns).
 //
 // Operands: Q and K are K-major.  V keeps its token rows and is read as the
 // MN-major operand, so nothing is transposed.  At 4 bits the converter's pairs
@@ -74,16 +75,16 @@ struct Plan {
   static constexpr int OFF_Q = 0, OFF_K = 2 * TILE, OFF_V = 4 * TILE, OFF_S = 6 * TILE;
   static constexpr int SLOTS = 3;                      // of token scales (see the converters)
   static constexpr int OFF_BAR = OFF_S + SLOTS * 3 * kKeys * 4;
-  static constexpr int BARS = 22 + SLOTS + 2 * kRing + 1;
+  static constexpr int BARS = 24 + SLOTS + 2 * kRing + 1;
   static constexpr int OFF_PIECE = OFF_BAR + BARS * 8;
   static constexpr int OFF_MISC = OFF_PIECE + kRing * static_cast<int>(sizeof(Piece));
   static constexpr int SMEM = OFF_MISC + 16 + 1024;    // 1024: aligned by hand
-  static constexpr uint32_t COL_S = 0, COL_O = 256;    // S_w at 128 w, O_w at 256 + 128 w
+  static constexpr uint32_t COL_S = 0, COL_O = 256;    // S_w at 128 w + 64 c, O_w at 256 + 128 w
 };
 static_assert(Plan<128>::SMEM <= 232448, "shared memory plan too large");
 
-// D fp32, A and B fp16, M = 128; S: N = 128, both K-major; PV: N = D, B MN-major
-constexpr uint32_t kIdescS = (1u << 4) | (128u >> 3 << 17) | (128u >> 4 << 24);
+// D fp32, A and B fp16, M = 128; S: N = 64, both K-major; PV: N = D, B MN-major
+constexpr uint32_t kIdescS = (1u << 4) | (64u >> 3 << 17) | (128u >> 4 << 24);
 template <int D>
 __host__ __device__ constexpr uint32_t idesc_pv() {
   return (1u << 4) | (1u << 16) | (static_cast<uint32_t>(D) >> 3 << 17) | (128u >> 4 << 24);
@@ -314,13 +315,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
   auto k_empty = [&](int s) { return bar0 + 8u * (6 + s); };
   auto v_full = [&](int s) { return bar0 + 8u * (8 + s); };
   auto v_empty = [&](int s) { return bar0 + 8u * (10 + s); };
-  auto s_full = [&](int w) { return bar0 + 8u * (12 + w); };
-  auto p_full = [&](int w, int c) { return bar0 + 8u * (14 + 2 * w + c); };  // keys 64 c .. + 63
-  auto o_full = [&](int w) { return bar0 + 8u * (18 + w); };
-  auto a_done = [&](int w) { return bar0 + 8u * (20 + w); };  // products of a tile's first 64 keys
-  auto sc_full = [&](int i) { return bar0 + 8u * (22 + i); };
-  auto piece_full = [&](int i) { return bar0 + 8u * (22 + PL::SLOTS + i); };
-  auto piece_empty = [&](int i) { return bar0 + 8u * (22 + PL::SLOTS + kRing + i); };
+  // per row half w and key half c of a tile: scores there, weights there, products done
+  auto s_full = [&](int w, int c) { return bar0 + 8u * (12 + 2 * w + c); };
+  auto p_full = [&](int w, int c) { return bar0 + 8u * (16 + 2 * w + c); };
+  auto o_done = [&](int w, int c) { return bar0 + 8u * (20 + 2 * w + c); };
+  auto sc_full = [&](int i) { return bar0 + 8u * (24 + i); };
+  auto piece_full = [&](int i) { return bar0 + 8u * (24 + PL::SLOTS + i); };
+  auto piece_empty = [&](int i) { return bar0 + 8u * (24 + PL::SLOTS + kRing + i); };
   const uint32_t drain = bar0 + 8u * (PL::BARS - 1);
   Piece *pieces = reinterpret_cast<Piece *>(sm + PL::OFF_PIECE);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + PL::OFF_MISC);
@@ -333,11 +334,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
       mbar_init(k_empty(i), 1);
       mbar_init(v_full(i), 4);
       mbar_init(v_empty(i), 1);
-      mbar_init(s_full(i), 1);
-      mbar_init(p_full(i, 0), kSoftWarps / 2);
-      mbar_init(p_full(i, 1), kSoftWarps / 2);
-      mbar_init(o_full(i), 1);
-      mbar_init(a_done(i), 1);
+      for (int c = 0; c < 2; ++c) {
+        mbar_init(s_full(i, c), 1);
+        mbar_init(p_full(i, c), kSoftWarps / 2);
+        mbar_init(o_done(i, c), 1);
+      }
     }
     for (int i = 0; i < PL::SLOTS; ++i) mbar_init(sc_full(i), 4);
     for (int i = 0; i < kRing; ++i) {
@@ -396,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
     const int r0 = w * 128 + quad * 32 + sub * 16;  // the warp's first row
     const uint32_t lanes = static_cast<uint32_t>(quad * 32 + sub * 16) << 16;
     const uint32_t col_s = lanes + PL::COL_S + 128 * w, col_o = lanes + PL::COL_O + 128 * w;
-    uint32_t s_phase = 0, o_phase = 0;
+    uint32_t s_phase = 0;  // of the tile's barriers
     uint32_t tiles = 0;  // so far
     bool ok = true;
     while (ok && wait(piece_full(reader.i), reader.phase)) {
@@ -431,16 +432,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
       bool fresh = true;
       for (; j < j_end; j += kKeys) {
         const uint32_t slot = tiles % PL::SLOTS;
-        ok = wait(s_full(w), s_phase) && wait(sc_full(slot), (tiles / PL::SLOTS) & 1u);
+        ok = wait(sc_full(slot), (tiles / PL::SLOTS) & 1u);
         if (!ok) break;
         ++tiles;
-        s_phase ^= 1u;
-        tc_fence_after();
         const float2 *sc = reinterpret_cast<const float2 *>(sm + PL::OFF_S + slot * (3 * kKeys * 4)) + t;
-        // 64 keys at a time: their weights are handed over, and multiplied, while
-        // the others are being made (and half the registers do)
+        // 64 keys at a time, each half of the tile with its own columns of TMEM: while
+        // one half's weights are made, the other half's products and the scores of
+        // the next tile run
 #pragma unroll 1
         for (int c = 0; c < 2; ++c, sc += kKeys / 4) {
+          ok = wait(s_full(w, c), s_phase);
+          if (!ok) break;
+          tc_fence_after();
           // u[4 n + 2 y + e]: row y, column 64 c + 8 n + 2 t + e
           uint32_t s[32];
           tmem_ld_frag(col_s + 64 * c, s);
@@ -487,10 +490,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
               l[y][0] *= a[y];
               l[y][1] *= a[y];
             }
-            // O is this warp's to change once the products so far are in: those of
-            // the tile's first 64 keys have a barrier of their own
-            if (c == 1) ok = ok && wait(a_done(w), s_phase ^ 1u);
+            // O is this warp's to change once the products of the 64 keys before are in
             if (!fresh || c == 1) {
+              ok = wait(o_done(w, c ^ 1), c == 1 ? s_phase : s_phase ^ 1u);
+              if (!ok) break;
               tc_fence_after();
 #pragma unroll 1
               for (int q = 0; q < D / 32; ++q) {
@@ -519,13 +522,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
               v[2 * n + y] = *reinterpret_cast<const uint32_t *>(&h);
             }
           }
-          tmem_st_half_frag(col_s + 32 * c, v);
+          tmem_st_half_frag(col_s + 64 * c, v);
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(p_full(w, c));
         }
+        if (!ok) break;
         fresh = false;
+        s_phase ^= 1u;
       }
       if (!ok) break;
       // -- the item's (or piece's) end
@@ -551,9 +556,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
         }
       }
       if (!whole && x.t0 == 0 && threadIdx.x == 0) descs[blockIdx.x] = Desc{x.b, x.h, x.qt, x.last};
-      ok = wait(o_full(w), o_phase);
+      ok = wait(o_done(w, 1), s_phase ^ 1u);
       if (!ok) break;
-      o_phase ^= 1u;
       tc_fence_after();
 #pragma unroll 1
       for (int q = 0; q < D / 32; ++q) {
@@ -693,24 +697,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
       uint32_t kph = 0, vph = 0, qph[2] = {0, 0}, pph[2] = {0, 0};
       const uint64_t q_desc = sw128_desc(base + PL::OFF_Q), k_desc = sw128_desc(base + PL::OFF_K);
       const uint64_t v_desc0 = v_desc(base + PL::OFF_V);
-      auto scores = [&](int w) {
+      // S_w of keys 64 c .. + 63 of the open K stage
+      auto scores = [&](int w, int c) {
         tc_fence_after();
-        const uint64_t a = q_desc + w * (PL::TILE >> 4), b = k_desc + ks * (PL::TILE >> 4);
+        const uint64_t a = q_desc + w * (PL::TILE >> 4), b = k_desc + ks * (PL::TILE >> 4) + c * (64 * 128 >> 4);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t at = ((k >> 2) * PL::SUB + (k & 3) * 32) >> 4;
-          mma_ss(on, PL::COL_S + 128 * w, a + at, b + at, kIdescS, k > 0);
+          mma_ss(on, PL::COL_S + 128 * w + 64 * c, a + at, b + at, kIdescS, k > 0);
         }
-        commit_if(on, s_full(w));
+        commit_if(on, s_full(w, c));
       };
       // O_w += P V over keys 64 c .. + 63
       auto values = [&](int w, int c, bool fresh) {
         tc_fence_after();
-        const uint64_t b = v_desc0 + vs * (PL::TILE >> 4);
+        const uint64_t b = v_desc0 + vs * (PL::TILE >> 4) + c * (64 * 128 >> 4);
 #pragma unroll
-        for (int k = 4 * c; k < 4 * c + 4; ++k)
-          mma_ts(on, PL::COL_O + 128 * w, PL::COL_S + 128 * w + 8 * k, b + k * (2048 >> 4),
+        for (int k = 0; k < 4; ++k)
+          mma_ts(on, PL::COL_O + 128 * w, PL::COL_S + 128 * w + 64 * c + 8 * k, b + k * (2048 >> 4),
                  idesc_pv<D>(), !(fresh && k == 0));
+        commit_if(on, o_done(w, c));
       };
       // the K stage whose scores are next: waited for once, released after the last half
       auto open_k = [&]() { return wait(k_full(ks), kph); };
@@ -723,12 +729,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
       // the first scores of a piece
       auto start = [&](const Piece &z) {
         if (!open_k()) return false;
-        for (int w = 0; w < 2 && z.R > 128 * w; ++w) {
-          if (!wait(q_full(w), qph[w])) return false;
-          qph[w] ^= 1u;
-          scores(w);
-          if (z.t1 - z.t0 == 1) commit_if(on, q_empty(w));
-        }
+        for (int c = 0; c < 2; ++c)
+          for (int w = 0; w < 2 && z.R > 128 * w; ++w) {
+            if (c == 0) {
+              if (!wait(q_full(w), qph[w])) return false;
+              qph[w] ^= 1u;
+            }
+            scores(w, c);
+            if (c == 1 && z.t1 - z.t0 == 1) commit_if(on, q_empty(w));
+          }
         close_k();
         return true;
       };
@@ -746,40 +755,28 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
           }
           ok = wait(v_full(vs), vph);
           if (!ok) break;
-          auto finish = [&](int w) {  // O_w += P_w V of tile i
-            if (x.R <= 128 * w) return true;
-            if (!wait(p_full(w, 0), pph[w])) return false;
-            values(w, 0, i == x.t0);
-            commit_if(on, a_done(w));
-            if (!wait(p_full(w, 1), pph[w])) return false;
-            pph[w] ^= 1u;
-            values(w, 1, false);
-            if (last) commit_if(on, o_full(w));
-            return true;
-          };
-          if (!last) {
-            ok = finish(0) && open_k();
-            if (!ok) break;
-            scores(0);
-            // the item's last scores: its Q rows may be replaced
-            if (i + 2 == x.t1) commit_if(on, q_empty(0));
-            ok = finish(1);
-            if (!ok) break;
-            commit_if(on, v_empty(vs));
-            if (x.R > 128) {
-              scores(1);
-              if (i + 2 == x.t1) commit_if(on, q_empty(1));
-            }
-            close_k();
-          } else {
-            // nothing of this item waits for the next one's rows
-            ok = finish(0) && finish(1);
-            if (!ok) break;
-            commit_if(on, v_empty(vs));
-            if (more) {
-              ok = start(y);
+          if (!last) ok = open_k();
+          for (int c = 0; c < 2 && ok; ++c)
+            for (int w = 0; w < 2 && x.R > 128 * w; ++w) {
+              ok = wait(p_full(w, c), pph[w]);
               if (!ok) break;
+              values(w, c, i == x.t0 && c == 0);
+              if (!last) {
+                // into the buffer whose weights have just been used
+                scores(w, c);
+                // the item's last scores: its Q rows may be replaced
+                if (c == 1 && i + 2 == x.t1) commit_if(on, q_empty(w));
+              }
             }
+          if (!ok) break;
+          pph[0] ^= 1u;
+          if (x.R > 128) pph[1] ^= 1u;
+          commit_if(on, v_empty(vs));
+          if (!last) {
+            close_k();
+          } else if (more) {  // nothing of this item waits for the next one's rows
+            ok = start(y);
+            if (!ok) break;
           }
           vs ^= 1;
           if (vs == 0) vph ^= 1u;
