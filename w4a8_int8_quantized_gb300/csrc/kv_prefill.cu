@@ -642,51 +642,79 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
         }
       }
     };
-    Piece x;
-    while (ok && next_piece(reader, x)) {
-      const int end = min(x.hi_max, x.len);
-      for (int i = x.t0; i < x.t1; ++i) {
-        const int a = x.first + i * kKeys + tok;
-        const int page = a < end ? page_of(p, x.b, a >> p.kv.page_shift) : -1;
-        const long long row = p.kv.row(page < 0 ? 0 : page, x.h) + (a & pmask);
-        uint4 kv[NV], vv[NV];
-        float ks = 0.f, vs = 0.f;
-#pragma unroll
-        for (int e = 0; e < NV; ++e) kv[e] = vv[e] = make_uint4(0, 0, 0, 0);
-        if (page >= 0) {
-          const uint4 *kp = reinterpret_cast<const uint4 *>(p.kv.kc + row * ROW);
-#pragma unroll
-          for (int e = 0; e < NV; ++e) kv[e] = __ldg(kp + e);
-          ks = __ldg(p.kv.ks + row);
-          vs = __ldg(p.kv.vs + row);
-          const uint4 *vp = reinterpret_cast<const uint4 *>(p.kv.vc + row * ROW);
-#pragma unroll
-          for (int e = 0; e < NV; ++e) vv[e] = __ldg(vp + e);
-        }
-        ok = wait(k_empty(st), phase);
-        if (!ok) break;
-        convert(kv, base + PL::OFF_K + st * PL::TILE);
-        const uint32_t sc = base + PL::OFF_S + slot * (3 * kKeys * 4) + tok * 4;
-        const float sv = vs == 0.f ? 1.f : vs;  // s_v = 0: all codes 0, any scale will do
-        sts1(sc, page < 0 ? 0.f : ks * (p.scale * kLog2e));
-        sts1(sc + kKeys * 4, page < 0 ? -CUDART_INF_F : log2_fast(sv));
-        sts1(sc + 2 * kKeys * 4, page < 0 ? 0.f : 1.f / sv);
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(k_full(st));
-          mbar_arrive(sc_full(slot));
-        }
-        ok = wait(v_empty(st), phase);
-        if (!ok) break;
-        convert(vv, base + PL::OFF_V + st * PL::TILE);
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(v_full(st));
-        slot = slot + 1 == PL::SLOTS ? 0 : slot + 1;
-        st ^= 1;
-        if (st == 0) phase ^= 1u;
+    // The codes of the next K are fetched when this tile's are converted, those of
+    // the next V likewise, so that memory's latency lies under the other's work.
+    // (Loads of 8 whole rows side by side instead of a row a lane took 352 us for
+    // what this takes PREFETCHUS: one warp a scheduler is bound by its instructions.)
+    // The tile to fetch: its sequence, head, this lane's token, where the keys
+    // end, and the piece's tiles after it.
+    int tb = 0, th = 0, ta = 0, tend = 0, left = 0;
+    auto advance = [&]() {
+      if (left > 0) {
+        ta += kKeys;
+        --left;
+        return true;
       }
+      Piece x;
+      if (!next_piece(reader, x)) return false;
+      tb = x.b;
+      th = x.h;
+      ta = x.first + x.t0 * kKeys + tok;
+      tend = min(x.hi_max, x.len);
+      left = x.t1 - x.t0 - 1;
+      return true;
+    };
+    uint4 kv[NV], vv[NV];
+    float ks = 0.f, vs = 0.f;
+    long long row = -1;  // of the token in the cache; -1: left out
+    auto load = [&](const uint8_t *codes, uint4 (&v)[NV]) {
+#pragma unroll
+      for (int e = 0; e < NV; ++e) {
+        v[e] = make_uint4(0, 0, 0, 0);
+        if (row >= 0) v[e] = __ldg(reinterpret_cast<const uint4 *>(codes + row * ROW) + e);
+      }
+    };
+    auto load_k = [&]() {
+      const int page = ta < tend ? page_of(p, tb, ta >> p.kv.page_shift) : -1;
+      row = page < 0 ? -1 : p.kv.row(page, th) + (ta & pmask);
+      load(p.kv.kc, kv);
+      if (row >= 0) {
+        ks = __ldg(p.kv.ks + row);
+        vs = __ldg(p.kv.vs + row);
+      }
+    };
+    bool have = advance();
+    if (have) {
+      load_k();
+      load(p.kv.vc, vv);
+    }
+    while (ok && have) {
+      ok = wait(k_empty(st), phase);
+      if (!ok) break;
+      convert(kv, base + PL::OFF_K + st * PL::TILE);
+      const uint32_t sc = base + PL::OFF_S + slot * (3 * kKeys * 4) + tok * 4;
+      const float sv = vs == 0.f ? 1.f : vs;  // s_v = 0: all codes 0, any scale will do
+      sts1(sc, row < 0 ? 0.f : ks * (p.scale * kLog2e));
+      sts1(sc + kKeys * 4, row < 0 ? -CUDART_INF_F : log2_fast(sv));
+      sts1(sc + 2 * kKeys * 4, row < 0 ? 0.f : 1.f / sv);
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(k_full(st));
+        mbar_arrive(sc_full(slot));
+      }
+      have = advance();
+      if (have) load_k();
+      ok = wait(v_empty(st), phase);
+      if (!ok) break;
+      convert(vv, base + PL::OFF_V + st * PL::TILE);
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(v_full(st));
+      if (have) load(p.kv.vc, vv);
+      slot = slot + 1 == PL::SLOTS ? 0 : slot + 1;
+      st ^= 1;
+      if (st == 0) phase ^= 1u;
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
