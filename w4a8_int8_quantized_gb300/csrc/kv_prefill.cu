@@ -7,16 +7,16 @@
 // (2048 cycles of the tensor pipe at D = 128) against 17 KB of cache, so it is
 // bound by the tensor pipe, with the softmax (32768 exponentials) close behind.
 //
-// One CTA of 24 warps per SM:
-//   warps 0-7, 8-15  softmax of rows 0-127 and 128-255, 16 rows a warp: scores
+// One CTA of 16 warps per SM:
+//   warps 0-3, 4-7   softmax of rows 0-127 and 128-255, 32 rows a warp: scores
 //                    from TMEM, weights P back over them as fp16;
-//   warps 16-19      converters: a thread owns a token; codes to fp16 (exact)
+//   warps 8-11       converters: a thread owns a token; codes to fp16 (exact)
 //                    into 128-byte-swizzled stages, and the token's scales;
-//   warp 20          issues the MMAs: S_0, S_1 of the next keys go between the
-//                    P V of the two row halves, so that one half's softmax runs
-//                    under the other half's products;
-//   warps 21, 22     bring the next item's Q rows while the current one finishes;
-//   warp 23          walks this block's range of work and publishes its pieces.
+//   warp 12          issues the MMAs: once the weights of 64 keys are there, their
+//                    P V, then the scores of the next tile into the same buffer,
+//                    while the softmax works on the other buffer;
+//   warps 13, 14     bring the next item's Q rows while the current one finishes;
+//   warp 15          walks this block's range of work and publishes its pieces.
 // TMEM: S_0, S_1 (two buffers of 64 keys each, P in the first half of its buffer's
 // columns), O_0, O_1 (D columns).
 //
@@ -48,11 +48,13 @@
 namespace w8a8 {
 namespace {
 
-constexpr int kSoftWarps = 16, kWarps = kSoftWarps + 8, kThreads = 32 * kWarps;
+constexpr int kSoftWarps = 8, kWarps = kSoftWarps + 8, kThreads = 32 * kWarps;
 constexpr int kRows = 256;  // of an item
 constexpr int kKeys = 128;  // of a tile
 constexpr int kRing = 4;    // published pieces
-constexpr int kItemCost = 3;  // of an item beyond its tiles, in tiles: its start and end
+// An item's start and end, in tiles, for the split (a prompt of 4516 tokens: 3 276 us,
+// 4 240, 5 227, 6 230, 8 235).
+constexpr int kItemCost = 5;
 
 // A piece of an item: its tiles t0 .. t1 - 1 of nt.
 struct Piece {
@@ -382,20 +384,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
   };
   Reader reader;
 
-  // Registers per warpgroup: 4 * 88 + 72 + 56 = 6 * 80, the launch's share (launch_t
-  // checks that the kernel was built with 80)
+  // Registers per warpgroup: 2 * 168 + 96 + 80 = 4 * 128, the launch's share (allow_smem
+  // checks that the kernel was built with 128)
   if (warp < kSoftWarps) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
     // ------------------------------------------------------------ softmax ----
-    // Scores come as fragments: a thread (lane 4 g + t) holds rows g and g + 8 of
-    // its warp's 16 and two of every 8 columns, so a token's scales, read from
-    // shared memory, serve two rows.  (One row a thread needs 96 16-byte
-    // broadcasts per row and tile, more than the 2048 cycles of MMAs; four rows a
-    // thread leave two warps a scheduler, too few to cover the latencies: a
-    // prompt of 4516 tokens took 426 us.)
-    const int w = warp >> 3, quad = warp & 3, sub = (warp >> 2) & 1, g = lane >> 2, t = lane & 3;
-    const int r0 = w * 128 + quad * 32 + sub * 16;  // the warp's first row
-    const uint32_t lanes = static_cast<uint32_t>(quad * 32 + sub * 16) << 16;
+    // Scores come as fragments: a thread (lane 4 g + t) holds rows g + 8 y of its
+    // warp's 32 and two of every 8 columns, so a token's scales, read from shared
+    // memory, serve four rows.  Shared memory is the tightest resource here: per
+    // tile the MMAs read 256 KB of operands (2048 cycles), the converters write 64
+    // and these reads take 96; two rows a thread on twice the warps doubles them
+    // (512 tokens behind 32256: 283 us against 263), one row a thread with
+    // 16-byte broadcasts quadruples them.
+    constexpr int Y = 4;  // rows of a thread: g + 8 y
+    const int w = warp >> 2, g = lane >> 2, t = lane & 3;
+    const int r0 = w * 128 + (warp & 3) * 32;  // the warp's first row
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    constexpr uint32_t kLane16 = 16u << 16;
     const uint32_t col_s = lanes + PL::COL_S + 128 * w, col_o = lanes + PL::COL_O + 128 * w;
     uint32_t s_phase = 0;  // of the tile's barriers
     uint32_t tiles = 0;  // so far
@@ -417,9 +422,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
         if (r < x.R) visible(p, x.len - x.nq + (x.qt * kRows + r) / p.group, x.len, lo, hi);
       };
       int lo_max = 0, hi_min = 0x7fffffff;
-      float m[2], l[2][2];
+      float m[Y], l[Y][2];
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
+      for (int y = 0; y < Y; ++y) {
         int lo, hi;
         limits(y, lo, hi);
         lo_max = max(lo_max, lo);
@@ -444,21 +449,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
           ok = wait(s_full(w, c), s_phase);
           if (!ok) break;
           tc_fence_after();
-          // u[4 n + 2 y + e]: row y, column 64 c + 8 n + 2 t + e
-          uint32_t s[32];
-          tmem_ld_frag(col_s + 64 * c, s);
-          tmem_wait_ld<32>(s);
+          // u[32 (y / 2) + 4 n + 2 (y % 2) + e]: row y, column 64 c + 8 n + 2 t + e
+          uint32_t s[64];
+#pragma unroll
+          for (int z = 0; z < 2; ++z) tmem_ld_frag(col_s + 64 * c + z * kLane16, s + 32 * z);
+          tmem_wait_ld<64>(s);
           float *u = reinterpret_cast<float *>(s);
+          auto at = [&](int y, int n) { return u + 32 * (y >> 1) + 4 * n + 2 * (y & 1); };
 #pragma unroll
           for (int n = 0; n < 8; ++n) {
             const float2 k = sc[4 * n], z = sc[kKeys / 2 + 4 * n];
-            fma2(u[4 * n], u[4 * n + 1], u[4 * n], u[4 * n + 1], k.x, k.y, z.x, z.y);
-            fma2(u[4 * n + 2], u[4 * n + 3], u[4 * n + 2], u[4 * n + 3], k.x, k.y, z.x, z.y);
+#pragma unroll
+            for (int y = 0; y < Y; ++y) {
+              float *d = at(y, n);
+              fma2(d[0], d[1], d[0], d[1], k.x, k.y, z.x, z.y);
+            }
           }
           const int jc = j + 64 * c;
           if (__any_sync(0xffffffffu, lo_max > jc || hi_min < jc + 64)) {
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
+            for (int y = 0; y < Y; ++y) {
               int lo, hi;
               limits(y, lo, hi);
               lo -= jc + 2 * t;
@@ -467,21 +477,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
               for (int n = 0; n < 8; ++n)
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
-                  if (8 * n + e < lo || 8 * n + e >= hi) u[4 * n + 2 * y + e] = -CUDART_INF_F;
+                  if (8 * n + e < lo || 8 * n + e >= hi) at(y, n)[e] = -CUDART_INF_F;
             }
           }
-          float top[2];
+          float top[Y];
+          bool over = false;
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const float *d = u + 2 * y;
-            top[y] = fmaxf(d[0], d[1]);
+          for (int y = 0; y < Y; ++y) {
+            top[y] = fmaxf(at(y, 0)[0], at(y, 0)[1]);
 #pragma unroll
-            for (int n = 1; n < 8; ++n) top[y] = max3(top[y], d[4 * n], d[4 * n + 1]);
+            for (int n = 1; n < 8; ++n) top[y] = max3(top[y], at(y, n)[0], at(y, n)[1]);
+            over |= top[y] > m[y] + kRoom;
           }
-          if (__any_sync(0xffffffffu, top[0] > m[0] + kRoom || top[1] > m[1] + kRoom)) {
-            float a[2];
+          if (__any_sync(0xffffffffu, over)) {
+            float a[Y];
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
+            for (int y = 0; y < Y; ++y) {
               top[y] = fmaxf(top[y], __shfl_xor_sync(0xffffffffu, top[y], 1));
               top[y] = fmaxf(top[y], __shfl_xor_sync(0xffffffffu, top[y], 2));
               const float nm = top[y] > m[y] + kRoom ? top[y] - kHead : m[y];
@@ -495,34 +506,37 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
               ok = wait(o_done(w, c ^ 1), c == 1 ? s_phase : s_phase ^ 1u);
               if (!ok) break;
               tc_fence_after();
-#pragma unroll 1
-              for (int q = 0; q < D / 32; ++q) {
-                uint32_t v[16];
-                tmem_ld_frag4(col_o + 32 * q, v);
-                tmem_wait_ld<16>(v);
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                  v[e] = __float_as_uint(__uint_as_float(v[e]) * a[(e >> 1) & 1]);
-                tmem_st_frag4(col_o + 32 * q, v);
-              }
+              for (int z = 0; z < 2; ++z)
+#pragma unroll 1
+                for (int q = 0; q < D / 32; ++q) {
+                  uint32_t v[16];
+                  tmem_ld_frag4(col_o + 32 * q + z * kLane16, v);
+                  tmem_wait_ld<16>(v);
+#pragma unroll
+                  for (int e = 0; e < 16; ++e)
+                    v[e] = __float_as_uint(__uint_as_float(v[e]) * a[2 * z + ((e >> 1) & 1)]);
+                  tmem_st_frag4(col_o + 32 * q + z * kLane16, v);
+                }
             }
           }
           // 8 scores become 4 columns of fp16 pairs
-          uint32_t v[16];
+          uint32_t v[32];
 #pragma unroll
           for (int n = 0; n < 8; ++n) {
             const float2 rv = sc[kKeys + 4 * n];
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              float *d = u + 4 * n + 2 * y;
+            for (int y = 0; y < Y; ++y) {
+              float *d = at(y, n);
               add2(d[0], d[1], d[0], d[1], -m[y]);
               const float w0 = exp2_fast(d[0]), w1 = exp2_fast(d[1]);
               fma2(l[y][0], l[y][1], w0, w1, rv.x, rv.y, l[y][0], l[y][1]);
               const __half2 h = __floats2half2_rn(w0, w1);
-              v[2 * n + y] = *reinterpret_cast<const uint32_t *>(&h);
+              v[16 * (y >> 1) + 2 * n + (y & 1)] = *reinterpret_cast<const uint32_t *>(&h);
             }
           }
-          tmem_st_half_frag(col_s + 64 * c, v);
+#pragma unroll
+          for (int z = 0; z < 2; ++z) tmem_st_half_frag(col_s + 64 * c + z * kLane16, v + 16 * z);
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
@@ -534,17 +548,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
       }
       if (!ok) break;
       // -- the item's (or piece's) end
-      float inv[2], sum[2];
-      long long row[2];  // of the output; -1: past the item's rows
+      float inv[Y];
+      long long row[Y];  // of the output; -1: past the item's rows
       const bool whole = x.t0 == 0 && x.t1 == x.nt;
       const long long part = static_cast<long long>(blockIdx.x) * 2 + (x.t0 == 0 ? 1 : 0);
       float *part_at = parts + part * kRows * (D + 2);
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
+      for (int y = 0; y < Y; ++y) {
         float z = l[y][0] + l[y][1];
         z += __shfl_xor_sync(0xffffffffu, z, 1);
         z += __shfl_xor_sync(0xffffffffu, z, 2);
-        sum[y] = z;
         inv[y] = z == 0.f ? 0.f : 1.f / z;
         const int r = r0 + 8 * y + g, ri = x.qt * kRows + r;
         row[y] = r < x.R ? (static_cast<long long>(x.q0) + ri / p.group) * p.Hq + x.h * p.group + ri % p.group : -1;
@@ -559,14 +572,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
       ok = wait(o_done(w, 1), s_phase ^ 1u);
       if (!ok) break;
       tc_fence_after();
+#pragma unroll
+      for (int z16 = 0; z16 < 2; ++z16)
 #pragma unroll 1
       for (int q = 0; q < D / 32; ++q) {
-        // v[4 n + 2 y + e]: row y, column 32 q + 8 n + 2 t + e
         uint32_t v[16];
-        tmem_ld_frag4(col_o + 32 * q, v);
+        tmem_ld_frag4(col_o + 32 * q + z16 * kLane16, v);
         tmem_wait_ld<16>(v);
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
+        for (int f = 0; f < 2; ++f) {
+          const int y = 2 * z16 + f;
           if (!whole) {
             // columns stay as they are (the join knows their order): a row's 32 bytes
             // from four lanes
@@ -575,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
 #pragma unroll
               for (int n = 0; n < 4; ++n)
                 *reinterpret_cast<float2 *>(dst + 8 * n) =
-                    make_float2(__uint_as_float(v[4 * n + 2 * y]), __uint_as_float(v[4 * n + 2 * y + 1]));
+                    make_float2(__uint_as_float(v[4 * n + 2 * f]), __uint_as_float(v[4 * n + 2 * f + 1]));
             }
           } else {
             // the four lanes of a row exchange pairs, so that lane t has the 8 columns
@@ -583,8 +598,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
             uint32_t h[4], o[4];
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
-              const __half2 z = __floats2half2_rn(__uint_as_float(v[4 * n + 2 * y]) * inv[y],
-                                                  __uint_as_float(v[4 * n + 2 * y + 1]) * inv[y]);
+              const __half2 z = __floats2half2_rn(__uint_as_float(v[4 * n + 2 * f]) * inv[y],
+                                                  __uint_as_float(v[4 * n + 2 * f + 1]) * inv[y]);
               h[n] = *reinterpret_cast<const uint32_t *>(&z);
             }
 #pragma unroll
@@ -608,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
       done_piece(reader);
     }
   } else if (warp < kSoftWarps + 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
     // --------------------------------------------------------- converters ----
     // The scales have a third slot: a tile's are read until both halves' weights
     // are written, and slot s is refilled for tile i + 3 only once the K stage
@@ -644,8 +659,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
     };
     // The codes of the next K are fetched when this tile's are converted, those of
     // the next V likewise, so that memory's latency lies under the other's work.
-    // (Loads of 8 whole rows side by side instead of a row a lane took 352 us for
-    // what this takes PREFETCHUS: one warp a scheduler is bound by its instructions.)
+    // (Loads of 8 whole rows side by side instead of a row a lane were a quarter slower
+    // overall: one warp a scheduler is bound by its instructions.)
     // The tile to fetch: its sequence, head, this lane's token, where the keys
     // end, and the piece's tiles after it.
     int tb = 0, th = 0, ta = 0, tend = 0, left = 0;
@@ -717,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
       if (st == 0) phase ^= 1u;
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     if (warp == kSoftWarps + 4) {
       // ------------------------------------------------------------- MMAs ----
       const uint32_t on = elect();
@@ -951,9 +966,9 @@ bool allow_smem() {
   if (!done[dev])
     done[dev] = cudaFuncSetAttribute(kv_prefill_kernel<BITS, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      Plan<D>::SMEM) == cudaSuccess;
-  // the warpgroups' register shares add up to what a launch with 80 brings
+  // the warpgroups' register shares add up to what a launch with 128 brings
   cudaFuncAttributes a;
-  if (done[dev] && (cudaFuncGetAttributes(&a, kv_prefill_kernel<BITS, D>) != cudaSuccess || a.numRegs != 80))
+  if (done[dev] && (cudaFuncGetAttributes(&a, kv_prefill_kernel<BITS, D>) != cudaSuccess || a.numRegs != 128))
     done[dev] = false;
   return done[dev];
 }
