@@ -77,7 +77,7 @@ struct Plan {
   static constexpr int OFF_Q = 0, OFF_K = 2 * TILE, OFF_V = 4 * TILE, OFF_S = 6 * TILE;
   static constexpr int SLOTS = 3;                      // of token scales (see the converters)
   static constexpr int OFF_BAR = OFF_S + SLOTS * 3 * kKeys * 4;
-  static constexpr int BARS = 24 + SLOTS + 2 * kRing + 1;
+  static constexpr int BARS = 24 + 2 * kRing + 1;
   static constexpr int OFF_PIECE = OFF_BAR + BARS * 8;
   static constexpr int OFF_MISC = OFF_PIECE + kRing * static_cast<int>(sizeof(Piece));
   static constexpr int SMEM = OFF_MISC + 16 + 1024;    // 1024: aligned by hand
@@ -321,9 +321,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
   auto s_full = [&](int w, int c) { return bar0 + 8u * (12 + 2 * w + c); };
   auto p_full = [&](int w, int c) { return bar0 + 8u * (16 + 2 * w + c); };
   auto o_done = [&](int w, int c) { return bar0 + 8u * (20 + 2 * w + c); };
-  auto sc_full = [&](int i) { return bar0 + 8u * (24 + i); };
-  auto piece_full = [&](int i) { return bar0 + 8u * (24 + PL::SLOTS + i); };
-  auto piece_empty = [&](int i) { return bar0 + 8u * (24 + PL::SLOTS + kRing + i); };
+  auto piece_full = [&](int i) { return bar0 + 8u * (24 + i); };
+  auto piece_empty = [&](int i) { return bar0 + 8u * (24 + kRing + i); };
   const uint32_t drain = bar0 + 8u * (PL::BARS - 1);
   Piece *pieces = reinterpret_cast<Piece *>(sm + PL::OFF_PIECE);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + PL::OFF_MISC);
@@ -342,7 +341,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
         mbar_init(o_done(i, c), 1);
       }
     }
-    for (int i = 0; i < PL::SLOTS; ++i) mbar_init(sc_full(i), 4);
     for (int i = 0; i < kRing; ++i) {
       mbar_init(piece_full(i), 1);
       mbar_init(piece_empty(i), kSoftWarps + 4 + 1 + 2);  // softmax, converter, MMA and Q warps
@@ -437,8 +435,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
       bool fresh = true;
       for (; j < j_end; j += kKeys) {
         const uint32_t slot = tiles % PL::SLOTS;
-        ok = wait(sc_full(slot), (tiles / PL::SLOTS) & 1u);
-        if (!ok) break;
         ++tiles;
         const float2 *sc = reinterpret_cast<const float2 *>(sm + PL::OFF_S + slot * (3 * kKeys * 4)) + t;
         // 64 keys at a time, each half of the tile with its own columns of TMEM: while
@@ -446,6 +442,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
         // the next tile run
 #pragma unroll 1
         for (int c = 0; c < 2; ++c, sc += kKeys / 4) {
+          // the token scales are there too: they precede K's arrival, which these
+          // scores waited for (a barrier of their own: 2 us of 227)
           ok = wait(s_full(w, c), s_phase);
           if (!ok) break;
           tc_fence_after();
@@ -575,50 +573,50 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
 #pragma unroll
       for (int z16 = 0; z16 < 2; ++z16)
 #pragma unroll 1
-      for (int q = 0; q < D / 32; ++q) {
-        uint32_t v[16];
-        tmem_ld_frag4(col_o + 32 * q + z16 * kLane16, v);
-        tmem_wait_ld<16>(v);
+        for (int q = 0; q < D / 32; ++q) {
+          uint32_t v[16];
+          tmem_ld_frag4(col_o + 32 * q + z16 * kLane16, v);
+          tmem_wait_ld<16>(v);
 #pragma unroll
-        for (int f = 0; f < 2; ++f) {
-          const int y = 2 * z16 + f;
-          if (!whole) {
-            // columns stay as they are (the join knows their order): a row's 32 bytes
-            // from four lanes
-            float *dst = part_at + (r0 + 8 * y + g) * D + 32 * q + 2 * t;
-            if (row[y] >= 0) {
+          for (int f = 0; f < 2; ++f) {
+            const int y = 2 * z16 + f;
+            if (!whole) {
+              // columns stay as they are (the join knows their order): a row's 32 bytes
+              // from four lanes
+              float *dst = part_at + (r0 + 8 * y + g) * D + 32 * q + 2 * t;
+              if (row[y] >= 0) {
 #pragma unroll
-              for (int n = 0; n < 4; ++n)
-                *reinterpret_cast<float2 *>(dst + 8 * n) =
-                    make_float2(__uint_as_float(v[4 * n + 2 * f]), __uint_as_float(v[4 * n + 2 * f + 1]));
+                for (int n = 0; n < 4; ++n)
+                  *reinterpret_cast<float2 *>(dst + 8 * n) =
+                      make_float2(__uint_as_float(v[4 * n + 2 * f]), __uint_as_float(v[4 * n + 2 * f + 1]));
+              }
+            } else {
+              // the four lanes of a row exchange pairs, so that lane t has the 8 columns
+              // of n = t: 64 contiguous bytes a row
+              uint32_t h[4], o[4];
+#pragma unroll
+              for (int n = 0; n < 4; ++n) {
+                const __half2 z = __floats2half2_rn(__uint_as_float(v[4 * n + 2 * f]) * inv[y],
+                                                    __uint_as_float(v[4 * n + 2 * f + 1]) * inv[y]);
+                h[n] = *reinterpret_cast<const uint32_t *>(&z);
+              }
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int n = t ^ k;  // what lane t ^ k is to have
+                const uint32_t z = n & 2 ? (n & 1 ? h[3] : h[2]) : (n & 1 ? h[1] : h[0]);
+                const uint32_t got = k ? __shfl_xor_sync(0xffffffffu, z, k) : z;
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+                  if (s == n) o[s] = got;  // lane s's pair of columns 2 s, 2 s + 1
+              }
+              uint4 z = make_uint4(o[0], o[1], o[2], o[3]);
+              if (BITS == 4)  // columns 2 s, 2 s + 1 are d = s and s + 4
+                z = make_uint4(__byte_perm(o[0], o[1], 0x5410), __byte_perm(o[2], o[3], 0x5410),
+                               __byte_perm(o[0], o[1], 0x7632), __byte_perm(o[2], o[3], 0x7632));
+              if (row[y] >= 0) *reinterpret_cast<uint4 *>(p.out + row[y] * D + 32 * q + 8 * t) = z;
             }
-          } else {
-            // the four lanes of a row exchange pairs, so that lane t has the 8 columns
-            // of n = t: 64 contiguous bytes a row
-            uint32_t h[4], o[4];
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-              const __half2 z = __floats2half2_rn(__uint_as_float(v[4 * n + 2 * f]) * inv[y],
-                                                  __uint_as_float(v[4 * n + 2 * f + 1]) * inv[y]);
-              h[n] = *reinterpret_cast<const uint32_t *>(&z);
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int n = t ^ k;  // what lane t ^ k is to have
-              const uint32_t z = n & 2 ? (n & 1 ? h[3] : h[2]) : (n & 1 ? h[1] : h[0]);
-              const uint32_t got = k ? __shfl_xor_sync(0xffffffffu, z, k) : z;
-#pragma unroll
-              for (int s = 0; s < 4; ++s)
-                if (s == n) o[s] = got;  // lane s's pair of columns 2 s, 2 s + 1
-            }
-            uint4 z = make_uint4(o[0], o[1], o[2], o[3]);
-            if (BITS == 4)  // columns 2 s, 2 s + 1 are d = s and s + 4
-              z = make_uint4(__byte_perm(o[0], o[1], 0x5410), __byte_perm(o[2], o[3], 0x5410),
-                             __byte_perm(o[0], o[1], 0x7632), __byte_perm(o[2], o[3], 0x7632));
-            if (row[y] >= 0) *reinterpret_cast<uint4 *>(p.out + row[y] * D + 32 * q + 8 * t) = z;
           }
         }
-      }
       tc_fence_before();
       done_piece(reader);
     }
@@ -714,10 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
       sts1(sc + 2 * kKeys * 4, row < 0 ? 0.f : 1.f / sv);
       fence_proxy_async();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(k_full(st));
-        mbar_arrive(sc_full(slot));
-      }
+      if (lane == 0) mbar_arrive(k_full(st));
       have = advance();
       if (have) load_k();
       ok = wait(v_empty(st), phase);
