@@ -359,6 +359,99 @@ def test_indices_outside_their_range():
         assert w8.w8a8_check_status() == 0
 
 
+# ------------------------------------------------- how the work is divided ----
+
+@pytest.mark.parametrize("B", [32, 33, 100, 700, 1300])
+def test_decode_of_many_sequences(B):
+    rng = np.random.default_rng(B)
+    lens = rng.integers(0, 60, B).tolist()
+    c = Cache(rng, lens, 1, 64, 16, 4)
+    q = rows(rng, B, 4, 64)
+    check(c, q, [1] * B, *attend(c, q))
+    assert w8.w8a8_check_status() == 0
+
+
+@pytest.mark.parametrize("B", [140, 530, 1100])
+def test_prompts_of_many_sequences(B):
+    rng = np.random.default_rng(B)
+    lens = rng.integers(0, 50, B)
+    new = np.minimum(rng.integers(0, 10, B), lens)
+    new[7], lens[7] = 90, 90                                 # rows for two blocks of 256
+    c = Cache(rng, lens.tolist(), 1, 64, 16, 8)
+    q = rows(rng, int(new.sum()), 4, 64)
+    check(c, q, new.tolist(), *attend(c, q, new.tolist(), max_q=90))
+    assert w8.w8a8_check_status() == 0
+
+
+@pytest.mark.parametrize("new,group", [([17], 1), ([31, 2], 1), ([32, 32], 1), ([33, 1], 1), ([8, 3], 4),
+                                       ([6, 5], 5), ([4], 8), ([5], 8), ([2, 1], 16), ([3, 2], 16)])
+def test_rows_around_the_change_of_kernel(new, group):
+    rng = np.random.default_rng(sum(new) + group)
+    c = Cache(rng, [500, 45][:len(new)], 2, 128, 32, 4)
+    q = rows(rng, sum(new), 2 * group, 128)
+    check(c, q, new, *attend(c, q, new, max_q=max(new)))
+    loose = attend(c, q, new)                                # max_q left to the number of rows
+    check(c, q, new, *loose)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("new,window,causal", [([40], 0, True), ([70], 0, False), ([33, 12], 4000, True), ([300], 700, True)])
+def test_long_keys_cut_between_blocks(bits, D, new, window, causal):
+    """Items whose keys many blocks share; the joined result is the same each time."""
+    rng = np.random.default_rng(bits + D + sum(new))
+    c = Cache(rng, [9003, 5000][:len(new)], 1, D, 64, bits)
+    q = rows(rng, sum(new), 4, D)
+    kw = dict(causal=causal, window=window)
+    first = attend(c, q, new, max_q=max(new), **kw)
+    check(c, q, new, *first, **kw)
+    for _ in range(3):
+        for a, b in zip(first, attend(c, q, new, max_q=max(new), **kw)):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("new", [[1], [8], [100]])
+@pytest.mark.parametrize("page", [16, 1024])
+def test_windows_over_released_pages(new, page):
+    """Pages wholly before every window may be anyone's: neither read nor reported."""
+    rng = np.random.default_rng(page + new[0])
+    c = Cache(rng, [6000], 2, 128, page, 4)
+    first = (6000 - new[0] + 1 - 300) // page                # page of the first key any row sees
+    c.table[0, :first] = -1
+    q = rows(rng, new[0], 8, 128)
+    check(c, q, new, *attend(c, q, new, window=300), window=300)
+    assert w8.w8a8_check_status() == 0
+
+
+@pytest.mark.parametrize("new", [[1, 1], [40, 3]])
+def test_table_much_wider_than_the_lengths(new):
+    rng = np.random.default_rng(6)
+    c = Cache(rng, [77, 300], 2, 128, 16, 4)
+    wide = np.full((2, 20000), 2 ** 31 - 1, np.int32)
+    wide[:, :c.table.shape[1] - 1] = c.table[:, :-1]
+    c.table = wide
+    q = rows(rng, sum(new), 8, 128)
+    check(c, q, new, *attend(c, q, new))
+    assert w8.w8a8_check_status() == 0
+
+
+def test_pages_in_order_and_out_of_order():
+    """Runs of neighbouring pages, and none: the same bits."""
+    rng = np.random.default_rng(12)
+    n = 3000
+    for bits, D in ((4, 128), (8, 64)):
+        c = Cache(rng, [n], 2, D, 16, bits)
+        q = rows(rng, 1, 8, D)
+        apart = attend(c, q)
+        count = -(-n // 16)
+        c.table = np.arange(c.pages - count, c.pages, dtype=np.int32)[None]
+        w8.kv_cache_write(cuda(c.k[0]), cuda(c.v[0]), cuda(c.slots(0, np.arange(n))), c.handle)
+        together = attend(c, q)
+        check(c, q, [1], *together)
+        for a, b in zip(apart, together):
+            assert torch.equal(a, b)
+
+
 def test_refusals():
     c = w8.KVCache.empty(4, 2, 16, 64)
     table = torch.zeros(1, 4, dtype=torch.int32, device="cuda")
