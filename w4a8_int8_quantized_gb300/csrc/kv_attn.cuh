@@ -23,8 +23,8 @@ __device__ __forceinline__ void store_row4(const KvAttnParams &p, long long row,
 }
 
 // Partial results of an item cut by ranges: block i of the line left two slots of
-// ROWS rows, D sums each, then (reference, sum of weights) per row; its item's
-// first piece is in slot 1, any other in slot 0.
+// ROWS rows' D sums each (in the kernel's own order), then (reference, sum of
+// weights) per row; its item's first piece is in slot 1, any other in slot 0.
 template <int D, int ROWS>
 struct Partials {
   static constexpr long long SIZE = static_cast<long long>(ROWS) * (D + 2);
@@ -35,44 +35,57 @@ struct Partials {
   }
 };
 
-// A warp joins row r of the pieces i0, i0 + step, ... up to `last`, in that order:
-// lane's four elements (from 4 lane on, if D reaches there), the reference and
-// the sum.  U pieces are fetched at a time, so that the few there are cost one
-// round trip.
-template <int D, int ROWS, int U>
-__device__ __forceinline__ void join_row(const Partials<D, ROWS> &ps, int r, int i0, int step, int last,
-                                         int lane, float4 &o, float &m, float &l) {
-  o = make_float4(0.f, 0.f, 0.f, 0.f);
-  m = kNoRef;
-  l = 0.f;
-  for (int i = i0; i <= last; i += U * step) {
-    float4 x[U];
-    float2 s[U];
+// A row's sums against reference m, and its sum of weights.
+template <int V>
+struct JoinedRow {
+  float4 o[V];
+  float m = kNoRef, l = 0.f;
+  __device__ __forceinline__ JoinedRow() {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-      s[u] = make_float2(kNoRef, 0.f);
-      if (i + u * step <= last) {
-        const float *p = ps.slot(i + u * step);
-        s[u] = *reinterpret_cast<const float2 *>(p + ROWS * D + 2 * r);
-        if (lane * 4 < D) x[u] = *reinterpret_cast<const float4 *>(p + r * D + lane * 4);
+    for (int v = 0; v < V; ++v) o[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+};
+
+// Adds row r of the pieces i, i + step, ... (U of them, none beyond `last`), in that
+// order: the V times four sums at `at`, `at` + `stride`, ... of a slot (none if
+// negative).  All are fetched before the first is used.
+template <int U, int D, int ROWS, int V>
+__device__ __forceinline__ void join_pieces(const Partials<D, ROWS> &ps, int r, int at, int stride, int i,
+                                            int step, int last, JoinedRow<V> &x) {
+  float4 y[U][V];
+  float2 s[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    s[u] = make_float2(kNoRef, 0.f);
+#pragma unroll
+    for (int v = 0; v < V; ++v) y[u][v] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (i + u * step <= last) {
+      const float *p = ps.slot(i + u * step);
+      s[u] = *reinterpret_cast<const float2 *>(p + ROWS * D + 2 * r);
+      if (at >= 0) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) y[u][v] = *reinterpret_cast<const float4 *>(p + at + v * stride);
       }
     }
-    float top = m;
+  }
+  float top = x.m;
 #pragma unroll
-    for (int u = 0; u < U; ++u) top = fmaxf(top, s[u].x);
-    const float a = exp2_fast(m - top);
-    o = make_float4(o.x * a, o.y * a, o.z * a, o.w * a);
-    l *= a;
-    m = top;
+  for (int u = 0; u < U; ++u) top = fmaxf(top, s[u].x);
+  const float a = exp2_fast(x.m - top);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const float b = exp2_fast(s[u].x - m);
-      l = fmaf(b, s[u].y, l);
-      o.x = fmaf(b, x[u].x, o.x);
-      o.y = fmaf(b, x[u].y, o.y);
-      o.z = fmaf(b, x[u].z, o.z);
-      o.w = fmaf(b, x[u].w, o.w);
+  for (int v = 0; v < V; ++v) x.o[v] = make_float4(x.o[v].x * a, x.o[v].y * a, x.o[v].z * a, x.o[v].w * a);
+  x.l *= a;
+  x.m = top;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const float b = exp2_fast(s[u].x - top);
+    x.l = fmaf(b, s[u].y, x.l);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      x.o[v].x = fmaf(b, y[u][v].x, x.o[v].x);
+      x.o[v].y = fmaf(b, y[u][v].y, x.o[v].y);
+      x.o[v].z = fmaf(b, y[u][v].z, x.o[v].z);
+      x.o[v].w = fmaf(b, y[u][v].w, x.o[v].w);
     }
   }
 }

@@ -65,8 +65,10 @@ struct Piece {
   int last;            // range that holds the item's last tile
 };
 
-struct Desc {
-  int b, h, qt, last;
+// An item cut by ranges, for the join: its first query, kv head, row block, rows and
+// the range of its last tile.
+struct alignas(16) Desc {
+  int q0, h, qt, R, last;
 };
 
 template <int D>
@@ -80,7 +82,9 @@ struct Plan {
   static constexpr int BARS = 24 + 2 * kRing + 1;
   static constexpr int OFF_PIECE = OFF_BAR + BARS * 8;
   static constexpr int OFF_MISC = OFF_PIECE + kRing * static_cast<int>(sizeof(Piece));
-  static constexpr int SMEM = OFF_MISC + 16 + 1024;    // 1024: aligned by hand
+  static constexpr int OFF_LIM = OFF_MISC + 16;        // keys each row sees
+  static constexpr int SMEM = OFF_LIM + kRows * 8 + 1024;  // 1024: aligned by hand
+  static_assert(OFF_LIM % 8 == 0, "row limits are pairs");
   static constexpr uint32_t COL_S = 0, COL_O = 256;    // S_w at 128 w + 64 c, O_w at 256 + 128 w
 };
 static_assert(Plan<128>::SMEM <= 232448, "shared memory plan too large");
@@ -276,7 +280,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
   extern __shared__ uint8_t raw[];
   __shared__ long long sums[kThreads];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  asm volatile("griddepcontrol.launch_dependents;");
+  // The next kernel is not let in early: the join's blocks would all take their places on
+  // the SMs that finish first (prompt 211 us against 202, chunk 255 against 240).
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // -- this block's range of tiles --------------------------------------------
@@ -382,10 +387,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
   };
   Reader reader;
 
-  // Registers per warpgroup: 2 * 168 + 96 + 80 = 4 * 128, the launch's share (allow_smem
-  // checks that the kernel was built with 128)
+  // Registers per warpgroup, together the launch's share of 4 * 128 (allow_smem checks
+  // that the kernel was built with 128).  The converters hold a K and a V row each, which
+  // at 8 bits does not fit in 80 (ragged prompts 224 us against 195); at 4 bits the softmax
+  // has more use for them (prompt 222 us against 224).
+  constexpr int kSoftRegs = BITS == 4 ? 176 : 168, kConvRegs = BITS == 4 ? 80 : 96, kRestRegs = 80;
+  static_assert(2 * kSoftRegs + kConvRegs + kRestRegs == 4 * 128, "register shares");
   if (warp < kSoftWarps) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     // ------------------------------------------------------------ softmax ----
     // Scores come as fragments: a thread (lane 4 g + t) holds rows g + 8 y of its
     // warp's 32 and two of every 8 columns, so a token's scales, read from shared
@@ -400,6 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     constexpr uint32_t kLane16 = 16u << 16;
     const uint32_t col_s = lanes + PL::COL_S + 128 * w, col_o = lanes + PL::COL_O + 128 * w;
+    int2 *limit = reinterpret_cast<int2 *>(sm + PL::OFF_LIM) + r0;
     uint32_t s_phase = 0;  // of the tile's barriers
     uint32_t tiles = 0;  // so far
     bool ok = true;
@@ -412,21 +422,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
         done_piece(reader);
         continue;
       }
-      // keys that row g + 8 y sees; rows past the item's: all
-      auto limits = [&](int y, int &lo, int &hi) {
-        const int r = r0 + 8 * y + g;
-        lo = 0;
-        hi = 0x7fffffff;
-        if (r < x.R) visible(p, x.len - x.nq + (x.qt * kRows + r) / p.group, x.len, lo, hi);
-      };
-      int lo_max = 0, hi_min = 0x7fffffff;
+      // keys that row r0 + lane sees (rows past the item's: all), for whoever holds it
+      int lo = 0, hi = 0x7fffffff;
+      if (r0 + lane < x.R) visible(p, x.len - x.nq + (x.qt * kRows + r0 + lane) / p.group, x.len, lo, hi);
+      limit[lane] = make_int2(lo, max(hi, 0));
+      const int lo_max = __reduce_max_sync(0xffffffffu, lo), hi_min = __reduce_min_sync(0xffffffffu, hi);
+      __syncwarp();
       float m[Y], l[Y][2];
 #pragma unroll
       for (int y = 0; y < Y; ++y) {
-        int lo, hi;
-        limits(y, lo, hi);
-        lo_max = max(lo_max, lo);
-        hi_min = min(hi_min, hi);
         m[y] = kNoRef;
         l[y][0] = l[y][1] = 0.f;
       }
@@ -464,18 +468,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
             }
           }
           const int jc = j + 64 * c;
-          if (__any_sync(0xffffffffu, lo_max > jc || hi_min < jc + 64)) {
+          if (hi_min < jc + 64) {
 #pragma unroll
             for (int y = 0; y < Y; ++y) {
-              int lo, hi;
-              limits(y, lo, hi);
-              lo -= jc + 2 * t;
-              hi -= jc + 2 * t;
+              const int end = limit[8 * y + g].y - jc - 2 * t;
 #pragma unroll
               for (int n = 0; n < 8; ++n)
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
-                  if (8 * n + e < lo || 8 * n + e >= hi) at(y, n)[e] = -CUDART_INF_F;
+                  if (8 * n + e >= end) at(y, n)[e] = -CUDART_INF_F;
+            }
+          }
+          if (lo_max > jc) {
+#pragma unroll
+            for (int y = 0; y < Y; ++y) {
+              const int begin = limit[8 * y + g].x - jc - 2 * t;
+#pragma unroll
+              for (int n = 0; n < 8; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  if (8 * n + e < begin) at(y, n)[e] = -CUDART_INF_F;
             }
           }
           float top[Y];
@@ -493,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
             for (int y = 0; y < Y; ++y) {
               top[y] = fmaxf(top[y], __shfl_xor_sync(0xffffffffu, top[y], 1));
               top[y] = fmaxf(top[y], __shfl_xor_sync(0xffffffffu, top[y], 2));
-              const float nm = top[y] > m[y] + kRoom ? top[y] - kHead : m[y];
+              const float nm = top[y] > m[y] + kRoom ? top[y] : m[y];
               a[y] = exp2_fast(m[y] - nm);
               m[y] = nm;
               l[y][0] *= a[y];
@@ -545,83 +557,72 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
         s_phase ^= 1u;
       }
       if (!ok) break;
-      // -- the item's (or piece's) end
-      float inv[Y];
-      long long row[Y];  // of the output; -1: past the item's rows
-      const bool whole = x.t0 == 0 && x.t1 == x.nt;
-      const long long part = static_cast<long long>(blockIdx.x) * 2 + (x.t0 == 0 ? 1 : 0);
-      float *part_at = parts + part * kRows * (D + 2);
+      // -- the item's (or piece's) end: lane 8 y + g takes the row that lanes 4 g .. + 3
+      // summed as their y, so that a lane's columns are consecutive and the code is
+      // short (it is fetched anew every time: exchanging the fragments' pairs among four
+      // lanes took 16000 cycles a piece)
+      float ms = 0.f, zs = 0.f;
 #pragma unroll
       for (int y = 0; y < Y; ++y) {
         float z = l[y][0] + l[y][1];
         z += __shfl_xor_sync(0xffffffffu, z, 1);
         z += __shfl_xor_sync(0xffffffffu, z, 2);
-        inv[y] = z == 0.f ? 0.f : 1.f / z;
-        const int r = r0 + 8 * y + g, ri = x.qt * kRows + r;
-        row[y] = r < x.R ? (static_cast<long long>(x.q0) + ri / p.group) * p.Hq + x.h * p.group + ri % p.group : -1;
-        if (t == 0 && r < x.R) {
-          if (!whole)
-            *reinterpret_cast<float2 *>(part_at + kRows * D + 2 * r) = make_float2(m[y], z);
-          else if (p.lse != nullptr)
-            p.lse[row[y]] = z == 0.f ? -CUDART_INF_F : (m[y] + log2f(z)) * kLn2;
+        z = __shfl_sync(0xffffffffu, z, 4 * (lane & 7));
+        const float my = __shfl_sync(0xffffffffu, m[y], 4 * (lane & 7));
+        if (lane >> 3 == y) {
+          zs = z;
+          ms = my;
         }
       }
-      if (!whole && x.t0 == 0 && threadIdx.x == 0) descs[blockIdx.x] = Desc{x.b, x.h, x.qt, x.last};
+      const int r = r0 + lane, ri = x.qt * kRows + r;
+      const bool in = r < x.R, whole = x.t0 == 0 && x.t1 == x.nt;
+      const long long row = (static_cast<long long>(x.q0) + ri / p.group) * p.Hq + x.h * p.group + ri % p.group;
+      const long long part = static_cast<long long>(blockIdx.x) * 2 + (x.t0 == 0 ? 1 : 0);
+      float *part_at = parts + part * kRows * (D + 2);
+      const float inv = zs == 0.f ? 0.f : 1.f / zs;
+      if (!whole) {
+        if (in) *reinterpret_cast<float2 *>(part_at + kRows * D + 2 * r) = make_float2(ms, zs);
+        if (x.t0 == 0 && threadIdx.x == 0) descs[blockIdx.x] = Desc{x.q0, x.h, x.qt, x.R, x.last};
+      } else if (in && p.lse != nullptr) {
+        p.lse[row] = zs == 0.f ? -CUDART_INF_F : (ms + log2f(zs)) * kLn2;
+      }
       ok = wait(o_done(w, 1), s_phase ^ 1u);
       if (!ok) break;
       tc_fence_after();
-#pragma unroll
-      for (int z16 = 0; z16 < 2; ++z16)
 #pragma unroll 1
-        for (int q = 0; q < D / 32; ++q) {
-          uint32_t v[16];
-          tmem_ld_frag4(col_o + 32 * q + z16 * kLane16, v);
-          tmem_wait_ld<16>(v);
+      for (int q = 0; q < D / 32; ++q) {
+        uint32_t v[32];
+        tmem_ld32(col_o + 32 * q, v);
+        tmem_wait_ld<32>(v);
+        if (!in) continue;
+        if (!whole) {
+          // four columns of every row, then the next four: the lanes' stores are
+          // consecutive.  (The columns' order stays; the join knows it.)
+          float4 *dst = reinterpret_cast<float4 *>(part_at) + 8 * q * kRows + r;
 #pragma unroll
-          for (int f = 0; f < 2; ++f) {
-            const int y = 2 * z16 + f;
-            if (!whole) {
-              // columns stay as they are (the join knows their order): a row's 32 bytes
-              // from four lanes
-              float *dst = part_at + (r0 + 8 * y + g) * D + 32 * q + 2 * t;
-              if (row[y] >= 0) {
+          for (int n = 0; n < 8; ++n)
+            dst[n * kRows] = make_float4(__uint_as_float(v[4 * n]), __uint_as_float(v[4 * n + 1]),
+                                 __uint_as_float(v[4 * n + 2]), __uint_as_float(v[4 * n + 3]));
+        } else {
+          uint4 *dst = reinterpret_cast<uint4 *>(p.out + row * D + 32 * q);
 #pragma unroll
-                for (int n = 0; n < 4; ++n)
-                  *reinterpret_cast<float2 *>(dst + 8 * n) =
-                      make_float2(__uint_as_float(v[4 * n + 2 * f]), __uint_as_float(v[4 * n + 2 * f + 1]));
-              }
-            } else {
-              // the four lanes of a row exchange pairs, so that lane t has the 8 columns
-              // of n = t: 64 contiguous bytes a row
-              uint32_t h[4], o[4];
-#pragma unroll
-              for (int n = 0; n < 4; ++n) {
-                const __half2 z = __floats2half2_rn(__uint_as_float(v[4 * n + 2 * f]) * inv[y],
-                                                    __uint_as_float(v[4 * n + 2 * f + 1]) * inv[y]);
-                h[n] = *reinterpret_cast<const uint32_t *>(&z);
-              }
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int n = t ^ k;  // what lane t ^ k is to have
-                const uint32_t z = n & 2 ? (n & 1 ? h[3] : h[2]) : (n & 1 ? h[1] : h[0]);
-                const uint32_t got = k ? __shfl_xor_sync(0xffffffffu, z, k) : z;
-#pragma unroll
-                for (int s = 0; s < 4; ++s)
-                  if (s == n) o[s] = got;  // lane s's pair of columns 2 s, 2 s + 1
-              }
-              uint4 z = make_uint4(o[0], o[1], o[2], o[3]);
-              if (BITS == 4)  // columns 2 s, 2 s + 1 are d = s and s + 4
-                z = make_uint4(__byte_perm(o[0], o[1], 0x5410), __byte_perm(o[2], o[3], 0x5410),
-                               __byte_perm(o[0], o[1], 0x7632), __byte_perm(o[2], o[3], 0x7632));
-              if (row[y] >= 0) *reinterpret_cast<uint4 *>(p.out + row[y] * D + 32 * q + 8 * t) = z;
-            }
+          for (int n = 0; n < 4; ++n) {
+            // at 4 bits columns 2 s, 2 s + 1 of an 8 are d = s and s + 4
+            auto pair = [&](int i) {
+              const int c0 = BITS == 4 ? (i < 2 ? 4 * i : 4 * i - 7) : 2 * i, c1 = BITS == 4 ? c0 + 2 : c0 + 1;
+              const __half2 z = __floats2half2_rn(__uint_as_float(v[8 * n + c0]) * inv,
+                                                  __uint_as_float(v[8 * n + c1]) * inv);
+              return *reinterpret_cast<const uint32_t *>(&z);
+            };
+            dst[n] = make_uint4(pair(0), pair(1), pair(2), pair(3));
           }
         }
+      }
       tc_fence_before();
       done_piece(reader);
     }
   } else if (warp < kSoftWarps + 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvRegs));
     // --------------------------------------------------------- converters ----
     // The scales have a third slot: a tile's are read until both halves' weights
     // are written, and slot s is refilled for tile i + 3 only once the K stage
@@ -727,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
       if (st == 0) phase ^= 1u;
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRestRegs));
     if (warp == kSoftWarps + 4) {
       // ------------------------------------------------------------- MMAs ----
       const uint32_t on = elect();
@@ -922,33 +923,38 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
-// Joins the partials of the items cut by the ranges: block (c, y) takes rows 8 y
-// .. + 7 of the item that starts in range c and ends in a later one, a warp a row.
+// Joins the partials of the items cut by the ranges: block (c, y) takes rows
+// kJoinRows y .. of the item that starts in range c and ends in a later one, a
+// thread eight columns of a row.  Most items have two pieces, one for each side of
+// a cut; the few of a short call with long keys have one for every range.  (A warp a
+// row and four pieces at a time, whether there or not, was bound by its
+// instructions and took 15 us of a prompt's.)
+constexpr int kJoinRows = 16;
+
 template <int BITS, int D>
-__global__ void __launch_bounds__(256) kv_prefill_join_kernel(const KvAttnParams p, int ranges) {
+__global__ void __launch_bounds__(kJoinRows * D / 8) kv_prefill_join_kernel(const KvAttnParams p, int ranges) {
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Desc de = reinterpret_cast<const Desc *>(p.ws)[blockIdx.x];
-  if (de.last < 0) return;
-  int q0, nq, len;
-  seq_of(p, de.b, q0, nq, len);
-  const int lane = threadIdx.x & 31, r = blockIdx.y * 8 + (threadIdx.x >> 5), ri = de.qt * kRows + r;
-  if (ri >= nq * p.group) return;
-  const Partials<D, kRows> ps{reinterpret_cast<const float *>(reinterpret_cast<const Desc *>(p.ws) + ranges),
-                              static_cast<int>(blockIdx.x)};
-  float4 o;
-  float m, l;
-  join_row<D, kRows, 4>(ps, r, blockIdx.x, 1, de.last, lane, o, m, l);
-  if (BITS == 4) {
-    // columns 0 .. 7 of an 8 are d = 0, 4, 1, 5, 2, 6, 3, 7: the lane of the first four
-    // gives d 4, 5 for d 2, 3
-    const bool odd = lane & 1;
-    const float a = __shfl_xor_sync(0xffffffffu, odd ? o.x : o.y, 1);
-    const float b = __shfl_xor_sync(0xffffffffu, odd ? o.z : o.w, 1);
-    o = odd ? make_float4(a, b, o.y, o.w) : make_float4(o.x, o.z, a, b);
+  const int first = blockIdx.x;
+  const Desc de = reinterpret_cast<const Desc *>(p.ws)[first];
+  const int r = blockIdx.y * kJoinRows + threadIdx.x % kJoinRows;
+  const int c = threadIdx.x / kJoinRows;  // of 8 columns
+  const Partials<D, kRows> ps{reinterpret_cast<const float *>(reinterpret_cast<const Desc *>(p.ws) + ranges), first};
+  JoinedRow<2> x;
+  const int at = (2 * c * kRows + r) * 4;
+  // where the first two pieces would be is known before the item is
+  join_pieces<2>(ps, r, at, 4 * kRows, first, 1, min(first + 1, ranges - 1), x);
+  if (de.last < 0 || r >= de.R) return;
+  for (int i = first + 2; i <= de.last; i += 4) join_pieces<4>(ps, r, at, 4 * kRows, i, 1, de.last, x);
+  const int ri = de.qt * kRows + r;
+  const long long row = (static_cast<long long>(de.q0) + ri / p.group) * p.Hq + de.h * p.group + ri % p.group;
+  float4 a = x.o[0], b = x.o[1];
+  if (BITS == 4) {  // columns 2 s, 2 s + 1 are d = s and s + 4
+    a = make_float4(x.o[0].x, x.o[0].z, x.o[1].x, x.o[1].z);
+    b = make_float4(x.o[0].y, x.o[0].w, x.o[1].y, x.o[1].w);
   }
-  const long long row = (static_cast<long long>(q0) + ri / p.group) * p.Hq + de.h * p.group + ri % p.group;
-  if (lane * 4 < D) store_row4<D>(p, row, lane * 4, o, m, l);
+  store_row4<D>(p, row, 8 * c, a, x.m, x.l);
+  store_row4<D>(p, row, 8 * c + 4, b, x.m, x.l);
 }
 
 template <int BITS, int D>
@@ -993,8 +999,8 @@ int launch_t(const KvAttnParams &p, cudaStream_t s) {
     return W8A8_ERR_CUDA;
   }
   if (tiles > 1) {  // else no item can be cut
-    cfg.gridDim = dim3(static_cast<unsigned>(grid), kRows / 8);
-    cfg.blockDim = dim3(256);
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), kRows / kJoinRows);
+    cfg.blockDim = dim3(kJoinRows * D / 8);
     cfg.dynamicSmemBytes = 0;
     if (cudaLaunchKernelEx(&cfg, kv_prefill_join_kernel<BITS, D>, p, grid) != cudaSuccess) {
       cudaGetLastError();
