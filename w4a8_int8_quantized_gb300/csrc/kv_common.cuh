@@ -71,13 +71,19 @@ __device__ __forceinline__ void visible(const KvAttnParams &p, int pos, int len,
   lo = p.window > 0 ? max(pos + 1 - p.window, 0) : 0;
 }
 
+__device__ __forceinline__ int entry_of(const KvAttnParams &p, int b, int i) {
+  return __ldg(p.table + static_cast<long long>(b) * p.table_w + i);
+}
+
 // Page of a table entry; an entry outside the cache reads as -1 (its tokens
 // are left out) and is reported.
-__device__ __forceinline__ int page_of(const KvAttnParams &p, int b, int i) {
-  const int e = __ldg(p.table + static_cast<long long>(b) * p.table_w + i);
+__device__ __forceinline__ int checked_page(const KvAttnParams &p, int e) {
   if (static_cast<unsigned>(e) < static_cast<unsigned long long>(p.kv.pages)) return e;
   if (p.kv.err != nullptr) atomicCAS(p.kv.err, 0u, static_cast<unsigned>(kDevErrIndex));
   return -1;
+}
+__device__ __forceinline__ int page_of(const KvAttnParams &p, int b, int i) {
+  return checked_page(p, entry_of(p, b, i));
 }
 
 // ---- exact conversion of codes to fp16 --------------------------------------

@@ -389,9 +389,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
 
   // Registers per warpgroup, together the launch's share of 4 * 128 (allow_smem checks
   // that the kernel was built with 128).  The converters hold a K and a V row each, which
-  // at 8 bits does not fit in 80 (ragged prompts 224 us against 195); at 4 bits the softmax
-  // has more use for them (prompt 222 us against 224).
-  constexpr int kSoftRegs = BITS == 4 ? 176 : 168, kConvRegs = BITS == 4 ? 80 : 96, kRestRegs = 80;
+  // at 8 bits does not fit in 80 (ragged prompts 177 us against 128).
+  constexpr int kSoftRegs = 168, kConvRegs = 96, kRestRegs = 80;
   static_assert(2 * kSoftRegs + kConvRegs + kRestRegs == 4 * 128, "register shares");
   if (warp < kSoftWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
@@ -627,8 +626,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
     // The scales have a third slot: a tile's are read until both halves' weights
     // are written, and slot s is refilled for tile i + 3 only once the K stage
     // of tile i + 1 is free, whose scores are issued after those weights.
-    constexpr int ROW = D * BITS / 8, NV = ROW / 16;  // 16-byte vectors of a token
-    const int tok = (warp - kSoftWarps) * 32 + lane;
+    // A lane owns a token's scales; the codes of a warp's 32 tokens lie in two runs of
+    // 16 (a page holds a multiple of 16), read 512 consecutive bytes at a time.  Which
+    // 16 of them a lane takes is chosen so that 8 lanes' stores of one chunk each, of
+    // 8 / VPS rows, fall into different banks.  (With a token a lane, whose loads touch
+    // 32 lines each, ragged prompts at 8 bits took 149 us against 128.)
+    constexpr int ROW = D * BITS / 8, NV = ROW / 16;  // bytes of a token; a lane's vectors
+    constexpr int VPS = BITS / 2, RP = 8 / VPS;       // vectors of 64 d; rows of 8 lanes
+    constexpr int RL = 512 / ROW, CPV = 16 / BITS;    // rows of a load; chunks of a vector
+    const int cw = warp - kSoftWarps, tok = cw * 32 + lane;
+    const int vrow = (lane >> 3) / PL::SUBS * RP + lane / VPS % RP;
+    const int vk = (lane >> 3) % PL::SUBS * VPS + lane % VPS;
+    const uint32_t lane_at = chunk_at(cw * 32 + vrow, CPV * vk);
+    const int lane_from = vrow * ROW + vk * 16;
     const Nibbles nib;
     int st = 0, slot = 0;
     uint32_t phase = 1;  // the first wait on an empty stage passes
@@ -638,66 +648,74 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const uint32_t y[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        // token 16 (i / (NV / 2)) + RL (i % (NV / 2)) + vrow of the warp's
+        const int t0 = 16 * (i / (NV / 2)) + RL * (i % (NV / 2));
+        const uint32_t at = (stage + lane_at) ^ ((t0 & 7) << 4);
         if (BITS == 4) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             uint32_t o[4];
             nib.to_h(y[e], o);
-            sts4(stage + chunk_at(tok, 4 * i + e), make_uint4(o[0], o[1], o[2], o[3]));
+            sts4((at ^ (e << 4)) + 128 * t0, make_uint4(o[0], o[1], o[2], o[3]));
           }
         } else {
 #pragma unroll
-          for (int e = 0; e < 4; e += 2) {
+          for (int e = 0; e < 2; ++e) {
             uint4 o;
-            bytes_to_h(y[e], o.x, o.y);
-            bytes_to_h(y[e + 1], o.z, o.w);
-            sts4(stage + chunk_at(tok, 2 * i + e / 2), o);
+            bytes_to_h(y[2 * e], o.x, o.y);
+            bytes_to_h(y[2 * e + 1], o.z, o.w);
+            sts4((at ^ (e << 4)) + 128 * t0, o);
           }
         }
       }
     };
     // The codes of the next K are fetched when this tile's are converted, those of
     // the next V likewise, so that memory's latency lies under the other's work.
-    // (Loads of 8 whole rows side by side instead of a row a lane were a quarter slower
-    // overall: one warp a scheduler is bound by its instructions.)
     // The tile to fetch: its sequence, head, this lane's token, where the keys
-    // end, and the piece's tiles after it.
-    int tb = 0, th = 0, ta = 0, tend = 0, left = 0;
+    // end, and the piece's tiles after it; and the table's entry of the token's page,
+    // itself fetched a tile ahead.
+    int tb = 0, th = 0, ta = 0, tend = 0, left = 0, entry = 0;
     auto advance = [&]() {
       if (left > 0) {
         ta += kKeys;
         --left;
-        return true;
+      } else {
+        Piece x;
+        if (!next_piece(reader, x)) return false;
+        tb = x.b;
+        th = x.h;
+        ta = x.first + x.t0 * kKeys + tok;
+        tend = min(x.hi_max, x.len);
+        left = x.t1 - x.t0 - 1;
       }
-      Piece x;
-      if (!next_piece(reader, x)) return false;
-      tb = x.b;
-      th = x.h;
-      ta = x.first + x.t0 * kKeys + tok;
-      tend = min(x.hi_max, x.len);
-      left = x.t1 - x.t0 - 1;
+      if (ta < tend) entry = entry_of(p, tb, ta >> p.kv.page_shift);
       return true;
     };
-    uint4 kv[NV], vv[NV];
+    uint4 kv[NV] = {}, vv[NV] = {};
     float ks = 0.f, vs = 0.f;
-    long long row = -1;  // of the token in the cache; -1: left out
+    long long row = -1;              // of the token in the cache; -1: left out
+    long long run[2] = {-1, -1};     // of the warp's tokens 0 and 16
+    // Codes of tokens that are left out are any: they are finite, and weigh nothing
     auto load = [&](const uint8_t *codes, uint4 (&v)[NV]) {
 #pragma unroll
-      for (int e = 0; e < NV; ++e) {
-        v[e] = make_uint4(0, 0, 0, 0);
-        if (row >= 0) v[e] = __ldg(reinterpret_cast<const uint4 *>(codes + row * ROW) + e);
-      }
+      for (int e = 0; e < NV; ++e)
+        if (run[e / (NV / 2)] >= 0)
+          v[e] = __ldg(reinterpret_cast<const uint4 *>(codes + run[e / (NV / 2)] * ROW + lane_from + 512 * (e % (NV / 2))));
     };
+    bool ahead = advance();  // whether that tile is there
     auto load_k = [&]() {
-      const int page = ta < tend ? page_of(p, tb, ta >> p.kv.page_shift) : -1;
+      const int page = ta < tend ? checked_page(p, entry) : -1;
       row = page < 0 ? -1 : p.kv.row(page, th) + (ta & pmask);
+      run[0] = __shfl_sync(0xffffffffu, row, 0);
+      run[1] = __shfl_sync(0xffffffffu, row, 16);
       load(p.kv.kc, kv);
       if (row >= 0) {
         ks = __ldg(p.kv.ks + row);
         vs = __ldg(p.kv.vs + row);
       }
+      ahead = advance();
     };
-    bool have = advance();
+    bool have = ahead;
     if (have) {
       load_k();
       load(p.kv.vc, vv);
@@ -714,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(k_full(st));
-      have = advance();
+      have = ahead;
       if (have) load_k();
       ok = wait(v_empty(st), phase);
       if (!ok) break;
