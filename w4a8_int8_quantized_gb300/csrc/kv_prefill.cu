@@ -859,15 +859,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
         constexpr int C = D / 8, RPS = 32 / C;  // rows per step of the warp
         const int c = lane % C;
         const uint32_t dst = base + PL::OFF_Q + w * PL::TILE;
+        // row ri's query and head, then those of RPS rows on (a division a row made this
+        // the longest part of a short item)
+        const int ri = x.qt * kRows + w * 128 + lane / C, dt = RPS / p.group, dg = RPS % p.group;
+        int tk = x.q0 + ri / p.group, gh = ri % p.group;
+        const __half *q_h = p.q + static_cast<long long>(x.h * p.group) * p.q_hs + 8 * c;
 #pragma unroll 4
         for (int rr = lane / C; rr < 128; rr += RPS) {
           const bool in = w * 128 + rr < x.R;
-          const int ri = x.qt * kRows + (in ? w * 128 + rr : 0);
-          const __half *src = p.q + (x.q0 + ri / p.group) * p.q_ts +
-                              static_cast<long long>(x.h * p.group + ri % p.group) * p.q_hs + 8 * c;
+          const __half *src = in ? q_h + tk * p.q_ts + gh * p.q_hs : p.q;
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + chunk_at(rr, c)), "l"(src),
                        "r"(in ? 16 : 0)
                        : "memory");
+          tk += dt;
+          gh += dg;
+          if (gh >= p.group) {
+            gh -= p.group;
+            ++tk;
+          }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
         if (BITS == 4) {  // this lane's own chunks, d in the order 0, 4, 1, 5, 2, 6, 3, 7
