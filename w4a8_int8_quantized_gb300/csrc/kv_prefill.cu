@@ -22,8 +22,7 @@
 //
 // Operands: Q and K are K-major.  V keeps its token rows and is read as the
 // MN-major operand, so nothing is transposed.  At 4 bits the converter's pairs
-// (d, d + 4) permute the d of each 8; Q is stored with the same permutation and
-// the output undoes it for V.
+// (d, d + 4) permute the d of each 8 of V; the output undoes it.
 //
 // Softmax, with the codes exact and both scales in fp32: u = S (scale log2e s_k)
 // + log2 s_v, p = 2^(u - M), O = sum p code_v, l = sum p / s_v.  M is the lazy
@@ -52,9 +51,9 @@ constexpr int kSoftWarps = 8, kWarps = kSoftWarps + 8, kThreads = 32 * kWarps;
 constexpr int kRows = 256;  // of an item
 constexpr int kKeys = 128;  // of a tile
 constexpr int kRing = 4;    // published pieces
-// An item's start and end, in tiles, for the split (a prompt of 4516 tokens: 3 276 us,
-// 4 240, 5 227, 6 230, 8 235).
-constexpr int kItemCost = 5;
+// An item's start and end, in tiles, for the split (a prompt of 4516 tokens and six
+// ragged ones: 3 167 and 122 us, 4 170 and 124, 5 171 and 127).
+constexpr int kItemCost = 3;
 
 // A piece of an item: its tiles t0 .. t1 - 1 of nt.
 struct Piece {
@@ -644,7 +643,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
     uint32_t phase = 1;  // the first wait on an empty stage passes
     const int pmask = (1 << p.kv.page_shift) - 1;
     bool ok = true;
-    auto convert = [&](const uint4 (&v)[NV], uint32_t stage) {
+    // The nibble trick gives pairs (d, d + 4).  K's are put in order, since permuting Q
+    // instead delays an item's start; V's stay, and the output undoes them.
+    auto convert = [&](const uint4 (&v)[NV], uint32_t stage, bool order) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const uint32_t y[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
@@ -656,6 +657,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
           for (int e = 0; e < 4; ++e) {
             uint32_t o[4];
             nib.to_h(y[e], o);
+            if (order) {
+              const uint32_t z[4] = {__byte_perm(o[0], o[1], 0x5410), __byte_perm(o[2], o[3], 0x5410),
+                                     __byte_perm(o[0], o[1], 0x7632), __byte_perm(o[2], o[3], 0x7632)};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) o[i] = z[i];
+            }
             sts4((at ^ (e << 4)) + 128 * t0, make_uint4(o[0], o[1], o[2], o[3]));
           }
         } else {
@@ -723,7 +730,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
     while (ok && have) {
       ok = wait(k_empty(st), phase);
       if (!ok) break;
-      convert(kv, base + PL::OFF_K + st * PL::TILE);
+      convert(kv, base + PL::OFF_K + st * PL::TILE, true);
       const uint32_t sc = base + PL::OFF_S + slot * (3 * kKeys * 4) + tok * 4;
       const float sv = vs == 0.f ? 1.f : vs;  // s_v = 0: all codes 0, any scale will do
       sts1(sc, row < 0 ? 0.f : ks * (p.scale * kLog2e));
@@ -736,7 +743,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
       if (have) load_k();
       ok = wait(v_empty(st), phase);
       if (!ok) break;
-      convert(vv, base + PL::OFF_V + st * PL::TILE);
+      convert(vv, base + PL::OFF_V + st * PL::TILE, false);
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(v_full(st));
@@ -852,43 +859,36 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
       Piece x;
       while (next_piece(reader, x)) {
         if (x.R <= w * 128) continue;
+        // where the half's rows lane, lane + 32, ... are (in elements; -1: beyond the
+        // item's, zero): found before Q is free, since from there on every cycle delays
+        // the item's first scores
+        long long from[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int r = w * 128 + 32 * k + lane, ri = x.qt * kRows + r;
+          from[k] = r < x.R ? (x.q0 + ri / p.group) * p.q_ts +
+                                  static_cast<long long>(x.h * p.group + ri % p.group) * p.q_hs
+                            : -1;
+        }
         if (!wait(q_empty(w), phase)) break;
         phase ^= 1u;
-        // all rows in flight at once (by way of registers it took 8 round trips);
-        // rows beyond the item's are zero; a lane takes chunk lane % (D / 8) of every row
-        constexpr int C = D / 8, RPS = 32 / C;  // rows per step of the warp
+        // all rows in flight at once (by way of registers it took 8 round trips); a lane
+        // takes chunk lane % C of every row.  (With the addresses worked out at each step
+        // the issue alone took 8000 to 13000 cycles;
+        // four steps at a time instead of all, a prompt takes 168 us against 165.)
+        constexpr int C = D / 8, RPS = 32 / C;  // chunks of a row; rows per step of the warp
         const int c = lane % C;
         const uint32_t dst = base + PL::OFF_Q + w * PL::TILE;
-        // row ri's query and head, then those of RPS rows on (a division a row made this
-        // the longest part of a short item)
-        const int ri = x.qt * kRows + w * 128 + lane / C, dt = RPS / p.group, dg = RPS % p.group;
-        int tk = x.q0 + ri / p.group, gh = ri % p.group;
-        const __half *q_h = p.q + static_cast<long long>(x.h * p.group) * p.q_hs + 8 * c;
-#pragma unroll 4
-        for (int rr = lane / C; rr < 128; rr += RPS) {
-          const bool in = w * 128 + rr < x.R;
-          const __half *src = in ? q_h + tk * p.q_ts + gh * p.q_hs : p.q;
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + chunk_at(rr, c)), "l"(src),
-                       "r"(in ? 16 : 0)
-                       : "memory");
-          tk += dt;
-          gh += dg;
-          if (gh >= p.group) {
-            gh -= p.group;
-            ++tk;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int i = 0; i < 32; i += RPS) {
+            const long long f = __shfl_sync(0xffffffffu, from[k], i + lane / C);
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + chunk_at(32 * k + i + lane / C, c)),
+                         "l"(p.q + (f < 0 ? 0 : f + 8 * c)), "r"(f < 0 ? 0 : 16)
+                         : "memory");
           }
-        }
         asm volatile("cp.async.wait_all;" ::: "memory");
-        if (BITS == 4) {  // this lane's own chunks, d in the order 0, 4, 1, 5, 2, 6, 3, 7
-#pragma unroll 4
-          for (int rr = lane / C; rr < 128; rr += RPS) {
-            const uint32_t a = dst + chunk_at(rr, c);
-            uint4 v;
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-            sts4(a, make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
-                               __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632)));
-          }
-        }
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(q_full(w));
