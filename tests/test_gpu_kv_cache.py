@@ -396,6 +396,16 @@ def test_rows_around_the_change_of_kernel(new, group):
 
 @pytest.mark.parametrize("bits", [4, 8])
 @pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("new", [[16], [17], [32], [33]])
+def test_rows_around_the_change_of_kernel_by_type(bits, D, new):
+    rng = np.random.default_rng(bits + D + new[0])
+    c = Cache(rng, [333], 2, D, 16, bits)
+    q = rows(rng, new[0], 2, D)
+    check(c, q, new, *attend(c, q, new, max_q=new[0]))
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("new,window,causal", [([40], 0, True), ([70], 0, False), ([33, 12], 4000, True), ([300], 700, True)])
 def test_long_keys_cut_between_blocks(bits, D, new, window, causal):
     """Items whose keys many blocks share; the joined result is the same each time."""

@@ -121,8 +121,8 @@ size_t kv_cache_attention_workspace_bytes(int T, int q_heads, int B, int max_q, 
     return 0;
   if (T == 0 || B == 0) return 0;
   const long long rows = static_cast<long long>(max_q < T ? max_q : T) * (q_heads / cache->kv_heads);
-  return rows <= kFewRows ? kv_decode_workspace(cache->head_dim, rows)
-                          : kv_prefill_workspace(cache->head_dim);
+  return rows <= few_rows(cache->bits, cache->head_dim) ? kv_decode_workspace(cache->head_dim, rows)
+                                                              : kv_prefill_workspace(cache->head_dim);
 }
 
 int kv_cache_attention(const w8a8_half *q, long long q_token_stride, long long q_head_stride,
@@ -174,7 +174,7 @@ int kv_cache_attention(const w8a8_half *q, long long q_token_stride, long long q
   p.out = reinterpret_cast<__half *>(out);
   p.lse = lse;
   p.ws = static_cast<float *>(workspace);
-  const bool few = static_cast<long long>(max_q) * p.group <= kFewRows;
+  const bool few = static_cast<long long>(max_q) * p.group <= few_rows(cache->bits, cache->head_dim);
   return (few ? launch_kv_decode : launch_kv_prefill)(p, cache->bits, cache->head_dim,
                                                       static_cast<cudaStream_t>(stream));
 }

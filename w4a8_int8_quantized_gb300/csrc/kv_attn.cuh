@@ -91,10 +91,16 @@ __device__ __forceinline__ void join_pieces(const Partials<D, ROWS> &ps, int r, 
 }
 
 // Rows per kv head and sequence up to which the few-row kernel runs, else the
-// tensor-memory one.  Measured (8 kv heads, D = 128, 4 bits; 16 sequences of 4000
-// tokens): 32 rows 57 us against 84, 64 rows 98 against 86; one sequence of 32768:
-// 37 against 48, and 57 against 51.
-constexpr int kFewRows = 32;
+// tensor-memory one.  It works through 16 rows at a time, so its time goes up in
+// steps of 16.  Measured with 8 kv heads, 16 sequences of 4000 tokens (us, few rows
+// against many):
+//              16 rows   24 to 32   33 to 64
+//   4 bits, 128   37, 60    57, 61    98, 62
+//   8 bits, 128   46, 68    72, 68   129, 69
+//   4 bits,  64   37, 51    55, 51    93, 52
+//   8 bits,  64   29, 51    43, 51    71, 51
+// One sequence of 32768 tokens and 64 of 1000 give the same picture.
+constexpr int few_rows(int bits, int D) { return bits * D == 512 ? 32 : 16; }
 
 size_t kv_decode_workspace(int D, long long rows);
 int launch_kv_decode(const KvAttnParams &p, int bits, int D, cudaStream_t s);
