@@ -35,6 +35,11 @@
 // cut into equal ranges, one per SM, whatever the lengths, the causal triangle
 // and the number of items; an item cut by ranges leaves fp32 partials that a
 // second kernel joins in order.
+//
+// Measured (8 kv heads of 4 rows, D = 128, 4 bits): 512 tokens behind 32256 215 us,
+// 1.27 PFLOP/s, 0.67 of a measured dense product; a prompt of 4516 tokens 165 us, 1.01.
+// A tile takes about 3700 cycles: shared memory is busy for 3300 of them (see the
+// softmax), the tensor pipe for 2048.  An item's start and end add about 9000.
 #include <math_constants.h>
 
 #include <mutex>
@@ -399,8 +404,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
     // memory, serve four rows.  Shared memory is the tightest resource here: per
     // tile the MMAs read 256 KB of operands (2048 cycles), the converters write 64
     // and these reads take 96; two rows a thread on twice the warps doubles them
-    // (512 tokens behind 32256: 283 us against 263), one row a thread with
-    // 16-byte broadcasts quadruples them.
+    // (512 tokens behind 32256: 283 us against 263 when it was tried), one row a
+    // thread with 16-byte broadcasts quadruples them.
     constexpr int Y = 4;  // rows of a thread: g + 8 y
     const int w = warp >> 2, g = lane >> 2, t = lane & 3;
     const int r0 = w * 128 + (warp & 3) * 32;  // the warp's first row
@@ -445,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
 #pragma unroll 1
         for (int c = 0; c < 2; ++c, sc += kKeys / 4) {
           // the token scales are there too: they precede K's arrival, which these
-          // scores waited for (a barrier of their own: 2 us of 227)
+          // scores waited for (a barrier of their own cost 1 %)
           ok = wait(s_full(w, c), s_phase);
           if (!ok) break;
           tc_fence_after();
@@ -955,7 +960,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
 // thread eight columns of a row.  Most items have two pieces, one for each side of
 // a cut; the few of a short call with long keys have one for every range.  (A warp a
 // row and four pieces at a time, whether there or not, was bound by its
-// instructions and took 15 us of a prompt's.)
+// instructions and took 15 us of a prompt; 9 now.)
 constexpr int kJoinRows = 16;
 
 template <int BITS, int D>
