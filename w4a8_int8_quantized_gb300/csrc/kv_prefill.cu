@@ -247,6 +247,13 @@ __device__ __forceinline__ void sts1(uint32_t a, float v) {
   asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
 }
 
+// Counts of units are 64 bits wide but rarely that large, and a 64-bit division takes
+// hundreds of cycles of a call's start.
+__device__ __forceinline__ long long div_units(long long a, long long b) {
+  if (((a | b) >> 31) == 0) return static_cast<unsigned>(a) / static_cast<unsigned>(b);
+  return a / b;
+}
+
 // Rows and tiles of entity e = sequence * nqt + row block; 0 tiles: no rows.
 struct Entity {
   int b, qt, R, q0, nq, len, first, hi_max, nt;
@@ -282,7 +289,8 @@ template <int BITS, int D>
 __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnParams p) {
   using PL = Plan<D>;
   extern __shared__ uint8_t raw[];
-  __shared__ long long sums[kThreads];
+  __shared__ long long sums[kWarps], first_at;  // of the warps; units before the first entity
+  __shared__ int first_e;                       // the entity of this block's first unit, or one before
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // The next kernel is not let in early: the join's blocks would all take their places on
   // the SMs that finish first (prompt 211 us against 202, chunk 255 against 240).
@@ -291,31 +299,35 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
   // -- this block's range of tiles --------------------------------------------
   const int nqt = static_cast<int>((static_cast<long long>(p.max_q) * p.group + kRows - 1) / kRows);
   const int entities = p.B * nqt, per_thread = (entities + kThreads - 1) / kThreads;
-  {
-    long long x = 0;
-    for (int i = 0; i < per_thread; ++i) {
-      const int e = threadIdx.x * per_thread + i;
-      if (e < entities) x += entity_of(p, nqt, e).cost() * p.kv.heads;
-    }
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    sums[threadIdx.x] = x;
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) x += sums[w * 32 + 31];
-    __syncthreads();
-    sums[threadIdx.x] = x;
-    __syncthreads();
+  long long mine = 0, upto = 0;  // units of this thread's entities, and of all up to them
+  for (int i = 0; i < per_thread; ++i) {
+    const int e = threadIdx.x * per_thread + i;
+    if (e < entities) mine += entity_of(p, nqt, e).cost() * p.kv.heads;
   }
-  const long long total = sums[kThreads - 1];
-  const long long per = (total + gridDim.x - 1) / gridDim.x;
+  upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += y;
+  }
+  if (lane == 31) sums[warp] = upto;
+  __syncthreads();
+  long long total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w == warp) upto += total;
+    total += sums[w];
+  }
+  const long long per = div_units(total + gridDim.x - 1, gridDim.x);
   const long long c0 = blockIdx.x * per, c1 = min(c0 + per, total);
   Desc *descs = reinterpret_cast<Desc *>(p.ws);
   float *parts = reinterpret_cast<float *>(descs + gridDim.x);
   if (threadIdx.x == 0) descs[blockIdx.x].last = -1;
   if (c0 >= c1) return;
+  if (upto - mine <= c0 && c0 < upto) {
+    first_e = threadIdx.x * per_thread;
+    first_at = upto - mine;
+  }
 
   const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
   uint8_t *sm = raw + (base - smem_u32(raw));
@@ -900,13 +912,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
       }
     } else {
       // ---------------------------------------------------------- the walk ----
-      int lo = 0, hi = kThreads - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (sums[mid] > c0) hi = mid; else lo = mid + 1;
-      }
-      int e = lo * per_thread;
-      long long start = lo > 0 ? sums[lo - 1] : 0;  // first tile of entity e
+      int e = first_e;
+      long long start = first_at;  // first unit of entity e
       Entity en = entity_of(p, nqt, e);
       Reader slot;
       uint32_t phase = 1;
@@ -920,7 +927,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
             start += en.cost() * p.kv.heads;
             en = entity_of(p, nqt, ++e);
           }
-          h = static_cast<int>((at - start) / en.cost());
+          h = static_cast<int>(div_units(at - start, en.cost()));
           istart = start + h * en.cost();
           t0 = static_cast<int>(max(at - istart - kItemCost, 0LL));
           t1 = static_cast<int>(max(min(en.cost(), c1 - istart) - kItemCost, 0LL));
@@ -934,7 +941,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
         } else {
           if (lane == 0)
             pieces[slot.i] = Piece{en.b, h, en.qt, en.R, en.q0, en.nq, en.len, en.first, en.hi_max,
-                                   t0, t1, en.nt, static_cast<int>((istart + en.cost() - 1) / per)};
+                                   t0, t1, en.nt, static_cast<int>(div_units(istart + en.cost() - 1, per))};
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(piece_full(slot.i));
