@@ -462,6 +462,27 @@ def test_pages_in_order_and_out_of_order():
             assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("bits,D", [(4, 128), (4, 64), (8, 128), (8, 64)])
+@pytest.mark.parametrize("new,group", [([32], 1), ([9, 32, 19], 1), ([8], 4), ([16], 2), ([60], 1)])
+def test_scales_left_by_an_earlier_call(bits, D, new, group):
+    """On-chip memory full of another call's NaN scales: keys that no row of a block
+    sees are not fetched, and what is there instead must not count."""
+    rng = np.random.default_rng(bits + D + sum(new))
+    dirt = w8.KVCache.empty(2000, 2, 16, D, bits)
+    dirt.k_codes.zero_()
+    dirt.v_codes.zero_()
+    dirt.k_scale.fill_(float("nan"))
+    dirt.v_scale.fill_(float("nan"))
+    table = torch.arange(2000, dtype=torch.int32, device="cuda")[None].repeat(4, 1)
+    c = Cache(rng, [39, 41, 300][:len(new)], 2, D, 32, bits)
+    q = rows(rng, sum(new), 2 * group, D)
+    for _ in range(3):
+        x = torch.zeros(4 * new[0], 2 * group, D, dtype=torch.float16, device="cuda")
+        w8.kv_cache_attention(x, dirt, table, torch.full((4,), 32000, dtype=torch.int32, device="cuda"),
+                              q_offsets=torch.arange(5, dtype=torch.int32, device="cuda") * new[0], max_q=max(new))
+        check(c, q, new, *attend(c, q, new, max_q=max(new)))
+
+
 def test_refusals():
     c = w8.KVCache.empty(4, 2, 16, 64)
     table = torch.zeros(1, 4, dtype=torch.int32, device="cuda")

@@ -340,7 +340,8 @@ struct Math {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const int a = j + 16 * i + 8 * r + tokg;
-          const bool out = a >= it.len || it.gone(p, a);
+          // from hi_max on nothing was copied: the stage holds an older step's scales
+          const bool out = a >= it.hi_max || it.gone(p, a);
           if (out) rv[i][r] = 0.f;
 #pragma unroll
           for (int n = 0; n < NT; ++n)
