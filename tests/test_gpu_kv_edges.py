@@ -1,0 +1,26 @@
+"""The quantized cache's attention where it is easy to get wrong: items that end
+inside a warp, waits that give up, weights far apart, rows that nobody owns.
+References and tolerances are those of kv_reference."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+from test_gpu_kv_cache import Cache, attend, check, rows  # noqa: E402
+
+if torch.cuda.is_available():
+    import w4a8_int8_quantized_gb300 as w8
+
+
+@pytest.mark.parametrize("bits,D", [(4, 128), (8, 64)])
+@pytest.mark.parametrize("new", [[33, 65, 95], [127, 129, 1], [161, 255, 257]])
+@pytest.mark.parametrize("behind", [0, 2500])
+def test_rows_that_do_not_fill_a_warp(bits, D, new, behind):
+    """Lanes without a row leave the warp's stores early and have to be back for its
+    next tensor-memory load; whole items, and items cut between blocks."""
+    rng = np.random.default_rng(bits + D + sum(new) + behind)
+    c = Cache(rng, [n + behind for n in new], 1, D, 64, bits)
+    q = rows(rng, sum(new), 1, D)
+    check(c, q, new, *attend(c, q, new, max_q=max(new)))
+    assert w8.w8a8_check_status() == 0

@@ -603,14 +603,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
       }
       ok = wait(o_done(w, 1), s_phase ^ 1u);
       if (!ok) break;
+      __syncwarp();  // lanes without a row skipped the stores above
       tc_fence_after();
 #pragma unroll 1
       for (int q = 0; q < D / 32; ++q) {
         uint32_t v[32];
         tmem_ld32(col_o + 32 * q, v);
         tmem_wait_ld<32>(v);
-        if (!in) continue;
-        if (!whole) {
+        if (in && !whole) {
           // four columns of every row, then the next four: the lanes' stores are
           // consecutive.  (The columns' order stays; the join knows it.)
           float4 *dst = reinterpret_cast<float4 *>(part_at) + 8 * q * kRows + r;
@@ -618,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
           for (int n = 0; n < 8; ++n)
             dst[n * kRows] = make_float4(__uint_as_float(v[4 * n]), __uint_as_float(v[4 * n + 1]),
                                  __uint_as_float(v[4 * n + 2]), __uint_as_float(v[4 * n + 3]));
-        } else {
+        } else if (in) {
           uint4 *dst = reinterpret_cast<uint4 *>(p.out + row * D + 32 * q);
 #pragma unroll
           for (int n = 0; n < 4; ++n) {
@@ -632,6 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
             dst[n] = make_uint4(pair(0), pair(1), pair(2), pair(3));
           }
         }
+        __syncwarp();  // lanes without a row rejoin: the next TMEM load is the whole warp's
       }
       tc_fence_before();
       done_piece(reader);
