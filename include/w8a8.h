@@ -256,10 +256,11 @@ int w8a8_gemm_i32(const int8_t *xq, const void *Wq, int M, int N, int K,
                   w8a8_stream_t stream);
 
 /* Test hook of the failure path (the method has no counterpart): sets, for
- * the tensor-core GEMM launches that follow (every entry point that runs
- * it), the limit of its bounded device-side waits in SM clock cycles
- * (0 = the default, about 2 s) and, with skip_first_copy = 1, leaves the
- * first weight-staging copy of each CTA unissued, so that the wait for it
+ * the launches of the tensor-core GEMM and of the cache attention that
+ * follow (every entry point that runs them), the limit of their bounded
+ * device-side waits in SM clock cycles (0 = the default, about 2 s) and,
+ * with skip_first_copy = 1, leaves the first weight-staging copy, or copy or
+ * hand-over of keys, of each CTA out, so that the wait for it
  * gives up: the kernel then returns early, its outputs are undefined, and
  * w8a8_check_status() reports W8A8_ERR_TIMEOUT.  No fault, trap or hang is
  * involved; the kernel still lets every copy it issued land before it

@@ -24,3 +24,25 @@ def test_rows_that_do_not_fill_a_warp(bits, D, new, behind):
     q = rows(rng, sum(new), 1, D)
     check(c, q, new, *attend(c, q, new, max_q=max(new)))
     assert w8.w8a8_check_status() == 0
+
+
+@pytest.mark.parametrize("lens,new,group", [([3000], [1], 4), ([300, 40], [4, 2], 4), ([90] * 1200, [1] * 1200, 1),
+                                            ([900, 300], [200, 40], 4)])
+def test_wait_that_gives_up(lens, new, group):
+    """A copy (few rows) or a hand-over (many rows) left out with the waits cut to about
+    1 ms: the kernel returns, the status says so, and the next call is right."""
+    rng = np.random.default_rng(len(lens))
+    c = Cache(rng, lens, 1, 128, 16, 4)
+    q = rows(rng, sum(new), group, 128)
+    call = lambda: attend(c, q, new, max_q=max(new))  # noqa: E731
+    assert w8.w8a8_check_status() == 0
+    try:
+        w8.w8a8_test_set_fault(2_000_000, True)
+        call()
+        status = w8.w8a8_check_status()
+    finally:
+        w8.w8a8_test_set_fault(0, False)
+    assert status == 5, w8.w8a8_status_string(status)
+    assert w8.w8a8_check_status() == 0
+    check(c, q, new, *call())
+    assert w8.w8a8_check_status() == 0

@@ -326,9 +326,9 @@ def w8a8_gemm_i32(xq, Wq, group_size: int = 0, wbits: int = 8, acc=None):
 
 
 def w8a8_test_set_fault(wait_limit_cycles: int = 0, skip_first_copy: bool = False) -> None:
-    """Test hook: the GEMM's bounded-wait limit (cycles, 0 = default) and
-    whether its first weight-staging copy per CTA is left unissued, for the
-    launches that follow."""
+    """Test hook: the bounded-wait limit (cycles, 0 = default) of the GEMM and of
+    the cache attention, and whether each CTA's first copy is left unissued, for
+    the launches that follow."""
     _check(load().w8a8_test_set_fault(int(wait_limit_cycles), int(bool(skip_first_copy))),
            "w8a8_test_set_fault")
 

@@ -32,6 +32,14 @@ int read_and_clear_device_error(unsigned int *code);
 // device), passed to the kernels as an argument; nullptr on failure.
 unsigned int *device_error_word();
 
+// Limit of every bounded wait, in SM clock cycles (about 2 s at 2 GHz).
+constexpr long long kTimeoutCycles = 4000000000LL;
+
+// What w8a8_test_set_fault() asks of the next launches: the limit of their waits,
+// and whether each block's first copy is left unissued.
+long long role_wait_limit();
+bool skip_first_copy();
+
 enum DeviceErrorCode : unsigned int {
   kDevErrNone = 0,
   kDevErrFullBarrier = 1,    // producer/MMA wait on a filled stage

@@ -53,7 +53,6 @@
 // returns.
 #include <cuda.h>
 
-#include <atomic>
 #include <mutex>
 
 #include "common.cuh"
@@ -780,10 +779,6 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// Role-wait limit and test switch for the next launches (w8a8_test_set_fault).
-std::atomic<long long> g_wait_limit{kTimeoutCycles};
-std::atomic<int> g_skip_first_copy{0};
-
 // 2-D tensor map over a row-major [rows, cols] matrix of 1- or 2-byte
 // elements, box [box_rows, box_cols]; out-of-range elements read 0.  2-byte
 // maps use the 128-byte swizzle (box rows of exactly 128 bytes): the
@@ -898,8 +893,8 @@ int launch_gemm_any(const void *X, bool x_half, bool wonly, const float *sa, con
   p.y = y;
   p.acc_out = acc_out;
   p.err = err;
-  p.wait_limit = g_wait_limit.load();
-  p.skip_first_copy = g_skip_first_copy.load();
+  p.wait_limit = role_wait_limit();
+  p.skip_first_copy = skip_first_copy();
   if (wonly) {
     if (ks == 2) {
       if (bt == 128)
@@ -940,11 +935,3 @@ int launch_gemm_weight_only(const __half *x, const void *W, const float *sw, int
 }
 
 }  // namespace w8a8
-
-extern "C" int w8a8_test_set_fault(long long wait_limit_cycles, int skip_first_copy) {
-  if (wait_limit_cycles < 0 || (skip_first_copy != 0 && skip_first_copy != 1))
-    return W8A8_ERR_INVALID_ARG;
-  w8a8::g_wait_limit.store(wait_limit_cycles == 0 ? w8a8::kTimeoutCycles : wait_limit_cycles);
-  w8a8::g_skip_first_copy.store(skip_first_copy);
-  return W8A8_OK;
-}

@@ -174,6 +174,8 @@ int kv_cache_attention(const w8a8_half *q, long long q_token_stride, long long q
   p.out = reinterpret_cast<__half *>(out);
   p.lse = lse;
   p.ws = static_cast<float *>(workspace);
+  p.wait_limit = role_wait_limit();
+  p.skip_first_copy = skip_first_copy();
   const bool few = static_cast<long long>(max_q) * p.group <= few_rows(cache->bits, cache->head_dim);
   return (few ? launch_kv_decode : launch_kv_prefill)(p, cache->bits, cache->head_dim,
                                                       static_cast<cudaStream_t>(stream));

@@ -38,6 +38,8 @@ struct KvAttnParams {
   __half *out;           // [T, Hq, D]
   float *lse;            // [T, Hq] or null
   float *ws;
+  long long wait_limit;  // of the kernels' waits, in cycles
+  int skip_first_copy;   // test only: each block's first copy or hand-over is left out
 };
 
 // Queries [q0, q0 + nq) and length of sequence b.  Offsets outside [0, T] or

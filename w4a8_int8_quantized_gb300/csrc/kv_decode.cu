@@ -99,8 +99,8 @@ __device__ __forceinline__ uint32_t smem_u32(const void *p) {
 }
 
 // Waits for a phase of an mbarrier, the whole warp together; false if it gave up
-// after about 2 s.
-__device__ __forceinline__ bool wait_stage(uint32_t bar, uint32_t parity) {
+// after `limit` cycles.
+__device__ __forceinline__ bool wait_stage(uint32_t bar, uint32_t parity, long long limit) {
   uint32_t ok;
   long long t0 = 0;
   for (int i = 0;; ++i) {
@@ -114,7 +114,7 @@ __device__ __forceinline__ bool wait_stage(uint32_t bar, uint32_t parity) {
         : "memory");
     if (ok) return true;
     if (i == 64) t0 = clock64();
-    if (i > 64 && __any_sync(0xffffffffu, clock64() - t0 > 4000000000LL)) return false;
+    if (i > 64 && __any_sync(0xffffffffu, clock64() - t0 > limit)) return false;
   }
 }
 
@@ -565,7 +565,6 @@ __global__ void __launch_bounds__(kThreads, Plan<BITS, D, NT>::BLOCKS)
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   __syncwarp();
   uint32_t phases = 0;  // bit s: parity of the next wait on stage s
-  bool ok = true;
   Math<BITS, D, NT> math(p, lane, smem_u32(dyn) + PL::OFF_SCALES + warp * PL::STEP * 16);
 
   // copies: lane i < 4 MT brings array i % 4 (K, V, K scales, V scales) of tile
@@ -618,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, Plan<BITS, D, NT>::BLOCKS)
       const int e = page_of(p, b, a >> p.kv.page_shift);
       return e < 0 ? -2 : e;
     };
-    auto issue = [&](int page, int j, int st) {
+    auto issue = [&](int page, int j, int st, bool lost = false) {
       if (__any_sync(0xffffffffu, page == -2)) it.bad = true;
       // tiles that follow one another in a page come in one copy
       const int run = (j & (run_tokens - 1)) == 0 ? run_tokens : 16;
@@ -630,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, Plan<BITS, D, NT>::BLOCKS)
                      "r"(__popc(there) / 4 * (run >> 4) * PL::TILE_BYTES)
                      : "memory");
       __syncwarp();
-      if (copies)
+      if (copies && !lost)
         bulk_copy(cdst + st * PL::STAGE,
                   hsrc + static_cast<size_t>(page) * page_bytes + ((j + ctile) & pmask) * cbytes,
                   run * cbytes, bar);
@@ -641,32 +640,40 @@ __global__ void __launch_bounds__(kThreads, Plan<BITS, D, NT>::BLOCKS)
     for (int i = 0; i <= S; ++i) page[i] = u0 + i < u1 ? page_at(j + i * PL::UNIT) : -1;
 #pragma unroll
     for (int i = 0; i < S; ++i)
-      if (u0 + i < u1) issue(page[i], j + i * PL::UNIT, i);
+      if (u0 + i < u1)
+        issue(page[i], j + i * PL::UNIT, i, i == 0 && warp == 0 && p.skip_first_copy && istart + u0 == c0);
     int next = page[S];
     int st = 0;
     math.begin(it);
 
-    for (int u = u0; u < u1; ++u, j += PL::UNIT) {
-      ok = ok && wait_stage(bars + 8 * st, (phases >> st) & 1u);
+    int u = u0;
+    for (; u < u1; ++u, j += PL::UNIT) {
+      if (!wait_stage(bars + 8 * st, (phases >> st) & 1u, p.wait_limit)) break;
       phases ^= 1u << st;
       math.step(it, ring + st * PL::STAGE, j, j < it.lo_max || j + PL::STEP > it.hi_min || it.bad);
       // refill the stage: every lane has its registers
       __syncwarp();
-      if (u + S < u1 && ok) {
+      if (u + S < u1) {
         issue(next, j + S * PL::UNIT, st);
         next = u + S + 1 < u1 ? page_at(j + (S + 1) * PL::UNIT) : -1;
       }
       st = st + 1 == S ? 0 : st + 1;
     }
 
-    if (!ok) {
-      // a copy did not land: report it, and let the others land (bounded)
+    if (u < u1) {
+      // a copy did not land: report it, and let those of the steps u .. u + S - 1,
+      // which are all that this warp has in flight, land (bounded)
       if (lane == 0) atomicCAS(p.kv.err, 0u, static_cast<unsigned>(kDevErrCacheCopy));
-      for (int i = 0; i < S; ++i) wait_stage(bars + 8 * i, (phases >> i) & 1u);
+      for (int i = u; i < u1 && i < u + S; ++i) {
+        wait_stage(bars + 8 * st, (phases >> st) & 1u, kTimeoutCycles);
+        st = st + 1 == S ? 0 : st + 1;
+      }
     }
 
     // -- join the warps -----------------------------------------------------------
-    __syncthreads();  // every ring is drained
+    // Every ring is drained.  After a wait that gave up no barrier is armed again: the
+    // block ends.
+    if (__syncthreads_or(u < u1)) return;
     math.finish(o_sm[warp], m_sm[warp], l_sm[warp]);
     __syncthreads();
     const bool whole = u0 == 0 && u1 == nu;

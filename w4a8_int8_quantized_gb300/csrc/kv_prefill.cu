@@ -131,11 +131,11 @@ __device__ __forceinline__ bool try_all(uint32_t bar, uint32_t parity) {
 // The wait itself, bounded: false if the block is aborting, or if this wait
 // gave up (which is recorded and aborts the block).
 __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile int *abort_flag,
-                                      unsigned int *err) {
+                                      unsigned int *err, long long limit) {
   const long long t0 = clock64();
   while (!try_all(bar, parity)) {
     if (__any_sync(0xffffffffu, *abort_flag != 0)) return false;
-    if (__any_sync(0xffffffffu, clock64() - t0 > kTimeoutCycles)) {
+    if (__any_sync(0xffffffffu, clock64() - t0 > limit)) {
       atomicCAS(err, 0u, static_cast<unsigned>(kDevErrCacheCopy));
       *abort_flag = 1;
       return false;
@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
   const uint32_t tmem = *tmem_slot;  // 0: all 512 columns are this block's
   unsigned int *err = p.kv.err;
   auto wait = [&](uint32_t bar, uint32_t parity) {
-    return try_all(bar, parity) || wait_all(bar, parity, abort_flag, err);
+    return try_all(bar, parity) || wait_all(bar, parity, abort_flag, err, p.wait_limit);
   };
   // a warp's view of the published pieces
   struct Reader {
@@ -745,6 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
       load_k();
       load(p.kv.vc, vv);
     }
+    bool lost = p.skip_first_copy && cw == 0;  // test only: the first hand-over
     while (ok && have) {
       ok = wait(k_empty(st), phase);
       if (!ok) break;
@@ -756,7 +757,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
       sts1(sc + 2 * kKeys * 4, row < 0 ? 0.f : 1.f / sv);
       fence_proxy_async();
       __syncwarp();
-      if (lane == 0) mbar_arrive(k_full(st));
+      if (lane == 0 && !lost) mbar_arrive(k_full(st));
+      lost = false;
       have = ahead;
       if (have) load_k();
       ok = wait(v_empty(st), phase);

@@ -1,6 +1,7 @@
 // Device-side error word shared by the kernels that contain bounded waits.
 // A kernel whose wait gives up stores a nonzero code (which wait) here and
 // returns; w8a8_check_status() reads and clears it.
+#include <atomic>
 #include <mutex>
 
 #include "common.cuh"
@@ -8,7 +9,12 @@
 namespace w8a8 {
 namespace {
 __device__ unsigned int g_device_error = 0;
+std::atomic<long long> g_wait_limit{kTimeoutCycles};
+std::atomic<int> g_skip_first_copy{0};
 }
+
+long long role_wait_limit() { return g_wait_limit.load(); }
+bool skip_first_copy() { return g_skip_first_copy.load() != 0; }
 
 unsigned int *device_error_word() {
   static unsigned int *cache[64] = {};
@@ -45,3 +51,11 @@ int read_and_clear_device_error(unsigned int *code) {
 }
 
 }  // namespace w8a8
+
+extern "C" int w8a8_test_set_fault(long long wait_limit_cycles, int skip_first_copy) {
+  if (wait_limit_cycles < 0 || (skip_first_copy != 0 && skip_first_copy != 1))
+    return W8A8_ERR_INVALID_ARG;
+  w8a8::g_wait_limit.store(wait_limit_cycles == 0 ? w8a8::kTimeoutCycles : wait_limit_cycles);
+  w8a8::g_skip_first_copy.store(skip_first_copy);
+  return W8A8_OK;
+}

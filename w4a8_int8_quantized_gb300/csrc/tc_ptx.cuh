@@ -8,9 +8,6 @@
 
 namespace w8a8 {
 
-// Limit of every bounded wait, in SM clock cycles (about 2 s at 2 GHz).
-constexpr long long kTimeoutCycles = 4000000000LL;
-
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
