@@ -7,7 +7,7 @@ import pytest
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
-from test_gpu_kv_cache import Cache, attend, check, rows  # noqa: E402
+from test_gpu_kv_cache import Cache, attend, check, cuda, rows  # noqa: E402
 
 if torch.cuda.is_available():
     import w4a8_int8_quantized_gb300 as w8
@@ -46,3 +46,23 @@ def test_wait_that_gives_up(lens, new, group):
     assert w8.w8a8_check_status() == 0
     check(c, q, new, *call())
     assert w8.w8a8_check_status() == 0
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("new", [1, 60])
+@pytest.mark.parametrize("size", [1.0, 0.05, 0.001])
+@pytest.mark.parametrize("at", [0, 200, 451])
+def test_leading_key_without_a_value(bits, new, size, at):
+    """A key far above the others whose value is zero (scale 0): the tokens that make up
+    the output keep their weights' bits."""
+    rng = np.random.default_rng(bits + new + at)
+    c = Cache(rng, [512], 1, 128, 16, bits)
+    q = rows(rng, new, 4, 128)
+    q[..., 0] = 4
+    c.k[0][..., 0] = 0
+    c.k[0][at] = 0
+    c.k[0][at, :, 0] = 28                                    # about 10 nats above the rest
+    c.v[0] = (c.v[0] * size).astype(np.float16)
+    c.v[0][at] = 0
+    w8.kv_cache_write(cuda(c.k[0]), cuda(c.v[0]), cuda(c.slots(0, np.arange(512))), c.handle)
+    check(c, q, [new], *attend(c, q, [new], max_q=new))

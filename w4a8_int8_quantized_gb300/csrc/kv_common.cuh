@@ -160,4 +160,11 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // 201 us against 180.)  A row starts at kNoRef, under every u.
 constexpr float kRoom = 15.f, kNoRef = -1e30f;
 
+// What stands for s_v where it is 0.  All codes are 0 there, so the products do not
+// need it, but u and with it M do: it lies below every scale that is ever stored (the
+// smallest is 2^-24 / 127), so that a token without a value never takes M above what
+// the tokens with one weigh.  (As 1, a leading key of this kind took the others'
+// weights out of fp16's range: with values of 0.05 they lost a tenth.)
+constexpr float kZeroScale = 0x1p-32f;
+
 }  // namespace w8a8

@@ -26,7 +26,7 @@
 // weight carries the value's scale: O = sum p code_v with exact codes, and the
 // row's sum is sum p / s_v.  M is the lazy reference of kv_common.cuh: while no
 // weight passes 2^15 (one vote per step) nothing is rescaled or exchanged.
-// s_v = 0 means all codes are 0: any scale will do, 1 is taken.
+// s_v = 0 (all codes 0) counts as kZeroScale.
 //
 // Split: the units (4 warps x one step of tokens) of all items form one line,
 // cut into equal ranges, one per resident block, so ragged lengths balance to
@@ -192,15 +192,14 @@ struct Item {
   }
 };
 
-// A token's scales from a stage: s_k times `f`, log2 s_v and 1 / s_v.  s_v = 0
-// has all codes 0, so any scale will do.
+// A token's scales from a stage: s_k times `f`, log2 s_v and 1 / s_v.
 __device__ __forceinline__ void token_scales(uint32_t ks_at, uint32_t vs_at, float f, float &sk,
                                              float &lv, float &rv) {
   uint32_t x, y;
   lds_words<1>(ks_at, &x);
   lds_words<1>(vs_at, &y);
   sk = __uint_as_float(x) * f;
-  const float sv = y == 0 ? 1.f : __uint_as_float(y);
+  const float sv = y == 0 ? kZeroScale : __uint_as_float(y);
   lv = log2_fast(sv);
   rv = rcp_fast(sv);
 }

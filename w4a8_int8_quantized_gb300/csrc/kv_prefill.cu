@@ -751,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
       if (!ok) break;
       convert(kv, base + PL::OFF_K + st * PL::TILE, true);
       const uint32_t sc = base + PL::OFF_S + slot * (3 * kKeys * 4) + tok * 4;
-      const float sv = vs == 0.f ? 1.f : vs;  // s_v = 0: all codes 0, any scale will do
+      const float sv = vs == 0.f ? kZeroScale : vs;
       sts1(sc, row < 0 ? 0.f : ks * (p.scale * kLog2e));
       sts1(sc + kKeys * 4, row < 0 ? -CUDART_INF_F : log2_fast(sv));
       sts1(sc + 2 * kKeys * 4, row < 0 ? 0.f : 1.f / sv);
