@@ -83,14 +83,14 @@ int w8a8_is_available(void);
 /* Static, human-readable name of a status code. */
 const char *w8a8_status_string(int status);
 
-/* Reads and clears the device-side error word that the kernels set when a
+/* Reads and clears the device-side error words that the kernels set when a
  * bounded wait on the tensor-core pipeline gives up, or when a GEMM kernel
  * finds its shared memory not 1 KB aligned and returns without doing
  * anything (both leave the outputs of that call undefined), or when a
  * key/value cache kernel meets a slot, page, length or query offset outside
  * its range (which it leaves out).  Synchronizes `stream`.  Returns W8A8_OK,
- * W8A8_ERR_TIMEOUT (for either of the first two causes), W8A8_ERR_INDEX or
- * W8A8_ERR_CUDA. */
+ * W8A8_ERR_TIMEOUT (for either of the first two causes, whatever else was
+ * reported), W8A8_ERR_INDEX or W8A8_ERR_CUDA. */
 int w8a8_check_status(w8a8_stream_t stream);
 
 /* Offline INT8 weight quantization ("cider 설치와 사용법":

@@ -66,3 +66,24 @@ def test_leading_key_without_a_value(bits, new, size, at):
     c.v[0][at] = 0
     w8.kv_cache_write(cuda(c.k[0]), cuda(c.v[0]), cuda(c.slots(0, np.arange(512))), c.handle)
     check(c, q, [new], *attend(c, q, [new], max_q=new))
+
+
+def test_timeout_is_reported_before_an_index():
+    """An index out of range does not hide a wait that gave up after it."""
+    cache = w8.KVCache.empty(2, 1, 16, 64)
+    x = torch.ones(1, 1, 64, dtype=torch.float16, device="cuda")
+    a = torch.ones(130, 512, dtype=torch.int8, device="cuda")
+    w = torch.ones(257, 512, dtype=torch.int8, device="cuda")
+    assert w8.w8a8_check_status() == 0
+    w8.kv_cache_write(x, x, torch.tensor([99], device="cuda"), cache)
+    try:
+        w8.w8a8_test_set_fault(2_000_000, True)
+        w8.w8a8_gemm_i32(a, w)
+        status = w8.w8a8_check_status()
+    finally:
+        w8.w8a8_test_set_fault(0, False)
+    assert status == 5, w8.w8a8_status_string(status)
+    assert w8.w8a8_check_status() == 0
+    w8.kv_cache_write(x, x, torch.tensor([99], device="cuda"), cache)
+    assert w8.w8a8_check_status() == 7
+    assert w8.w8a8_check_status() == 0

@@ -24,12 +24,12 @@ constexpr int kMaxK = 32768;
 constexpr int kSkinnyMaxM = 8;
 constexpr int kSkinnyMaxCodeBytes = 64 * 1024;
 
-// Reads and clears the device-side error word that kernels with bounded
-// waits set when a wait gives up (the value says which wait).
+// Reads and clears the device-side error words: the code of a wait that gave up
+// (it says which wait), else kDevErrIndex if an index was out of its range.
 int read_and_clear_device_error(unsigned int *code);
 
-// Device address of that word on the current device (looked up once per
-// device), passed to the kernels as an argument; nullptr on failure.
+// Device address of the first of these words on the current device (looked up
+// once per device), passed to the kernels as an argument; nullptr on failure.
 unsigned int *device_error_word();
 
 // Limit of every bounded wait, in SM clock cycles (about 2 s at 2 GHz).
@@ -51,6 +51,11 @@ enum DeviceErrorCode : unsigned int {
   kDevErrIndex = 7,          // cache kernels: a slot, page, length or offset outside its range
   kDevErrCacheCopy = 8,      // cache attention: a copy or a hand-over did not arrive
 };
+
+// A cache kernel met a slot, page, length or offset outside its range.
+__device__ __forceinline__ void report_index(unsigned int *err) {
+  if (err != nullptr) atomicCAS(err + 1, 0u, static_cast<unsigned>(kDevErrIndex));
+}
 
 inline bool aligned16(const void *p) {
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;

@@ -131,7 +131,7 @@ __device__ __forceinline__ bool find_slot(const KvView &c, long long slot, long 
   page = slot >> c.page_shift;
   off = static_cast<int>(slot) & ((1 << c.page_shift) - 1);
   if (page < c.pages) return true;
-  if (c.err != nullptr) atomicCAS(c.err, 0u, static_cast<unsigned>(kDevErrIndex));
+  report_index(c.err);
   return false;
 }
 

@@ -62,8 +62,7 @@ __device__ __forceinline__ void seq_of(const KvAttnParams &p, int b, int &q0, in
   const long long cap = static_cast<long long>(p.table_w) << p.kv.page_shift;
   len = static_cast<int>(min(static_cast<long long>(max(n, 0)), cap));
   bad |= len != n;
-  if (bad && p.kv.err != nullptr)
-    atomicCAS(p.kv.err, 0u, static_cast<unsigned>(kDevErrIndex));
+  if (bad) report_index(p.kv.err);
 }
 
 // Keys that the query at position pos of a sequence of len tokens sees:
@@ -81,7 +80,7 @@ __device__ __forceinline__ int entry_of(const KvAttnParams &p, int b, int i) {
 // are left out) and is reported.
 __device__ __forceinline__ int checked_page(const KvAttnParams &p, int e) {
   if (static_cast<unsigned>(e) < static_cast<unsigned long long>(p.kv.pages)) return e;
-  if (p.kv.err != nullptr) atomicCAS(p.kv.err, 0u, static_cast<unsigned>(kDevErrIndex));
+  report_index(p.kv.err);
   return -1;
 }
 __device__ __forceinline__ int page_of(const KvAttnParams &p, int b, int i) {

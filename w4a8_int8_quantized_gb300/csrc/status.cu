@@ -1,6 +1,8 @@
-// Device-side error word shared by the kernels that contain bounded waits.
-// A kernel whose wait gives up stores a nonzero code (which wait) here and
-// returns; w8a8_check_status() reads and clears it.
+// Device-side error words.  Word 0 is shared by the kernels that contain bounded
+// waits: a kernel whose wait gives up stores a nonzero code (which wait) there and
+// returns.  Word 1 is where the cache kernels report an index out of its range:
+// apart from the first, since it says less (the rest of that call is right) and must
+// not hide a wait that gave up after it.  w8a8_check_status() reads and clears both.
 #include <atomic>
 #include <mutex>
 
@@ -8,7 +10,7 @@
 
 namespace w8a8 {
 namespace {
-__device__ unsigned int g_device_error = 0;
+__device__ unsigned int g_device_error[2] = {0, 0};
 std::atomic<long long> g_wait_limit{kTimeoutCycles};
 std::atomic<int> g_skip_first_copy{0};
 }
@@ -38,15 +40,15 @@ unsigned int *device_error_word() {
 
 int read_and_clear_device_error(unsigned int *code) {
   *code = 0;
-  if (cudaMemcpyFromSymbol(code, g_device_error, sizeof(unsigned int)) !=
-      cudaSuccess)
+  unsigned int words[2] = {0, 0};
+  if (cudaMemcpyFromSymbol(words, g_device_error, sizeof(words)) != cudaSuccess)
     return W8A8_ERR_CUDA;
-  if (*code != 0) {
-    const unsigned int zero = 0;
-    if (cudaMemcpyToSymbol(g_device_error, &zero, sizeof(unsigned int)) !=
-        cudaSuccess)
+  if (words[0] != 0 || words[1] != 0) {
+    const unsigned int zero[2] = {0, 0};
+    if (cudaMemcpyToSymbol(g_device_error, zero, sizeof(zero)) != cudaSuccess)
       return W8A8_ERR_CUDA;
   }
+  *code = words[0] != 0 ? words[0] : words[1];
   return W8A8_OK;
 }
 
