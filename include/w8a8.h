@@ -346,8 +346,9 @@ size_t kv_cache_attention_workspace_bytes(int T, int q_heads, int B, int max_q, 
  * S_j = softmax_scale * k_scale[j] * (q . code_k[j]) with the codes exact and
  * fp32 sums; out = sum_j softmax(S)_j * v_scale[j] * code_v[j], one fp16
  * rounding at the end.  A query that sees no key gets out 0 and lse -inf.
- * Cache rows past seq_len may hold anything.  Results do not depend on the
- * order in which blocks run. */
+ * Cache rows that no query sees (past seq_len, before every window) may hold
+ * anything; of their pages only one that also holds a seen row has to be in
+ * the cache.  Results do not depend on the order in which blocks run. */
 int kv_cache_attention(const w8a8_half *q, long long q_token_stride, long long q_head_stride,
                        int T, int q_heads, const int32_t *q_offsets, int B, int max_q,
                        const int32_t *block_table, int table_width, const int32_t *seq_lens,

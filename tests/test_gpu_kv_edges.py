@@ -87,3 +87,21 @@ def test_timeout_is_reported_before_an_index():
     w8.kv_cache_write(x, x, torch.tensor([99], device="cuda"), cache)
     assert w8.w8a8_check_status() == 7
     assert w8.w8a8_check_status() == 0
+
+
+@pytest.mark.parametrize("bits,D", [(4, 128), (8, 64)])
+@pytest.mark.parametrize("new", [1, 5, 30, 100])
+@pytest.mark.parametrize("scale", [float("nan"), float("inf"), 1e-40, -1.0])
+def test_slots_before_the_window_may_hold_anything(bits, D, new, scale):
+    """Also those that share a page and a group of 16 with the window's first key."""
+    rng = np.random.default_rng(bits + new)
+    n, window = 999, 300
+    c = Cache(rng, [n], 2, D, 64, bits)
+    q = rows(rng, new, 8, D)
+    first = n - new + 1 - window
+    assert first % 16
+    slots = c.slots(0, np.arange(first))
+    c.handle.k_scale[slots // 64, :, slots % 64] = scale
+    c.handle.v_scale[slots // 64, :, slots % 64] = scale
+    check(c, q, [new], *attend(c, q, [new], max_q=new, window=window), window=window)
+    assert w8.w8a8_check_status() == 0

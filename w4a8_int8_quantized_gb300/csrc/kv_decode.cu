@@ -169,7 +169,8 @@ __device__ __forceinline__ void load_words(const uint8_t *p, uint32_t *o) {
 struct Item {
   int b, h, rb, R;             // sequence, kv head, row block, its rows
   int q0, nq, len;             // queries, tokens of the sequence
-  int lo_max, hi_min, hi_max;  // keys [lo_max, hi_min) are seen by all rows, none from hi_max on
+  int lo_max, hi_min;          // keys [lo_max, hi_min) are seen by all rows,
+  int lo_min, hi_max;          // those outside [lo_min, hi_max) by none
   bool bad;                    // a page outside the cache was met
 
   // output row of row c
@@ -339,8 +340,9 @@ struct Math {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const int a = j + 16 * i + 8 * r + tokg;
-          // from hi_max on nothing was copied: the stage holds an older step's scales
-          const bool out = a >= it.hi_max || it.gone(p, a);
+          // from hi_max on nothing was copied: the stage holds an older step's scales;
+          // before lo_min, in the 16 that hold the window's first key, any slot's
+          const bool out = a < it.lo_min || a >= it.hi_max || it.gone(p, a);
           if (out) rv[i][r] = 0.f;
 #pragma unroll
           for (int n = 0; n < NT; ++n)
@@ -601,8 +603,7 @@ __global__ void __launch_bounds__(kThreads, Plan<BITS, D, NT>::BLOCKS)
     it.len = len;
     it.bad = false;
     {
-      int x;
-      visible(p, len - nq + it.rb * COLS / p.group, len, x, it.hi_min);
+      visible(p, len - nq + it.rb * COLS / p.group, len, it.lo_min, it.hi_min);
       visible(p, len - nq + (it.rb * COLS + it.R - 1) / p.group, len, it.lo_max, it.hi_max);
     }
 

@@ -64,7 +64,8 @@ constexpr int kItemCost = 3;
 struct Piece {
   int b, h, qt, R;     // R: rows of the item; 0: no more pieces
   int q0, nq, len;     // of the sequence
-  int first, hi_max;   // token of tile 0; keys from hi_max on are seen by no row
+  int first;           // token of tile 0
+  int lo_min, hi_max;  // keys outside [lo_min, hi_max) are seen by no row
   int t0, t1, nt;
   int last;            // range that holds the item's last tile
 };
@@ -256,7 +257,7 @@ __device__ __forceinline__ long long div_units(long long a, long long b) {
 
 // Rows and tiles of entity e = sequence * nqt + row block; 0 tiles: no rows.
 struct Entity {
-  int b, qt, R, q0, nq, len, first, hi_max, nt;
+  int b, qt, R, q0, nq, len, first, lo_min, hi_max, nt;
   // units of the line that one of its items takes: kItemCost, then its tiles
   __device__ __forceinline__ long long cost() const { return nt > 0 ? nt + kItemCost : 0; }
 };
@@ -268,13 +269,13 @@ __device__ __forceinline__ Entity entity_of(const KvAttnParams &p, int nqt, int 
   const long long left = static_cast<long long>(x.nq) * p.group - static_cast<long long>(x.qt) * kRows;
   x.R = static_cast<int>(min(left, static_cast<long long>(kRows)));
   x.nt = 0;
-  x.first = x.hi_max = 0;
+  x.first = x.lo_min = x.hi_max = 0;
   if (x.R > 0) {
-    int lo, hi, lo2;
-    visible(p, x.len - x.nq + (x.qt * kRows) / p.group, x.len, lo, hi);
+    int hi, lo2;
+    visible(p, x.len - x.nq + (x.qt * kRows) / p.group, x.len, x.lo_min, hi);
     visible(p, x.len - x.nq + (x.qt * kRows + x.R - 1) / p.group, x.len, lo2, x.hi_max);
     x.hi_max = max(x.hi_max, 0);
-    x.first = min(lo, x.hi_max) & ~15;
+    x.first = min(x.lo_min, x.hi_max) & ~15;
     x.nt = max((x.hi_max - x.first + kKeys - 1) / kKeys, 1);
   }
   return x;
@@ -697,9 +698,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
     // The codes of the next K are fetched when this tile's are converted, those of
     // the next V likewise, so that memory's latency lies under the other's work.
     // The tile to fetch: its sequence, head, this lane's token, where the keys
-    // end, and the piece's tiles after it; and the table's entry of the token's page,
-    // itself fetched a tile ahead.
-    int tb = 0, th = 0, ta = 0, tend = 0, left = 0, entry = 0;
+    // begin and end, and the piece's tiles after it; and the table's entry of the token's
+    // page, itself fetched a tile ahead.
+    int tb = 0, th = 0, ta = 0, tlo = 0, tend = 0, left = 0, entry = 0;
     auto advance = [&]() {
       if (left > 0) {
         ta += kKeys;
@@ -708,8 +709,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
         Piece x;
         if (!next_piece(reader, x)) return false;
         tb = x.b;
-        th = x.h;
         ta = x.first + x.t0 * kKeys + tok;
+        th = x.h;
+        tlo = x.lo_min;
         tend = min(x.hi_max, x.len);
         left = x.t1 - x.t0 - 1;
       }
@@ -717,9 +719,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
       return true;
     };
     uint4 kv[NV] = {}, vv[NV] = {};
+    // the token's scales; kNone for s_v: left out.  (A bit pattern that no arithmetic
+    // makes: the row itself, kept for this, spilled at 8 bits.)
+    constexpr int kNone = -1;
     float ks = 0.f, vs = 0.f;
-    long long row = -1;              // of the token in the cache; -1: left out
-    long long run[2] = {-1, -1};     // of the warp's tokens 0 and 16
+    long long run[2] = {-1, -1};     // rows in the cache of the warp's tokens 0 and 16
     // Codes of tokens that are left out are any: they are finite, and weigh nothing
     auto load = [&](const uint8_t *codes, uint4 (&v)[NV]) {
 #pragma unroll
@@ -730,11 +734,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
     bool ahead = advance();  // whether that tile is there
     auto load_k = [&]() {
       const int page = ta < tend ? checked_page(p, entry) : -1;
-      row = page < 0 ? -1 : p.kv.row(page, th) + (ta & pmask);
+      const long long row = page < 0 ? -1 : p.kv.row(page, th) + (ta & pmask);
       run[0] = __shfl_sync(0xffffffffu, row, 0);
       run[1] = __shfl_sync(0xffffffffu, row, 16);
       load(p.kv.kc, kv);
-      if (row >= 0) {
+      vs = __int_as_float(kNone);
+      if (row >= 0 && ta >= tlo) {  // a slot that nobody sees may hold any scale
         ks = __ldg(p.kv.ks + row);
         vs = __ldg(p.kv.vs + row);
       }
@@ -752,9 +757,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
       convert(kv, base + PL::OFF_K + st * PL::TILE, true);
       const uint32_t sc = base + PL::OFF_S + slot * (3 * kKeys * 4) + tok * 4;
       const float sv = vs == 0.f ? kZeroScale : vs;
-      sts1(sc, row < 0 ? 0.f : ks * (p.scale * kLog2e));
-      sts1(sc + kKeys * 4, row < 0 ? -CUDART_INF_F : log2_fast(sv));
-      sts1(sc + 2 * kKeys * 4, row < 0 ? 0.f : 1.f / sv);
+      const bool none = __float_as_int(vs) == kNone;
+      sts1(sc, none ? 0.f : ks * (p.scale * kLog2e));
+      sts1(sc + kKeys * 4, none ? -CUDART_INF_F : log2_fast(sv));
+      sts1(sc + 2 * kKeys * 4, none ? 0.f : 1.f / sv);
       fence_proxy_async();
       __syncwarp();
       if (lane == 0 && !lost) mbar_arrive(k_full(st));
@@ -943,7 +949,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
           if (lane == 0) pieces[slot.i].R = 0;
         } else {
           if (lane == 0)
-            pieces[slot.i] = Piece{en.b, h, en.qt, en.R, en.q0, en.nq, en.len, en.first, en.hi_max,
+            pieces[slot.i] = Piece{en.b, h, en.qt, en.R, en.q0, en.nq, en.len, en.first, en.lo_min, en.hi_max,
                                    t0, t1, en.nt, static_cast<int>(div_units(istart + en.cost() - 1, per))};
         }
         __syncwarp();
