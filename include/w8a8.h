@@ -345,7 +345,11 @@ size_t kv_cache_attention_workspace_bytes(int T, int q_heads, int B, int max_q, 
  *               exponentials, or NULL
  * S_j = softmax_scale * k_scale[j] * (q . code_k[j]) with the codes exact and
  * fp32 sums; out = sum_j softmax(S)_j * v_scale[j] * code_v[j], one fp16
- * rounding at the end.  A query that sees no key gets out 0 and lse -inf.
+ * rounding at the end.  A query that sees no key gets out 0 and lse -inf, and
+ * so does a row that no sequence owns: before q_offsets[0], from q_offsets[B]
+ * on (a batch padded to a fixed T), or beyond a sequence's first max_q (which
+ * is reported, the others taken as if there were max_q).  Offsets out of
+ * order are reported; the rows that they touch are then undefined.
  * Cache rows that no query sees (past seq_len, before every window) may hold
  * anything; of their pages only one that also holds a seen row has to be in
  * the cache.  Results do not depend on the order in which blocks run. */

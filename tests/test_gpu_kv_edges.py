@@ -105,3 +105,54 @@ def test_slots_before_the_window_may_hold_anything(bits, D, new, scale):
     c.handle.v_scale[slots // 64, :, slots % 64] = scale
     check(c, q, [new], *attend(c, q, [new], max_q=new, window=window), window=window)
     assert w8.w8a8_check_status() == 0
+
+
+@pytest.mark.parametrize("new", [[1, 0, 3], [70, 0, 90], [2, 8, 1]])
+@pytest.mark.parametrize("before,after", [(0, 5), (4, 0), (3, 700)])
+def test_rows_that_no_sequence_owns(new, before, after):
+    """Padding before the first and after the last sequence: out 0, lse -inf, no report."""
+    rng = np.random.default_rng(sum(new) + before + after)
+    c = Cache(rng, [90, 20, 333], 2, 128, 16, 4)
+    q = rows(rng, before + sum(new) + after, 8, 128)
+    off = cuda((before + np.concatenate([[0], np.cumsum(new)])).astype(np.int32))
+    out = torch.full(q.shape, 7, dtype=torch.float16, device="cuda")
+    lse = torch.full(q.shape[:2], 7, dtype=torch.float32, device="cuda")
+    w8.kv_cache_attention(cuda(q), c.handle, cuda(c.table), cuda(np.array(c.lens, np.int32)), q_offsets=off,
+                          max_q=max(new), return_lse=True, out=out, lse=lse)
+    assert w8.w8a8_check_status() == 0
+    end = before + sum(new)
+    check(c, q[before:end], new, out[before:end], lse[before:end])
+    for rest in (slice(0, before), slice(end, None)):
+        assert not out[rest].any() and (lse[rest] == -np.inf).all()
+
+
+@pytest.mark.parametrize("max_q", [3, 40])
+def test_queries_beyond_max_q(max_q):
+    """Reported, and their rows hold 0 and -inf; the other sequences are right."""
+    rng = np.random.default_rng(max_q)
+    new = [max_q - 1, max_q + 7, max_q]
+    c = Cache(rng, [100, 200, 60], 2, 128, 16, 8)
+    q = rows(rng, sum(new), 8, 128)
+    out = torch.full(q.shape, 7, dtype=torch.float16, device="cuda")
+    lse = torch.full(q.shape[:2], 7, dtype=torch.float32, device="cuda")
+    attend(c, q, new, max_q=max_q, out=out, lse=lse)
+    assert w8.w8a8_check_status() == 7
+    over = slice(new[0] + max_q, new[0] + new[1])
+    assert not out[over].any() and (lse[over] == -np.inf).all()
+    for b, r in ((0, slice(0, new[0])), (2, slice(new[0] + new[1], None))):
+        one = Cache.__new__(Cache)
+        one.__dict__.update(c.__dict__, lens=[c.lens[b]], k=[c.k[b]], v=[c.v[b]])
+        check(one, q[r], [new[b]], out[r], lse[r])
+
+
+@pytest.mark.parametrize("T", [1, 700])
+def test_no_sequences(T):
+    """Query rows and no sequence: every row is padding."""
+    c = w8.KVCache.empty(4, 2, 16, 64)
+    out = torch.full((T, 4, 64), 7, dtype=torch.float16, device="cuda")
+    lse = torch.full((T, 4), 7, dtype=torch.float32, device="cuda")
+    w8.kv_cache_attention(torch.ones_like(out), c, torch.zeros(0, 3, dtype=torch.int32, device="cuda"),
+                          torch.zeros(0, dtype=torch.int32, device="cuda"),
+                          q_offsets=torch.zeros(1, dtype=torch.int32, device="cuda"), return_lse=True, out=out, lse=lse)
+    assert not out.any() and (lse == -np.inf).all()
+    assert w8.w8a8_check_status() == 0

@@ -139,7 +139,14 @@ int kv_cache_attention(const w8a8_half *q, long long q_token_stride, long long q
   if (q_offsets == nullptr && T != B) return W8A8_ERR_INVALID_ARG;
   if (static_cast<long long>(table_width) * cache->page_size > 0x7fffffffLL)
     return W8A8_ERR_INVALID_ARG;
-  if (T == 0 || B == 0) return W8A8_OK;
+  if (T == 0) return W8A8_OK;
+  if (B == 0) {  // no sequence owns a row
+    if (out == nullptr) return W8A8_ERR_INVALID_ARG;
+    if (!aligned(out, 16) || !aligned(lse, 4)) return W8A8_ERR_MISALIGNED;
+    W8A8_TRY(check_device());
+    return launch_kv_blank(reinterpret_cast<__half *>(out), lse, static_cast<long long>(T) * q_heads,
+                           cache->head_dim, static_cast<cudaStream_t>(stream));
+  }
   W8A8_TRY(check_cache(cache));
   W8A8_TRY(check_rows(q, q_token_stride, q_head_stride));
   if (out == nullptr || seq_lens == nullptr || (block_table == nullptr && table_width > 0))

@@ -22,6 +22,47 @@ __device__ __forceinline__ void store_row4(const KvAttnParams &p, long long row,
     p.lse[row] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * kLn2;
 }
 
+// Rows that no sequence owns: before the first, after the last (padding of a batch, say),
+// and beyond max_q queries of one (reported).
+__device__ __forceinline__ int offset_of(const int *q_offsets, int T, long long b) {
+  return min(max(__ldg(q_offsets + b), 0), T);
+}
+// Whether there are any, as far as this thread's share of the sequences tells.  Asked after
+// the offsets were read for the ranges, from L1 then: at the kernel's start it cost a
+// round trip to L2, 0.5 us.
+__device__ __forceinline__ bool some_unowned(const KvAttnParams &p) {
+  if (p.q_offsets == nullptr) return false;
+  bool any = offset_of(p.q_offsets, p.T, 0) > 0 || offset_of(p.q_offsets, p.T, p.B) < p.T;
+  for (long long b = blockIdx.x + static_cast<long long>(threadIdx.x) * gridDim.x; b < p.B;
+       b += static_cast<long long>(gridDim.x) * blockDim.x)
+    any |= offset_of(p.q_offsets, p.T, b + 1) - offset_of(p.q_offsets, p.T, b) > p.max_q;
+  return any;
+}
+// They get 0 and -inf, by the warps in which some thread found any: all threads, who all
+// see them, share the rows before and after; a sequence's are the warp's that looked at
+// it.  (A call with few arguments: inlined, it spilled in the many-row kernel.)
+template <int D>
+__device__ __noinline__ void blank_unowned(__half *out, float *lse, const int *q_offsets, int T, int Hq, int B,
+                                           int max_q) {
+  auto blank = [&](long long r0, long long r1, long long at, long long step) {
+#pragma unroll 1
+    for (long long i = r0 * Hq * (D / 8) + at; i < r1 * Hq * (D / 8); i += step)
+      reinterpret_cast<uint4 *>(out)[i] = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+    for (long long i = r0 * Hq + at; i < r1 * Hq && lse != nullptr; i += step) lse[i] = -CUDART_INF_F;
+  };
+  const long long at = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
+  const long long step = static_cast<long long>(gridDim.x) * blockDim.x;
+  blank(0, offset_of(q_offsets, T, 0), at, step);
+  blank(max(offset_of(q_offsets, T, B - 1), offset_of(q_offsets, T, B)), T, at, step);
+  const int lane = threadIdx.x & 31;
+  for (long long k = threadIdx.x - lane; blockIdx.x + k * gridDim.x < B; k += blockDim.x)
+    for (int i = 0; i < 32 && blockIdx.x + (k + i) * gridDim.x < B; ++i) {
+      const long long b = blockIdx.x + (k + i) * gridDim.x;
+      blank(static_cast<long long>(offset_of(q_offsets, T, b)) + max_q, offset_of(q_offsets, T, b + 1), lane, 32);
+    }
+}
+
 // Partial results of an item cut by ranges: block i of the line left two slots of
 // ROWS rows' D sums each (in the kernel's own order), then (reference, sum of
 // weights) per row; its item's first piece is in slot 1, any other in slot 0.
@@ -102,6 +143,7 @@ __device__ __forceinline__ void join_pieces(const Partials<D, ROWS> &ps, int r, 
 // One sequence of 32768 tokens and 64 of 1000 give the same picture.
 constexpr int few_rows(int bits, int D) { return bits * D == 512 ? 32 : 16; }
 
+int launch_kv_blank(__half *out, float *lse, long long rows, int D, cudaStream_t s);
 size_t kv_decode_workspace(int D, long long rows);
 int launch_kv_decode(const KvAttnParams &p, int bits, int D, cudaStream_t s);
 size_t kv_prefill_workspace(int D);

@@ -549,6 +549,7 @@ __global__ void __launch_bounds__(kThreads, Plan<BITS, D, NT>::BLOCKS)
   Desc *descs = reinterpret_cast<Desc *>(p.ws);
   float *parts = reinterpret_cast<float *>(descs + gridDim.x);
   if (threadIdx.x == 0) descs[blockIdx.x].last = -1;
+  if (__any_sync(0xffffffffu, some_unowned(p))) blank_unowned<D>(p.out, p.lse, p.q_offsets, p.T, p.Hq, p.B, p.max_q);
   if (c0 >= c1) return;
 
   int q0, nq, len, first, nu, nrb;

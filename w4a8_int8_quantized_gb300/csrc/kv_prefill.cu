@@ -324,6 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
   Desc *descs = reinterpret_cast<Desc *>(p.ws);
   float *parts = reinterpret_cast<float *>(descs + gridDim.x);
   if (threadIdx.x == 0) descs[blockIdx.x].last = -1;
+  if (__any_sync(0xffffffffu, some_unowned(p))) blank_unowned<D>(p.out, p.lse, p.q_offsets, p.T, p.Hq, p.B, p.max_q);
   if (c0 >= c1) return;
   if (upto - mine <= c0 && c0 < upto) {
     first_e = threadIdx.x * per_thread;
@@ -1058,7 +1059,22 @@ int launch_t(const KvAttnParams &p, cudaStream_t s) {
   return launch_status();
 }
 
+// Every row: a call with queries and no sequence.
+__global__ void __launch_bounds__(256) kv_blank_kernel(uint4 *out, long long vectors, float *lse, long long rows) {
+  const long long at = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x, step = static_cast<long long>(gridDim.x) * 256;
+  for (long long i = at; i < vectors; i += step) out[i] = make_uint4(0, 0, 0, 0);
+  if (lse != nullptr)
+    for (long long i = at; i < rows; i += step) lse[i] = -CUDART_INF_F;
+}
+
 }  // namespace
+
+int launch_kv_blank(__half *out, float *lse, long long rows, int D, cudaStream_t s) {
+  const long long vectors = rows * D / 8, want = (vectors + 255) / 256;
+  kv_blank_kernel<<<static_cast<int>(want < kNumSMsGB300 * 8 ? want : kNumSMsGB300 * 8), 256, 0, s>>>(
+      reinterpret_cast<uint4 *>(out), vectors, lse, rows);
+  return launch_status();
+}
 
 size_t kv_prefill_workspace(int D) {
   return kNumSMsGB300 * (sizeof(Desc) + 2 * sizeof(float) * kRows * (D + 2));
