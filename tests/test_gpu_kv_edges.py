@@ -156,3 +156,13 @@ def test_no_sequences(T):
                           q_offsets=torch.zeros(1, dtype=torch.int32, device="cuda"), return_lse=True, out=out, lse=lse)
     assert not out.any() and (lse == -np.inf).all()
     assert w8.w8a8_check_status() == 0
+
+
+@pytest.mark.parametrize("new", [[45, 1], [300, 20]])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 5])
+def test_window_without_bound_and_queries_before_every_key(new, window):
+    """The largest window with more queries than tokens: positions far below zero."""
+    rng = np.random.default_rng(sum(new))
+    c = Cache(rng, [37, 40], 2, 128, 16, 4)
+    q = rows(rng, sum(new), 8, 128)
+    check(c, q, new, *attend(c, q, new, max_q=max(new), window=window), window=window)

@@ -66,10 +66,11 @@ __device__ __forceinline__ void seq_of(const KvAttnParams &p, int b, int &q0, in
 }
 
 // Keys that the query at position pos of a sequence of len tokens sees:
-// [lo, hi).  pos may be negative (more queries than tokens): nothing.
+// [lo, hi).  pos may be negative (more queries than tokens): nothing.  (The window is
+// not taken from a position before its end: for a window near 2^31 that wraps.)
 __device__ __forceinline__ void visible(const KvAttnParams &p, int pos, int len, int &lo, int &hi) {
   hi = p.causal ? min(pos + 1, len) : len;
-  lo = p.window > 0 ? max(pos + 1 - p.window, 0) : 0;
+  lo = p.window > 0 && pos >= p.window ? pos + 1 - p.window : 0;
 }
 
 __device__ __forceinline__ int entry_of(const KvAttnParams &p, int b, int i) {
