@@ -166,3 +166,17 @@ def test_window_without_bound_and_queries_before_every_key(new, window):
     c = Cache(rng, [37, 40], 2, 128, 16, 4)
     q = rows(rng, sum(new), 8, 128)
     check(c, q, new, *attend(c, q, new, max_q=max(new), window=window), window=window)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("new,n", [(1, 40), (2, 5000), (60, 60), (60, 5000)])
+def test_outputs_at_the_largest_half(bits, new, n):
+    """Values of +-65504 (infinite ones are stored so) average to themselves, not to infinity."""
+    rng = np.random.default_rng(bits + new + n)
+    c = Cache(rng, [n], 2, 128, 16, bits)
+    q = rows(rng, new, 8, 128)
+    c.v[0][..., 5], c.v[0][..., 70] = np.inf, -65504
+    w8.kv_cache_write(cuda(c.k[0]), cuda(c.v[0]), cuda(c.slots(0, np.arange(n))), c.handle)
+    out, lse = attend(c, q, [new], max_q=new)
+    assert torch.isfinite(out).all()
+    check(c, q, [new], out, lse)

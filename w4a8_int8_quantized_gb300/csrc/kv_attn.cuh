@@ -7,17 +7,22 @@
 
 namespace w8a8 {
 
+// Two outputs as fp16.  They are averages of values of at most 65504, which the weights'
+// rounding to fp16 may take past 65520, where a plain rounding gives infinity: the largest
+// finite value stands for those.  NaN stays NaN.
+__device__ __forceinline__ uint32_t output2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
 // Four elements d .. d + 3 of a row from its unnormalised sums x and its sum
 // of weights l, both against reference m (base 2).
 template <int D>
 __device__ __forceinline__ void store_row4(const KvAttnParams &p, long long row, int d, float4 x,
                                            float m, float l) {
   const float r = l == 0.f ? 0.f : 1.f / l;
-  const __half2 a = __floats2half2_rn(x.x * r, x.y * r), b = __floats2half2_rn(x.z * r, x.w * r);
-  uint2 o;
-  o.x = *reinterpret_cast<const uint32_t *>(&a);
-  o.y = *reinterpret_cast<const uint32_t *>(&b);
-  *reinterpret_cast<uint2 *>(p.out + row * D + d) = o;
+  *reinterpret_cast<uint2 *>(p.out + row * D + d) = make_uint2(output2(x.x * r, x.y * r), output2(x.z * r, x.w * r));
   if (d == 0 && p.lse != nullptr)
     p.lse[row] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * kLn2;
 }

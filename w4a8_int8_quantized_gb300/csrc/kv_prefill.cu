@@ -627,9 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvAttnPar
             // at 4 bits columns 2 s, 2 s + 1 of an 8 are d = s and s + 4
             auto pair = [&](int i) {
               const int c0 = BITS == 4 ? (i < 2 ? 4 * i : 4 * i - 7) : 2 * i, c1 = BITS == 4 ? c0 + 2 : c0 + 1;
-              const __half2 z = __floats2half2_rn(__uint_as_float(v[8 * n + c0]) * inv,
-                                                  __uint_as_float(v[8 * n + c1]) * inv);
-              return *reinterpret_cast<const uint32_t *>(&z);
+              return output2(__uint_as_float(v[8 * n + c0]) * inv, __uint_as_float(v[8 * n + c1]) * inv);
             };
             dst[n] = make_uint4(pair(0), pair(1), pair(2), pair(3));
           }
