@@ -180,3 +180,17 @@ def test_outputs_at_the_largest_half(bits, new, n):
     out, lse = attend(c, q, [new], max_q=new)
     assert torch.isfinite(out).all()
     check(c, q, [new], out, lse)
+
+
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_scores_far_from_zero(new, sign):
+    """A score of 1e33 in either direction, the only one of its row: its value."""
+    rng = np.random.default_rng(new)
+    c = Cache(rng, [new], 2, 128, 16, 8)
+    q = rows(rng, new, 2, 128)
+    out, lse = attend(c, q, [new], max_q=new, softmax_scale=sign * 1e32, window=1)
+    _, _, vc, vs = c.quantized(0)
+    want = vc * vs[..., None]
+    np.testing.assert_allclose(out.double().cpu().numpy(), want, rtol=2.0 ** -10, atol=2.0 ** -24)
+    assert torch.isfinite(lse).all()

@@ -157,8 +157,9 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // so a weight is below 2^kRoom (fp16 holds 2^15.99) and the largest one at least 1:
 // what fp16 cannot hold, under 2^-25, is under 2^-25 of it.  (Set 7 below that u,
 // weights above 2^-21 stayed normal numbers, but M moved more often: a prompt took
-// 201 us against 180.)  A row starts at kNoRef, under every u.
-constexpr float kRoom = 15.f, kNoRef = -1e30f;
+// 201 us against 180.)  A row starts at kNoRef, under every u but the very last that
+// 32 bits hold.
+constexpr float kRoom = 15.f, kNoRef = -3e38f;
 
 // What stands for s_v where it is 0.  All codes are 0 there, so the products do not
 // need it, but u and with it M do: it lies below every scale that is ever stored (the
