@@ -194,3 +194,22 @@ def test_scores_far_from_zero(new, sign):
     want = vc * vs[..., None]
     np.testing.assert_allclose(out.double().cpu().numpy(), want, rtol=2.0 ** -10, atol=2.0 ** -24)
     assert torch.isfinite(lse).all()
+
+
+def test_more_sequences_times_heads_than_32_bits_hold():
+    B, heads = 1 << 21, 1024
+    cache = w8.KVCache.empty(1, heads, 16, 64)
+    x = torch.randn(16, heads, 64, device="cuda").half()
+    w8.kv_cache_write(x, x, torch.arange(16, device="cuda"), cache)
+    new = torch.zeros(B, dtype=torch.int32, device="cuda")
+    lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+    new[[5, B // 2, B - 1]] = 1
+    lens[[5, B // 2, B - 1]] = torch.tensor([3, 16, 7], dtype=torch.int32, device="cuda")
+    off = torch.zeros(B + 1, dtype=torch.int32, device="cuda")
+    off[1:] = new.cumsum(0).int()
+    q = torch.randn(3, heads, 64, device="cuda").half()
+    out = w8.kv_cache_attention(q, cache, torch.zeros(B, 1, dtype=torch.int32, device="cuda"), lens, q_offsets=off, max_q=1)
+    want = w8.kv_cache_attention(q, cache, torch.zeros(3, 1, dtype=torch.int32, device="cuda"),
+                                 torch.tensor([3, 16, 7], dtype=torch.int32, device="cuda"))
+    assert torch.equal(out, want)
+    assert w8.w8a8_check_status() == 0

@@ -770,7 +770,7 @@ long long most_units(const KvAttnParams &p) {
   const long long rb = (static_cast<long long>(p.max_q) * p.group + PL::COLS - 1) / PL::COLS;
   // + 15: the first unit starts on a multiple of 16 before the first key
   const long long units = tokens > 0 ? (tokens + 15 + PL::UNIT - 1) / PL::UNIT : 1;
-  return p.B * p.kv.heads * rb * units;
+  return static_cast<long long>(p.B) * p.kv.heads * rb * units;
 }
 
 // The kernel's shared memory, allowed once per device.
@@ -815,7 +815,7 @@ int launch_t(const KvAttnParams &p, cudaStream_t s) {
     cfg.gridDim = dim3(static_cast<unsigned>(grid), static_cast<unsigned>(most < PL::COLS ? most : PL::COLS));
     // items of many pieces: more warps fetch them (131072 tokens, 57 pieces: 4 warps
     // 40 us in all, 8 warps 38; 64 sequences, 2 pieces: 82 and 84)
-    const bool many = grid / (p.B * p.kv.heads) >= 32;
+    const bool many = grid / (static_cast<long long>(p.B) * p.kv.heads) >= 32;
     cfg.blockDim = dim3(many ? 256 : 128);
     cfg.dynamicSmemBytes = 0;
     if (cudaLaunchKernelEx(&cfg, many ? kv_decode_join_kernel<D, NT, 8> : kv_decode_join_kernel<D, NT, 4>,
