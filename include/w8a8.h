@@ -331,7 +331,8 @@ size_t kv_cache_attention_workspace_bytes(int T, int q_heads, int B, int max_q, 
  *               q_offsets[b + 1] - 1; NULL: one query per sequence (T == B)
  *   max_q       upper bound of the queries of one sequence (T is always
  *               one; a close bound makes a better launch)
- *   block_table int32 [B, table_width]: page ids of the sequence's tokens
+ *   block_table int32 [B, table_width]: page ids of the sequence's tokens;
+ *               table_width * page_size is at most 2^31 - 65536
  *   seq_lens    int32 [B]: tokens of the sequence in the cache, the queries'
  *               own included (write them first)
  *   softmax_scale  of the scores, 1 / sqrt(D) usually

@@ -137,7 +137,7 @@ int kv_cache_attention(const w8a8_half *q, long long q_token_stride, long long q
       !isfinite(softmax_scale))
     return W8A8_ERR_INVALID_ARG;
   if (q_offsets == nullptr && T != B) return W8A8_ERR_INVALID_ARG;
-  if (static_cast<long long>(table_width) * cache->page_size > 0x7fffffffLL)
+  if (static_cast<long long>(table_width) * cache->page_size > kMaxTokens)
     return W8A8_ERR_INVALID_ARG;
   if (T == 0) return W8A8_OK;
   if (B == 0) {  // no sequence owns a row

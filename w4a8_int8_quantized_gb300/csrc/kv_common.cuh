@@ -24,6 +24,11 @@ struct KvView {
 
 constexpr int kMinPage = 16, kMaxPage = 1024;
 
+// Tokens that a table may hold.  Token positions are 32-bit numbers, also those of the
+// last unit of work that lie past a sequence's end (fewer than 1024): they must not wrap,
+// or they would pass as positions before it, and the table be read before its start.
+constexpr long long kMaxTokens = 0x80000000LL - 65536;
+
 struct KvAttnParams {
   KvView kv;
   const __half *q;
