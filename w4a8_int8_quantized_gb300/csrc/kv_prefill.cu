@@ -1011,13 +1011,13 @@ bool allow_smem() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
   std::lock_guard<std::mutex> lock(mu);
-  if (!done[dev])
+  if (!done[dev]) {
+    // the warpgroups' register shares add up to what a launch with 128 brings
+    cudaFuncAttributes a;
     done[dev] = cudaFuncSetAttribute(kv_prefill_kernel<BITS, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     Plan<D>::SMEM) == cudaSuccess;
-  // the warpgroups' register shares add up to what a launch with 128 brings
-  cudaFuncAttributes a;
-  if (done[dev] && (cudaFuncGetAttributes(&a, kv_prefill_kernel<BITS, D>) != cudaSuccess || a.numRegs != 128))
-    done[dev] = false;
+                                     Plan<D>::SMEM) == cudaSuccess &&
+                cudaFuncGetAttributes(&a, kv_prefill_kernel<BITS, D>) == cudaSuccess && a.numRegs == 128;
+  }
   return done[dev];
 }
 
