@@ -4,6 +4,8 @@ References and tolerances are those of kv_reference."""
 import numpy as np
 import pytest
 
+import kv_reference as ref
+
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
@@ -213,3 +215,24 @@ def test_more_sequences_times_heads_than_32_bits_hold():
                                  torch.tensor([3, 16, 7], dtype=torch.int32, device="cuda"))
     assert torch.equal(out, want)
     assert w8.w8a8_check_status() == 0
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+def test_every_magnitude(bits):
+    """Every finite fp16 value as a row's largest: its scale and the codes of the row, half of
+    them within a few units in the last place of a tie."""
+    rng = np.random.default_rng(bits)
+    most = np.arange(0, 0x7c00, dtype=np.uint16).view(np.float16)
+    T, qmax, page = len(most), 2 ** (bits - 1) - 1, 1024
+    x = rng.uniform(-1, 1, (T, 1, 64)) * most[:, None, None].astype(np.float64)
+    ties = (rng.integers(-qmax, qmax, (T, 1, 32)) + 0.5) / qmax * most[:, None, None].astype(np.float64)
+    x[..., :32] = ties
+    x = x.astype(np.float16)
+    x[..., 40] = most[:, None]
+    cache = w8.KVCache.empty(-(-T // page), 1, page, 64, bits)
+    slots = np.arange(T)
+    w8.kv_cache_write(cuda(x), cuda(-x), cuda(slots), cache)
+    q, s = ref.quantize(x, bits)
+    for codes, scale, sign in ((cache.k_codes, cache.k_scale, 1), (cache.v_codes, cache.v_scale, -1)):
+        np.testing.assert_array_equal(scale.cpu().numpy()[slots // page, :, slots % page], s.astype(np.float32))
+        np.testing.assert_array_equal(codes.cpu().numpy()[slots // page, :, slots % page], ref.pack(sign * q, bits))
