@@ -500,7 +500,8 @@ def kv_cache_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tenso
     block_table int32 [B, pages], seq_lens int32 [B]; q_offsets int32 [B + 1]
     (None: one query per sequence); max_q: upper bound of one sequence's
     queries (default T).  causal, window: which keys a query sees.  Returns out
-    fp16 [T, q_heads, D], or (out, lse fp32 [T, q_heads]) with return_lse."""
+    fp16 [T, q_heads, D], or (out, lse fp32 [T, q_heads]) with return_lse.  Rows
+    that see no key, and rows of no sequence, hold 0 (lse -inf)."""
     ts, hs, T, heads = _rows(cache, q, "q", None, None)
     device = cache.device
     if not (isinstance(block_table, torch.Tensor) and block_table.dtype is _INT

@@ -145,7 +145,8 @@ __device__ __forceinline__ void join_pieces(const Partials<D, ROWS> &ps, int r, 
 //   8 bits, 128   46, 68    72, 68   129, 69
 //   4 bits,  64   37, 51    55, 51    93, 52
 //   8 bits,  64   29, 51    43, 51    71, 51
-// One sequence of 32768 tokens and 64 of 1000 give the same picture.
+// (the bytes alone: 10.3, 19.9, 5.4 and 10.3).  One sequence of 32768 tokens and 64 of
+// 1000 give the same picture.
 constexpr int few_rows(int bits, int D) { return bits * D == 512 ? 32 : 16; }
 
 int launch_kv_blank(__half *out, float *lse, long long rows, int D, cudaStream_t s);

@@ -160,7 +160,9 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // The running reference M of a row's exponents.  Weights are 2^(u - M); M is the
 // largest u seen when it was set and moves only when some u passes it by kRoom,
 // so a weight is below 2^kRoom (fp16 holds 2^15.99) and the largest one at least 1:
-// what fp16 cannot hold, under 2^-25, is under 2^-25 of it.  (Set 7 below that u,
+// what fp16 cannot hold, under 2^-25, is under 2^-25 of it.  That is a key's share: n keys
+// just under it, behind a dominant one, hold up to n 2^-25 together (0.4 % at 131072),
+// which the row's sum counts and the output does not.  (Set 7 below that u,
 // weights above 2^-21 stayed normal numbers, but M moved more often: a prompt took
 // 201 us against 180.)  A row starts at kNoRef, under every u but the very last that
 // 32 bits hold.

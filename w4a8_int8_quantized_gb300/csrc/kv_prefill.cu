@@ -27,7 +27,7 @@
 // Softmax, with the codes exact and both scales in fp32: u = S (scale log2e s_k)
 // + log2 s_v, p = 2^(u - M), O = sum p code_v, l = sum p / s_v.  M is the lazy
 // reference of kv_common.cuh, a row's own: O is rescaled (TMEM to TMEM) only when
-// some row of the warp passes it.  Tokens past the length get s_k = 0,
+// some row of the warp passes it.  Tokens that no row of the item sees get s_k = 0,
 // log2 s_v = -inf, 1 / s_v = 0, so only tiles at a row's causal end or window
 // start test single keys.
 //
