@@ -361,6 +361,122 @@ int kv_cache_attention(const w8a8_half *q, long long q_token_stride, long long q
                        void *workspace, size_t ws_bytes, w8a8_half *out, float *lse,
                        w8a8_stream_t stream);
 
+/* ---- the norm in front of a layer --------------------------------------
+ *
+ * Root-mean-square norm of fp16 rows, with the residual's addition before it
+ * and, instead of fp16 values, the 8-bit codes that the next layer reads:
+ *   h = fp16_rn(x + residual)            (h = x without a residual)
+ *   v = h * weight / sqrt(mean(h^2) + eps)
+ * v is an fp32 value (h * weight is exact, the sums are fp32); it is rounded
+ * once, to fp16 or to codes.  A row of zeros with eps 0 gives zeros.  No
+ * counterpart on the method's pages, which start at the layer's input: an
+ * addition of this library.  The conventions at the top of this file hold;
+ * x, residual, weight and all outputs are 16-byte aligned, K is a multiple of
+ * 16.
+ *   x            fp16 [M, K]
+ *   residual     fp16 [M, K], or NULL
+ *   weight       fp16 [K]
+ *   eps          >= 0, finite
+ *   residual_out fp16 [M, K] (out) h; may be residual or x itself; NULL if
+ *                and only if residual is NULL
+ * Other overlaps of an output with an input are not allowed. */
+
+/* Code formats of rms_norm_quantize(). */
+#define W8A8_CODES_INT8 0 /* int8, scales as quantize_act_per_token */
+#define W8A8_CODES_HALF 1 /* the same codes as fp16 values, as quantize_act_per_token_h */
+#define W8A8_CODES_FP8 2  /* e4m3, scales as quantize_act_fp8 */
+
+/* y fp16 [M, K] (out). */
+int rms_norm(const w8a8_half *x, const w8a8_half *residual, const w8a8_half *weight, int M, int K,
+             float eps, w8a8_half *residual_out, w8a8_half *y, w8a8_stream_t stream);
+
+/* Codes and scales of v.
+ *   format     W8A8_CODES_INT8 / _HALF: group_size 0, 64 or 128 (K a multiple
+ *              of it); q int8 or fp16 [M, K], scale fp32 [M, G].
+ *              W8A8_CODES_FP8: group_size 128; q e4m3 [M, K], scale e8m0
+ *              [M, ceil(K / 128)]. */
+int rms_norm_quantize(const w8a8_half *x, const w8a8_half *residual, const w8a8_half *weight, int M,
+                      int K, float eps, int format, int group_size, w8a8_half *residual_out, void *q,
+                      void *scale, w8a8_stream_t stream);
+
+/* ---- layers in 8-bit floats ---------------------------------------------
+ *
+ * The layer and a decoder's gated feed-forward block with e4m3 operands: the
+ * tensor cores' 8-bit float rate is twice the fp16 rate that the INT8 layer
+ * runs at on this GPU.  No counterpart on the method's pages: an addition of
+ * this library.
+ *
+ * Format of a row of K elements (weights and activations alike): e4m3 codes
+ * (1 byte: sign, 4 exponent bits, 3 mantissa bits, largest 448, no
+ * infinities) and one e8m0 scale byte b, 2^(b - 127), for every 128
+ * consecutive elements, the last group possibly shorter: ceil(K / 128) bytes.
+ * The quantizers' scale is the smallest power of two s with max|x| / s <= 448,
+ * 1 for a group of zeros and at least 2^-126; a code is e4m3_rn(x / s), ties
+ * to even.  The products take any codes but NaN (0x7f, 0xff) and scale bytes
+ * 1 .. 254.
+ *
+ * The conventions at the top of this file hold, with K (and F) a multiple of
+ * 16, code pointers 16-byte aligned and scale pointers at any address.  Sums
+ * are fp32 (the products of two codes are exact), rounded once to the output's
+ * type; their order depends on the sizes, not on timing. */
+
+/* fp16 rows to codes and scales.
+ *   x   fp16 [M, K];  xq e4m3 [M, K] (out);  scale_a e8m0 [M, ceil(K/128)] (out) */
+int quantize_act_fp8(const w8a8_half *x, int M, int K, uint8_t *xq, uint8_t *scale_a,
+                     w8a8_stream_t stream);
+/* The same for weights [N, K] (a launch that no later kernel overlaps). */
+int quantize_weight_fp8(const w8a8_half *W, int N, int K, uint8_t *Wq, uint8_t *scale_w,
+                        w8a8_stream_t stream);
+
+/* y[m, n] = fp16_rn(sum_k x[m, k] w[n, k]) over the values that the codes stand
+ * for.
+ *   xq e4m3 [M, K], scale_a e8m0 [M, ceil(K/128)]; Wq e4m3 [N, K], scale_w e8m0
+ *   [N, ceil(K/128)]; y fp16 [M, N] (out)
+ * All products here are launched with programmatic stream serialization, and
+ * the few-row kernels may read the weights (only these and their scales) before
+ * the previous kernel on the stream has finished: see w8a8_mv. */
+int fp8_gemm(const uint8_t *xq, const uint8_t *scale_a, const uint8_t *Wq, const uint8_t *scale_w,
+             int M, int N, int K, w8a8_half *y, w8a8_stream_t stream);
+
+/* Activations of the gated block. */
+#define W8A8_GATE_SILU 0 /* g / (1 + exp(-g)) */
+#define W8A8_GATE_GELU 1 /* g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2 */
+
+/* Both projections of a gated feed-forward block, the activation and the
+ * product in one kernel: h[m, f] = act(x Wg^T)[m, f] * (x Wu^T)[m, f], an fp32
+ * value, as fp16 (h) or as codes with scales (hq, scale_h).
+ *   xq, scale_a  as fp8_gemm;  Wg, Wu e4m3 [F, K] with scale_g, scale_u
+ *   h        fp16 [M, F] (out), or NULL for codes
+ *   hq       e4m3 [M, F], scale_h e8m0 [M, ceil(F/128)] (out), both NULL with h;
+ *            F a multiple of 16, at most 32768 (the K of a product to come) */
+int fp8_gated_gemm(const uint8_t *xq, const uint8_t *scale_a, const uint8_t *Wg,
+                   const uint8_t *scale_g, const uint8_t *Wu, const uint8_t *scale_u, int M, int F,
+                   int K, int activation, w8a8_half *h, uint8_t *hq, uint8_t *scale_h,
+                   w8a8_stream_t stream);
+
+/* Bytes of workspace of fp8_linear() (0 for invalid sizes). */
+size_t fp8_linear_workspace_bytes(int M, int K);
+
+/* The whole layer: quantize_act_fp8 into the workspace, then fp8_gemm.
+ *   x fp16 [M, K]; Wq, scale_w as fp8_gemm; y fp16 [M, N] (out)
+ *   workspace  at least fp8_linear_workspace_bytes(M, K), 256-byte aligned, else
+ *              W8A8_ERR_WORKSPACE; its content does not matter */
+int fp8_linear(const w8a8_half *x, const uint8_t *Wq, const uint8_t *scale_w, int M, int N, int K,
+               void *workspace, size_t ws_bytes, w8a8_half *y, w8a8_stream_t stream);
+
+/* Bytes of workspace of fp8_feed_forward() (0 for invalid sizes). */
+size_t fp8_feed_forward_workspace_bytes(int M, int K, int F);
+
+/* The whole gated feed-forward block: quantize_act_fp8, fp8_gated_gemm to codes,
+ * fp8_gemm: y = ((act(x Wg^T) * (x Wu^T)) as codes) Wd^T.
+ *   x fp16 [M, K]; Wg, Wu e4m3 [F, K]; Wd e4m3 [N, F]; y fp16 [M, N] (out)
+ *   workspace  at least fp8_feed_forward_workspace_bytes(M, K, F), 256-byte
+ *              aligned, else W8A8_ERR_WORKSPACE; its content does not matter */
+int fp8_feed_forward(const w8a8_half *x, const uint8_t *Wg, const uint8_t *scale_g,
+                     const uint8_t *Wu, const uint8_t *scale_u, const uint8_t *Wd,
+                     const uint8_t *scale_d, int M, int K, int F, int N, int activation,
+                     void *workspace, size_t ws_bytes, w8a8_half *y, w8a8_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

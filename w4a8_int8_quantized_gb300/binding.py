@@ -32,7 +32,10 @@ EXPORTS = ("w8a8_is_available", "w8a8_status_string", "w8a8_check_status",
            "w8a8_gemm", "w8a8_mv", "w4a8_gemm", "quantize_act_per_token_h", "w8a8_gemm_h",
            "w8a8_linear_workspace_bytes", "linear", "linear_noalloc", "w8a8_gemm_i32",
            "w8a8_test_set_fault", "weight_only_gemm", "kv_cache_write", "kv_cache_read",
-           "kv_cache_attention_workspace_bytes", "kv_cache_attention")
+           "kv_cache_attention_workspace_bytes", "kv_cache_attention", "rms_norm",
+           "rms_norm_quantize", "quantize_act_fp8", "quantize_weight_fp8", "fp8_gemm",
+           "fp8_gated_gemm", "fp8_linear_workspace_bytes", "fp8_linear",
+           "fp8_feed_forward_workspace_bytes", "fp8_feed_forward")
 
 
 class W8A8Error(RuntimeError):
@@ -76,6 +79,16 @@ def load(path: str | None = None):
             "kv_cache_attention_workspace_bytes": ([I, I, I, I, I, P], Z),
             "kv_cache_attention": ([P, L, L, I, I, P, I, I, P, I, P, P, ctypes.c_float, I, I, P,
                                     Z, P, P, P], I),
+            "rms_norm": ([P, P, P, I, I, ctypes.c_float, P, P, P], I),
+            "rms_norm_quantize": ([P, P, P, I, I, ctypes.c_float, I, I, P, P, P, P], I),
+            "quantize_act_fp8": ([P, I, I, P, P, P], I),
+            "quantize_weight_fp8": ([P, I, I, P, P, P], I),
+            "fp8_gemm": ([P, P, P, P, I, I, I, P, P], I),
+            "fp8_gated_gemm": ([P, P, P, P, P, P, I, I, I, I, P, P, P, P], I),
+            "fp8_linear_workspace_bytes": ([I, I], Z),
+            "fp8_linear": ([P, P, P, I, I, I, P, Z, P, P], I),
+            "fp8_feed_forward_workspace_bytes": ([I, I, I], Z),
+            "fp8_feed_forward": ([P, P, P, P, P, P, P, I, I, I, I, I, P, Z, P, P], I),
         }
         for name, (args, res) in sig.items():
             f = getattr(lib, name)
@@ -544,3 +557,243 @@ def kv_cache_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tenso
     if status:
         _check(status, "kv_cache_attention")
     return (out, lse) if return_lse else out
+
+
+# ---- the norm and the layers in 8-bit floats --------------------------------
+#
+# A decoding step's calls again: plain comparisons first, the words only when
+# one fails.
+
+_E4M3, _E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+_CODES = {"int8": (0, torch.int8), "half": (1, _HALF), "fp8": (2, _E4M3)}
+_GATES = {"silu": 0, "gelu": 1}
+
+
+def _rows_of(t, dtype, name: str, device=None, rows=None, cols=None):
+    """Sizes of t, a contiguous [rows, cols] of this type (None: any) on the device
+    (None: any CUDA device, which has to be the current one)."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == 2 and t.is_cuda
+            and t.is_contiguous() and (device is None or t.device == device)):
+        r, c = t.shape
+        if (rows is None or r == rows) and (cols is None or c == cols):
+            return r, c
+    _need(t, dtype, name)
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    raise ValueError(f"{name} must have shape {(rows, cols)} (None: any), got {tuple(t.shape)}")
+
+
+def _current(device) -> int:
+    """The current stream of the device, which has to be the current one."""
+    index = device.index
+    if _current_device() != index:
+        raise ValueError(f"the tensors are on {device}, which is not the current device")
+    return _raw_stream(index)
+
+
+def _given(t, dtype, name: str, device, rows: int, cols: int):
+    """t, checked, or a new [rows, cols] for it."""
+    if t is None:
+        return torch.empty((rows, cols), dtype=dtype, device=device)
+    _rows_of(t, dtype, name, device, rows, cols)
+    return t
+
+
+def _held(q, scale, name: str, device=None, rows=None, cols=None):
+    """Sizes of rows of 8-bit floats: e4m3 codes and their e8m0 scales."""
+    r, c = _rows_of(q, _E4M3, name, device, rows, cols)
+    _rows_of(scale, _E8M0, "the scales of " + name, q.device, r, (c + 127) >> 7)
+    return r, c
+
+
+def _scratch(workspace, need: int, device):
+    if workspace is None:
+        return torch.empty(need or 1, dtype=torch.uint8, device=device)
+    if not (isinstance(workspace, torch.Tensor) and workspace.dtype is torch.uint8
+            and workspace.device == device and workspace.is_contiguous()):
+        raise ValueError(f"workspace must be a contiguous torch.uint8 tensor on {device}")
+    return workspace
+
+
+def _norm_args(x, weight, residual, residual_out):
+    M, K = _rows_of(x, _HALF, "x")
+    device = x.device
+    if not (isinstance(weight, torch.Tensor) and weight.dtype is _HALF and weight.device == device
+            and weight.dim() == 1 and weight.shape[0] == K and weight.is_contiguous()):
+        _need(weight, _HALF, "weight", (K,))
+        raise ValueError(f"weight must be on {device}, got {weight.device}")
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out without a residual")
+        return M, K, device, 0, None, 0
+    _rows_of(residual, _HALF, "residual", device, M, K)
+    residual_out = _given(residual_out, _HALF, "residual_out", device, M, K)
+    return M, K, device, residual.data_ptr(), residual_out, residual_out.data_ptr()
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual=None, eps: float = 1e-5, y=None,
+             residual_out=None):
+    """Root-mean-square norm of fp16 x [M, K] with fp16 weight [K]: y fp16 [M, K].
+    With a residual [M, K], of h = fp16(x + residual): (y, h).  residual_out may
+    be the residual (or x) itself."""
+    M, K, device, r_at, h, h_at = _norm_args(x, weight, residual, residual_out)
+    y = _given(y, _HALF, "y", device, M, K)
+    status = (_lib or load()).rms_norm(x.data_ptr(), r_at, weight.data_ptr(), M, K, eps, h_at,
+                                       y.data_ptr(), _current(device))
+    if status:
+        _check(status, "rms_norm")
+    return y if h is None else (y, h)
+
+
+def rms_norm_quantize(x: torch.Tensor, weight: torch.Tensor, residual=None, eps: float = 1e-5,
+                      codes: str = "int8", group_size: int | None = None, q=None, scale=None,
+                      residual_out=None):
+    """rms_norm() with the result as 8-bit codes: (q [M, K], scale), with a residual
+    (q, scale, h).  codes "int8": int8, fp32 scales [M, G] as
+    quantize_act_per_token (group_size 0, 64 or 128; default 0); "half": the same
+    codes as fp16 values, as quantize_act_per_token_h; "fp8": float8_e4m3fn,
+    float8_e8m0fnu scales [M, ceil(K / 128)] as quantize_act_fp8."""
+    if codes not in _CODES:
+        raise ValueError(f"codes must be one of {sorted(_CODES)}, got {codes!r}")
+    form, dtype = _CODES[codes]
+    if group_size is None:
+        group_size = 128 if form == 2 else 0
+    if group_size not in ((128,) if form == 2 else (0, 64, 128)):
+        raise ValueError(f"group_size must be {'128' if form == 2 else '0, 64 or 128'} "
+                         f"for {codes} codes, got {group_size}")
+    M, K, device, r_at, h, h_at = _norm_args(x, weight, residual, residual_out)
+    q = _given(q, dtype, "q", device, M, K)
+    if form == 2:
+        scale = _given(scale, _E8M0, "scale", device, M, (K + 127) >> 7)
+    else:
+        scale = _given(scale, _FLOAT, "scale", device, M, _groups(K, group_size))
+    status = (_lib or load()).rms_norm_quantize(x.data_ptr(), r_at, weight.data_ptr(), M, K, eps,
+                                                form, group_size, h_at, q.data_ptr(),
+                                                scale.data_ptr(), _current(device))
+    if status:
+        _check(status, "rms_norm_quantize")
+    return (q, scale) if h is None else (q, scale, h)
+
+
+def _quantize_fp8(name: str, x, q, scale):
+    M, K = _rows_of(x, _HALF, "W" if name == "quantize_weight_fp8" else "x")
+    device = x.device
+    q = _given(q, _E4M3, "the codes", device, M, K)
+    scale = _given(scale, _E8M0, "the scales", device, M, (K + 127) >> 7)
+    status = getattr(_lib or load(), name)(x.data_ptr(), M, K, q.data_ptr(), scale.data_ptr(),
+                                           _current(device))
+    if status:
+        _check(status, name)
+    return q, scale
+
+
+def quantize_act_fp8(x: torch.Tensor, xq=None, scale_a=None):
+    """fp16 x [M, K] -> (float8_e4m3fn xq [M, K], float8_e8m0fnu scale_a
+    [M, ceil(K / 128)])."""
+    return _quantize_fp8("quantize_act_fp8", x, xq, scale_a)
+
+
+def quantize_weight_fp8(W: torch.Tensor, Wq=None, scale_w=None):
+    """fp16 W [N, K] -> (float8_e4m3fn Wq [N, K], float8_e8m0fnu scale_w
+    [N, ceil(K / 128)])."""
+    return _quantize_fp8("quantize_weight_fp8", W, Wq, scale_w)
+
+
+def fp8_gemm(xq, scale_a, Wq, scale_w, y=None):
+    """Product of 8-bit float rows: xq [M, K] x Wq [N, K]^T -> fp16 y [M, N]."""
+    M, K = _held(xq, scale_a, "xq")
+    device = xq.device
+    N, _ = _held(Wq, scale_w, "Wq", device, None, K)
+    y = _given(y, _HALF, "y", device, M, N)
+    status = (_lib or load()).fp8_gemm(xq.data_ptr(), scale_a.data_ptr(), Wq.data_ptr(),
+                                       scale_w.data_ptr(), M, N, K, y.data_ptr(), _current(device))
+    if status:
+        _check(status, "fp8_gemm")
+    return y
+
+
+def _gate(activation: str) -> int:
+    if activation not in _GATES:
+        raise ValueError(f"activation must be one of {sorted(_GATES)}, got {activation!r}")
+    return _GATES[activation]
+
+
+def fp8_gated_gemm(xq, scale_a, Wg, scale_g, Wu, scale_u, activation: str = "silu",
+                   codes: bool = False, h=None, scale_h=None):
+    """act(x Wg^T) * (x Wu^T) of 8-bit float rows xq [M, K], Wg, Wu [F, K]: fp16
+    h [M, F], or with codes (float8_e4m3fn h [M, F], float8_e8m0fnu scale_h
+    [M, ceil(F / 128)]) for the next product.  activation "silu" or "gelu" (the
+    tanh form)."""
+    gate = _gate(activation)
+    M, K = _held(xq, scale_a, "xq")
+    device = xq.device
+    F, _ = _held(Wg, scale_g, "Wg", device, None, K)
+    _held(Wu, scale_u, "Wu", device, F, K)
+    h = _given(h, _E4M3 if codes else _HALF, "h", device, M, F)
+    if codes:
+        scale_h = _given(scale_h, _E8M0, "scale_h", device, M, (F + 127) >> 7)
+        out = 0, h.data_ptr(), scale_h.data_ptr()
+    elif scale_h is not None:
+        raise ValueError("scale_h without codes")
+    else:
+        out = h.data_ptr(), 0, 0
+    status = (_lib or load()).fp8_gated_gemm(
+        xq.data_ptr(), scale_a.data_ptr(), Wg.data_ptr(), scale_g.data_ptr(), Wu.data_ptr(),
+        scale_u.data_ptr(), M, F, K, gate, *out, _current(device))
+    if status:
+        _check(status, "fp8_gated_gemm")
+    return (h, scale_h) if codes else h
+
+
+def fp8_linear_workspace_bytes(M: int, K: int) -> int:
+    return int(load().fp8_linear_workspace_bytes(M, K))
+
+
+def fp8_linear(x, Wq, scale_w, workspace=None, y=None):
+    """The whole layer in 8-bit floats: quantize_act_fp8 of fp16 x [M, K], then the
+    product with Wq [N, K] -> fp16 y [M, N]."""
+    M, K = _rows_of(x, _HALF, "x")
+    device = x.device
+    N, _ = _held(Wq, scale_w, "Wq", device, None, K)
+    lib = _lib or load()
+    if workspace is None:
+        workspace = _scratch(None, lib.fp8_linear_workspace_bytes(M, K), device)
+    else:
+        _scratch(workspace, 0, device)
+    y = _given(y, _HALF, "y", device, M, N)
+    status = lib.fp8_linear(x.data_ptr(), Wq.data_ptr(), scale_w.data_ptr(), M, N, K,
+                            workspace.data_ptr(), workspace.numel(), y.data_ptr(),
+                            _current(device))
+    if status:
+        _check(status, "fp8_linear")
+    return y
+
+
+def fp8_feed_forward_workspace_bytes(M: int, K: int, F: int) -> int:
+    return int(load().fp8_feed_forward_workspace_bytes(M, K, F))
+
+
+def fp8_feed_forward(x, Wg, scale_g, Wu, scale_u, Wd, scale_d, activation: str = "silu",
+                     workspace=None, y=None):
+    """A gated feed-forward block in 8-bit floats: fp16 x [M, K], Wg, Wu [F, K] and
+    Wd [N, F] -> fp16 y [M, N] = (act(x Wg^T) * (x Wu^T)) Wd^T, x and the hidden
+    values as e4m3 codes."""
+    gate = _gate(activation)
+    M, K = _rows_of(x, _HALF, "x")
+    device = x.device
+    F, _ = _held(Wg, scale_g, "Wg", device, None, K)
+    _held(Wu, scale_u, "Wu", device, F, K)
+    N, _ = _held(Wd, scale_d, "Wd", device, None, F)
+    lib = _lib or load()
+    if workspace is None:
+        workspace = _scratch(None, lib.fp8_feed_forward_workspace_bytes(M, K, F), device)
+    else:
+        _scratch(workspace, 0, device)
+    y = _given(y, _HALF, "y", device, M, N)
+    status = lib.fp8_feed_forward(
+        x.data_ptr(), Wg.data_ptr(), scale_g.data_ptr(), Wu.data_ptr(), scale_u.data_ptr(),
+        Wd.data_ptr(), scale_d.data_ptr(), M, K, F, N, gate, workspace.data_ptr(),
+        workspace.numel(), y.data_ptr(), _current(device))
+    if status:
+        _check(status, "fp8_feed_forward")
+    return y

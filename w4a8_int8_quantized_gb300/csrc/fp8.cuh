@@ -1,0 +1,56 @@
+// The library's 8-bit float rows: e4m3 codes with one power-of-two scale (an
+// e8m0 byte: 2^(byte - 127)) for every 128 consecutive elements of a row, the
+// last group of a row possibly shorter.
+//
+// The scale of a group is the smallest 2^e with max|x| / 2^e <= 448 (the
+// largest e4m3 value), 1 for a group of zeros, and at least 2^-126, so that
+// 2^-e is a normal fp32 number too.  x / 2^e is then exact in fp32 (but for
+// results below 2^-126), and the only rounding is the one to e4m3 (to nearest,
+// ties to even): half a step, 2^-4 relative, or 2^-10 of the scale below 2^-6
+// of it.  A power of two costs a float format nothing but up to one of the 17
+// binades it spans, and the tensor core takes it as an operand, so that no sum
+// is rescaled in a pass of its own.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+namespace w8a8 {
+
+constexpr int kFp8Group = 128;
+
+// e8m0 byte of a group whose largest magnitude is a: a = 1.m 2^E against
+// 448 = 1.75 2^8.
+__device__ __forceinline__ uint32_t fp8_scale_byte(float a) {
+  const uint32_t b = __float_as_uint(a);
+  const int e = static_cast<int>(b >> 23) - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return a == 0.f ? 127u : static_cast<uint32_t>(e < 1 ? 1 : e);
+}
+
+// 2^(byte - 127) and its reciprocal, for bytes 1 .. 253
+__device__ __forceinline__ float fp8_scale(uint32_t byte) { return __uint_as_float(byte << 23); }
+__device__ __forceinline__ float fp8_scale_inverse(uint32_t byte) {
+  return __uint_as_float((254u - byte) << 23);
+}
+
+// Four e4m3 codes (element 0 in the low byte)
+__device__ __forceinline__ uint32_t fp8_pack4(float a, float b, float c, float d) {
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+  return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+}
+
+// act(g) u, with act(g) = g / (1 + exp(-t)): t = g is SiLU; t = 2 sqrt(2 / pi)
+// (g + 0.044715 g^3) is GELU in its tanh form, since (1 + tanh z) / 2 = 1 / (1 +
+// exp(-2 z)).  exp and the quotient are the approximate ones (a few 2^-22
+// relative for |t| below 16, and where |t| is larger the exponential hardly
+// counts or the value is below 1e-6 of g): far inside one rounding to fp16 or
+// e4m3, which follows.  exp(-t) = inf gives 0.
+template <bool GELU>
+__device__ __forceinline__ float gated(float g, float u) {
+  const float t = GELU ? 1.5957691216057308f * fmaf(0.044715f * g * g, g, g) : g;
+  return __fdividef(g, 1.f + __expf(-t)) * u;
+}
+
+}  // namespace w8a8

@@ -1,0 +1,31 @@
+// The 8-bit float products' launchers, shared by their translation units.
+#pragma once
+
+#include "common.cuh"
+
+namespace w8a8 {
+
+// y = x w[0]^T, or act(x w[0]^T) (x w[1]^T) where w[1] is given, as fp16 (y) or
+// as e4m3 codes with scales (codes, scales).
+struct Fp8Params {
+  const uint8_t *x, *sx;        // e4m3 [M, K], e8m0 [M, G]
+  const uint8_t *w[2], *sw[2];  // e4m3 [N, K], e8m0 [N, G]
+  int M, N, K, G;
+  bool gelu;
+  __half *y;                    // fp16 [M, N]
+  uint8_t *codes, *scales;      // e4m3 [M, N], e8m0 [M, ceil(N / 128)]
+};
+
+__host__ __device__ __forceinline__ int fp8_groups_of(int K) { return (K + 127) / 128; }
+
+int launch_fp8_few(const Fp8Params &p, cudaStream_t s);
+
+int launch_quant_fp8(const __half *x, long rows, int K, bool weights, uint8_t *q, uint8_t *scale,
+                     cudaStream_t s);
+int launch_rms_norm(const __half *x, const __half *r, const __half *w, int M, int K, float eps,
+                    __half *h, __half *y, cudaStream_t s);
+int launch_rms_norm_quant(const __half *x, const __half *r, const __half *w, int M, int K,
+                          float eps, int format, int group_size, __half *h, void *q, void *scale,
+                          cudaStream_t s);
+
+}  // namespace w8a8
