@@ -60,7 +60,11 @@ Fp8Params product(const uint8_t *x, const uint8_t *sx, const uint8_t *w, const u
   return p;
 }
 
-int launch_product(const Fp8Params &p, cudaStream_t s) { return launch_fp8_few(p, s); }
+constexpr int kFewRows = 16;
+
+int launch_product(const Fp8Params &p, cudaStream_t s) {
+  return p.M <= kFewRows ? launch_fp8_few(p, s) : launch_fp8_tc(p, s);
+}
 
 // x, r, w, h of the norm; the outputs are the callers' to check
 int check_norm(const w8a8_half *x, const w8a8_half *residual, const w8a8_half *weight, int M, int K,

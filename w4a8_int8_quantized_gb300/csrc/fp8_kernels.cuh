@@ -19,6 +19,7 @@ struct Fp8Params {
 __host__ __device__ __forceinline__ int fp8_groups_of(int K) { return (K + 127) / 128; }
 
 int launch_fp8_few(const Fp8Params &p, cudaStream_t s);
+int launch_fp8_tc(const Fp8Params &p, cudaStream_t s);
 
 int launch_quant_fp8(const __half *x, long rows, int K, bool weights, uint8_t *q, uint8_t *scale,
                      cudaStream_t s);
