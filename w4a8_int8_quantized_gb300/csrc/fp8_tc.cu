@@ -23,7 +23,7 @@
 // stream weights.
 //
 // Warps of a CTA: 0 copies the codes (TMA), 1 issues the MMAs (in the pair's
-// first CTA), 2 and 3 gather the scale bytes into the layout that tcgen05.cp
+// first CTA; the second's passes on that its scales are there), 2 and 3 gather the scale bytes into the layout that tcgen05.cp
 // takes, 4 - 7 are the epilogue.  Persistent, static tiles.
 //
 // Tensor memory: two accumulators of 256 columns and two sets of scales (12
@@ -50,6 +50,7 @@ constexpr int kThreads = 256;
 constexpr int kRows = 128;     // tokens of a CTA's tile
 constexpr int kBlock = 128;    // K of a stage
 constexpr int kScaleBlocks = 4;  // stages of a set of scales
+constexpr int kScaleSets = 4;    // sets in shared memory (two of them in tensor memory)
 
 enum Mode { kLinear = 0, kGatedHalf = 1, kGatedCodes = 2 };
 
@@ -64,8 +65,8 @@ struct Plan {
   static constexpr int SF_BYTES = 512 * (1 + SFB);
   static constexpr int OFF_OUT = S * STAGE;      // 4 warps x 32 rows x 128 bytes
   static constexpr int OFF_SF = OFF_OUT + 4 * 4096;
-  static constexpr int OFF_BAR = OFF_SF + 2 * SF_BYTES;
-  static constexpr int NUM_BARS = 2 * S + 2 + 2 + 2 + 2 + 1;
+  static constexpr int OFF_BAR = OFF_SF + kScaleSets * SF_BYTES;
+  static constexpr int NUM_BARS = 2 * S + 2 * kScaleSets + 2 + 2 + 1;
   static constexpr int SMEM_BYTES = OFF_BAR + NUM_BARS * 8 + 16 + 1024;  // + alignment by hand
   static constexpr bool OVERLAP = BN == 256;
   static constexpr uint32_t SF_COLS = 4 * (1 + SFB);
@@ -82,7 +83,7 @@ struct TcParams {
   const uint8_t *sx, *sw[2];
   int M, N, G, nkb, ntiles, mtiles, ntn;  // N: columns of the output
   int m_first;      // tiles walk the tokens first
-  int words;        // bit 0: sx readable as words, bits 1, 2: sw[0], sw[1]
+  int access[3];    // bytes that a load of sx, sw[0], sw[1] may take at once: 16, 4 or 1
   bool gelu;
   __half *y;        // stored directly (no map) where the rows are not 16-byte multiples
   uint8_t *scales;
@@ -91,44 +92,57 @@ struct TcParams {
   int skip_first_copy;
 };
 
+// MMAs, scale copies and commits are predicated instructions of a converged
+// warp (`on`: the elected lane), so that descriptors stay in uniform registers.
+__device__ __forceinline__ uint32_t elect() {
+  uint32_t on;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(on));
+  return on;
+}
+
 template <int CG>
-__device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+__device__ __forceinline__ void mma_scaled(uint32_t on, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                            uint32_t sfa, uint32_t sfb, uint32_t accum) {
   if (CG == 2)
     asm volatile(
-        "{\n.reg .pred p;\nsetp.ne.b32 p, %6, 0;\n"
-        "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], "
-        "[%5], p;\n}\n" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accum));
+        "{\n.reg .pred p, q;\nsetp.ne.b32 p, %6, 0;\nsetp.ne.b32 q, %7, 0;\n"
+        "@q tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], "
+        "[%5], p;\n}\n" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accum), "r"(on));
   else
     asm volatile(
-        "{\n.reg .pred p;\nsetp.ne.b32 p, %6, 0;\n"
-        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], "
-        "[%5], p;\n}\n" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accum));
+        "{\n.reg .pred p, q;\nsetp.ne.b32 p, %6, 0;\nsetp.ne.b32 q, %7, 0;\n"
+        "@q tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], "
+        "[%5], p;\n}\n" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accum), "r"(on));
 }
 
 // 32 rows x 16 bytes from shared memory to 4 columns, the same in every
 // quarter of the lanes (with a pair: in either CTA, from its own memory)
 template <int CG>
-__device__ __forceinline__ void copy_scales(uint32_t tmem, uint32_t smem) {
+__device__ __forceinline__ void copy_scales(uint32_t on, uint32_t tmem, uint32_t smem) {
   // no swizzle, 8-row groups 128 bytes apart, descriptor version 1
   const uint64_t desc = static_cast<uint64_t>((smem & 0x3ffff) >> 4) | (uint64_t(8) << 16) |
                         (uint64_t(8) << 32) | (uint64_t(1) << 46);
   if (CG == 2)
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc));
+    asm volatile("{\n.reg .pred q;\nsetp.ne.b32 q, %2, 0;\n"
+                 "@q tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n}\n" ::"r"(tmem), "l"(desc), "r"(on));
   else
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc));
+    asm volatile("{\n.reg .pred q;\nsetp.ne.b32 q, %2, 0;\n"
+                 "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n}\n" ::"r"(tmem), "l"(desc), "r"(on));
 }
 
 // All MMAs issued so far arrive on this barrier when they are done, in both
 // CTAs of a pair.
 template <int CG>
-__device__ __forceinline__ void commit(uint32_t bar) {
+__device__ __forceinline__ void commit(uint32_t on, uint32_t bar) {
   if (CG == 2)
     asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], "
-        "%1;" ::"r"(bar), "h"(static_cast<uint16_t>(3)) : "memory");
+        "{\n.reg .pred q;\nsetp.ne.b32 q, %2, 0;\n"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], "
+        "%1;\n}\n" ::"r"(bar), "h"(static_cast<uint16_t>(3)), "r"(on) : "memory");
   else
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+    asm volatile("{\n.reg .pred q;\nsetp.ne.b32 q, %1, 0;\n"
+                 "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar),
+                 "r"(on)
                  : "memory");
 }
 
@@ -141,6 +155,12 @@ __device__ __forceinline__ uint32_t in_leader(uint32_t addr) {
 
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// The same for reads of tensor memory that have completed (tcgen05.wait::ld and
+// the fence before it order them): nothing else to release.
+__device__ __forceinline__ void arrive_read(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 template <int CG>
@@ -214,15 +234,15 @@ __device__ __forceinline__ Tile tile_at(const TcParams &p, int t) {
   return p.m_first ? Tile{t % p.mtiles, t / p.mtiles} : Tile{t / p.ntn, t % p.ntn};
 }
 
-// Four scale bytes (blocks 4 q .. 4 q + 3) of a row; 1.0 for what does not exist.
-__device__ __forceinline__ uint32_t scale_word(const uint8_t *s, bool as_word, long row, long rows, int G,
-                                               int q) {
-  if (row >= rows) return 0x7f7f7f7fu;
-  const uint8_t *at = s + row * G + 4 * q;
-  if (as_word) return *reinterpret_cast<const uint32_t *>(at);  // G % 4 == 0
+// The word at `at`; of one that is only partly within [first, end), the bytes
+// that are, and 1.0 for the others.
+__device__ __forceinline__ uint32_t word_within(uintptr_t at, uintptr_t first, uintptr_t end) {
+  if (at >= first && at + 4 <= end) return *reinterpret_cast<const uint32_t *>(at);
   uint32_t w = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w |= (4 * q + i < G ? static_cast<uint32_t>(at[i]) : 0x7fu) << (8 * i);
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i)
+    w |= (at + i >= first && at + i < end ? static_cast<uint32_t>(*reinterpret_cast<const uint8_t *>(at + i)) : 0x7fu)
+         << (8 * i);
   return w;
 }
 
@@ -273,22 +293,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto full = [&](int s) { return bar0 + 8u * s; };
   auto empty = [&](int s) { return bar0 + 8u * (S + s); };
   auto sf_full = [&](int i) { return bar0 + 8u * (2 * S + i); };
-  auto sf_empty = [&](int i) { return bar0 + 8u * (2 * S + 2 + i); };
-  auto acc_full = [&](int r) { return bar0 + 8u * (2 * S + 4 + r); };
-  auto acc_free = [&](int r) { return bar0 + 8u * (2 * S + 6 + r); };
-  const uint32_t drain = bar0 + 8u * (2 * S + 8);
+  auto sf_empty = [&](int i) { return bar0 + 8u * (2 * S + kScaleSets + i); };
+  auto acc_full = [&](int r) { return bar0 + 8u * (2 * (S + kScaleSets) + r); };
+  auto acc_free = [&](int r) { return bar0 + 8u * (2 * (S + kScaleSets) + 2 + r); };
+  const uint32_t drain = bar0 + 8u * (2 * (S + kScaleSets) + 4);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + PL::OFF_BAR + PL::NUM_BARS * 8);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   const Waits wait{abort_flag, p.err, p.wait_limit};
+  auto all_wait = [&](uint32_t bar, uint32_t parity, unsigned code) {
+    return __all_sync(0xffffffffu, wait(bar, parity, code)) != 0;
+  };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(full(s), 1);
       mbar_init(empty(s), 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(sf_full(i), 2 * CG);   // the two scale warps of each CTA
+    for (int i = 0; i < kScaleSets; ++i) {
+      mbar_init(sf_full(i), CG == 2 && rank == 0 ? 3 : 2);  // the scale warps; in the pair's first CTA, the second's sets too
       mbar_init(sf_empty(i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(acc_full(i), 1);
       mbar_init(acc_free(i), 4 * CG);  // the epilogue warps of each CTA
     }
@@ -370,42 +395,48 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------- MMAs ----
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
+      const uint32_t on = elect();
       constexpr uint32_t idesc = (1u << 23) | (static_cast<uint32_t>(BN >> 3) << 17) |
                                  (static_cast<uint32_t>(kRows * CG >> 4) << 24);
+      const uint64_t desc0 = sw128_desc(base);
       int s = 0, sets = 0, done = 0;
       uint32_t ph = 0;
       for (int t = first; t < p.ntiles && ok; t += step, ++done) {
         const uint32_t r = done & 1;
         if (PL::OVERLAP) {
-          if (done > 0) ok = wait(acc_free(0), (done - 1) & 1u, kDevErrTmemEmpty);
+          if (done > 0) ok = all_wait(acc_free(0), (done - 1) & 1u, kDevErrTmemEmpty);
         } else {
-          ok = wait(acc_free(r), ((done >> 1) & 1u) ^ 1u, kDevErrTmemEmpty);
+          ok = all_wait(acc_free(r), ((done >> 1) & 1u) ^ 1u, kDevErrTmemEmpty);
         }
         if (!ok) break;
         tc_fence_after();
         const uint32_t d = tmem + (r ? PL::ACC1 : 0);
         uint32_t sfa = 0;
         for (int kb = 0; kb < nkb; ++kb) {
-          const int id = kb % kScaleBlocks, set = sets & 1;
+          const int id = kb % kScaleBlocks, set = sets % kScaleSets;
           if (id == 0) {
-            if (!(ok = wait(sf_full(set), (sets >> 1) & 1u, kDevErrFullBarrier))) break;
-            sfa = tmem + PL::SF0 + set * PL::SF_COLS;
+            // the tensor memory of the set before last is written again
+            if (sets >= 2 && !(ok = all_wait(sf_empty((sets - 2) % kScaleSets),
+                                             ((sets - 2) / kScaleSets) & 1u, kDevErrEmptyBarrier)))
+              break;
+            if (!(ok = all_wait(sf_full(set), (sets / kScaleSets) & 1u, kDevErrFullBarrier))) break;
+            sfa = tmem + PL::SF0 + (sets & 1) * PL::SF_COLS;
             const uint32_t from = base + PL::OFF_SF + set * PL::SF_BYTES;
 #pragma unroll
-            for (int i = 0; i < 1 + PL::SFB; ++i) copy_scales<CG>(sfa + 4 * i, from + 512 * i);
+            for (int i = 0; i < 1 + PL::SFB; ++i) copy_scales<CG>(on, sfa + 4 * i, from + 512 * i);
           }
-          if (!(ok = wait(full(s), ph, kDevErrFullBarrier))) break;
+          if (!(ok = all_wait(full(s), ph, kDevErrFullBarrier))) break;
           tc_fence_after();
-          const uint32_t a = base + s * PL::STAGE, b = a + PL::A_BYTES;
+          const uint64_t a = desc0 + s * (PL::STAGE >> 4), b = a + (PL::A_BYTES >> 4);
           const uint32_t with_id = idesc | (static_cast<uint32_t>(id) << 29) | (static_cast<uint32_t>(id) << 4);
 #pragma unroll
           for (int k = 0; k < kBlock / 32; ++k)
-            mma_scaled<CG>(d, sw128_desc(a + k * 32), sw128_desc(b + k * 32), with_id, sfa, sfa + 4,
+            mma_scaled<CG>(on, d, a + k * 2, b + k * 2, with_id, sfa, sfa + 4,
                            kb > 0 || k > 0);
-          commit<CG>(empty(s));
+          commit<CG>(on, empty(s));
           if (id == kScaleBlocks - 1 || kb == nkb - 1) {
-            commit<CG>(sf_empty(set));
+            commit<CG>(on, sf_empty(set));
             ++sets;
           }
           if (++s == S) {
@@ -414,61 +445,119 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (!ok) break;
-        commit<CG>(acc_full(r));
+        commit<CG>(on, acc_full(r));
       }
       // every MMA has landed before tensor memory is freed
-      commit<CG>(drain);
+      commit<CG>(on, drain);
       wait_bar_teardown(drain, 0);
+      __syncwarp();
+    } else {
+      // The second CTA passes on that its scales are there.  Not the scale
+      // warps themselves: a release to the cluster waits for all that its
+      // thread has requested, and theirs have loads under way (the MMAs waited
+      // for scales a third of the time).
+      int sets = 0;
+      for (int t = first; t < p.ntiles && ok; t += step)
+        for (int q = 0; q < nsets; ++q, ++sets) {
+          const int set = sets % kScaleSets;
+          if (!(ok = all_wait(sf_full(set), (sets / kScaleSets) & 1u, kDevErrFullBarrier))) break;
+          if (lane == 0) arrive_cluster(in_leader(sf_full(set)));
+          __syncwarp();
+        }
     }
   } else if (warp < 4) {
     // ------------------------------------------------------------ scales ----
     // Set of 128 rows x 4 blocks: row r's word at (r % 32) 16 + (r / 32) 4, so
     // lane l gathers rows l, l + 32, l + 64, l + 96.  Warp 2 takes the tokens'
     // set and the second set of weights, warp 3 the first one.
-    auto gather = [&](const uint8_t *s, bool as_word, long row, long rows, int q) {
-      uint4 w;
-      w.x = scale_word(s, as_word, row, rows, p.G, q);
-      w.y = scale_word(s, as_word, row + 32, rows, p.G, q);
-      w.z = scale_word(s, as_word, row + 64, rows, p.G, q);
-      w.w = scale_word(s, as_word, row + 96, rows, p.G, q);
-      return w;
-    };
-    int sets = 0;
-    for (int t = first; t < p.ntiles && ok; t += step) {
-      const Tile tl = tile_at(p, t);
-      const long row = static_cast<long>(tl.m) * (kRows * CG) + rank * kRows + lane;
-      const long col = static_cast<long>(tl.n) * COLS + lane;
-      for (int q = 0; q < nsets; ++q, ++sets) {
-        uint4 v0, v1;
-        if (warp == 2) {
-          v0 = gather(p.sx, p.words & 1, row, p.M, q);
-          if (PL::SFB == 2)
-            v1 = MODE == kLinear ? gather(p.sw[0], p.words & 2, col + 128, p.N, q)
-                                 : gather(p.sw[1], p.words & 4, col, p.N, q);
-        } else {
-          v0 = gather(p.sw[0], p.words & 2, col, p.N, q);
-        }
-        const int set = sets & 1;
-        if (!__all_sync(0xffffffffu, wait(sf_empty(set), ((sets >> 1) & 1u) ^ 1u, kDevErrEmptyBarrier))) {
-          ok = false;
-          break;
-        }
-        uint8_t *at = sm + PL::OFF_SF + set * PL::SF_BYTES + lane * 16;
-        if (warp == 2) {
-          *reinterpret_cast<uint4 *>(at) = v0;
-          if (PL::SFB == 2) *reinterpret_cast<uint4 *>(at + 1024) = v1;
-        } else {
-          *reinterpret_cast<uint4 *>(at + 512) = v0;
-        }
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) {
-          if (CG == 2)
-            arrive_cluster(in_leader(sf_full(set)));
-          else
-            mbar_arrive(sf_full(set));
+    //
+    // A load queues behind the stages that this SM has requested, up to 192 KB,
+    // and touches 32 lines, of which few fit beside the stages: so up to four
+    // sets of a tile are requested at once (a line is fetched once for them),
+    // a batch ahead.  What does not exist is 1.0; behind a row's last block
+    // comes the next row's, which no MMA uses.
+    constexpr int BATCH = 4, PARTS = PL::SFB;
+    const bool two = warp == 2 && PARTS == 2;
+    const uint8_t *const from[2] = {warp == 2 ? p.sx : p.sw[0], MODE == kLinear ? p.sw[0] : p.sw[1]};
+    const int rows[2] = {warp == 2 ? p.M : p.N, p.N};
+    const int access[2] = {warp == 2 ? p.access[0] : p.access[1], MODE == kLinear ? p.access[1] : p.access[2]};
+    typedef uint32_t Batch[PARTS][4][BATCH];
+    int nt = first, nq = 0;  // the next batch to request
+    auto request = [&](Batch &w) {
+      if (nt >= p.ntiles) return;
+      const Tile tl = tile_at(p, nt);
+      const int col = tl.n * COLS, row = tl.m * (kRows * CG) + static_cast<int>(rank) * kRows;
+      const int r0[2] = {lane + (warp == 2 ? row : col), lane + (MODE == kLinear ? col + 128 : col)};
+#pragma unroll
+      for (int e = 0; e < PARTS; ++e) {
+        if (e == 1 && !two) continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = r0[e] + 32 * i;
+          const uint8_t *at = from[e] + static_cast<long>(r) * p.G + 4 * nq;
+          if (r >= rows[e]) {
+#pragma unroll
+            for (int j = 0; j < BATCH; ++j) w[e][i][j] = 0x7f7f7f7fu;
+          } else if (access[e] == 16) {  // then the sets of a tile are a multiple of BATCH
+            const uint4 v = *reinterpret_cast<const uint4 *>(at);
+            w[e][i][0] = v.x;
+            w[e][i][1] = v.y;
+            w[e][i][2] = v.z;
+            w[e][i][3] = v.w;
+          } else if (access[e] == 4) {
+#pragma unroll
+            for (int j = 0; j < BATCH; ++j)
+              if (nq + j < nsets) w[e][i][j] = *reinterpret_cast<const uint32_t *>(at + 4 * j);
+          } else {
+            // any address: the words around it, shifted
+            const uintptr_t lo = reinterpret_cast<uintptr_t>(from[e]), end = lo + static_cast<long>(rows[e]) * p.G;
+            const uintptr_t word = reinterpret_cast<uintptr_t>(at) & ~static_cast<uintptr_t>(3);
+            const uint32_t shift = (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(at)) & 3u) * 8u;
+            uint32_t v[BATCH + 1];
+#pragma unroll
+            for (int j = 0; j <= BATCH; ++j) v[j] = word_within(word + 4 * j, lo, end);
+#pragma unroll
+            for (int j = 0; j < BATCH; ++j) w[e][i][j] = __funnelshift_r(v[j], v[j + 1], shift);
+          }
         }
       }
+      if ((nq += BATCH) >= nsets) {
+        nq = 0;
+        nt += step;
+      }
+    };
+    int sets = 0;
+    auto hand_over = [&](const Batch &w, int count) {
+#pragma unroll
+      for (int j = 0; j < BATCH; ++j) {
+        if (j >= count || !ok) break;
+        const int set = sets % kScaleSets;
+        if (!(ok = all_wait(sf_empty(set), ((sets / kScaleSets) & 1u) ^ 1u, kDevErrEmptyBarrier))) break;
+        uint8_t *to = sm + PL::OFF_SF + set * PL::SF_BYTES + lane * 16;
+        *reinterpret_cast<uint4 *>(to + (warp == 2 ? 0 : 512)) = make_uint4(w[0][0][j], w[0][1][j], w[0][2][j], w[0][3][j]);
+        if (two)
+          *reinterpret_cast<uint4 *>(to + 1024) =
+              make_uint4(w[PARTS - 1][0][j], w[PARTS - 1][1][j], w[PARTS - 1][2][j], w[PARTS - 1][3][j]);
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sf_full(set));
+        ++sets;
+      }
+    };
+    Batch w0, w1;
+    request(w0);
+    for (int t = first, q = 0; t < p.ntiles && ok;) {
+      auto turn = [&](Batch &now, Batch &next) {
+        request(next);
+        hand_over(now, min(BATCH, nsets - q));
+        if ((q += BATCH) >= nsets) {
+          q = 0;
+          t += step;
+        }
+      };
+      turn(w0, w1);
+      if (t >= p.ntiles || !ok) break;
+      turn(w1, w0);
     }
   } else {
     // ---------------------------------------------------------- epilogue ----
@@ -495,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
           const uint32_t bar = acc_free(PL::OVERLAP ? 0 : r);
           if (CG == 2)
-            arrive_cluster(in_leader(bar));
+            arrive_read(in_leader(bar));
           else
             mbar_arrive(bar);
         }
@@ -685,8 +774,13 @@ int launch_t(const Fp8Params &f, cudaStream_t s) {
   p.ntiles = static_cast<int>(mt * nt);
   // the operand that is walked first is read again and again: the smaller one
   p.m_first = f.M <= f.N;
-  auto as_words = [&](const uint8_t *at) { return f.G % 4 == 0 && (reinterpret_cast<uintptr_t>(at) & 3u) == 0; };
-  p.words = (as_words(f.sx) ? 1 : 0) | (as_words(f.sw[0]) ? 2 : 0) | (f.sw[1] != nullptr && as_words(f.sw[1]) ? 4 : 0);
+  auto access = [&](const uint8_t *at) {
+    const uintptr_t low = reinterpret_cast<uintptr_t>(at) | static_cast<uintptr_t>(f.G);
+    return low % 16 == 0 ? 16 : low % 4 == 0 ? 4 : 1;
+  };
+  p.access[0] = access(f.sx);
+  p.access[1] = access(f.sw[0]);
+  p.access[2] = access(f.sw[1]);
   p.gelu = f.gelu;
   p.scales = f.scales;
   if ((p.err = device_error_word()) == nullptr) return W8A8_ERR_CUDA;
