@@ -60,10 +60,10 @@ Fp8Params product(const uint8_t *x, const uint8_t *sx, const uint8_t *w, const u
   return p;
 }
 
-constexpr int kFewRows = 16;
-
 int launch_product(const Fp8Params &p, cudaStream_t s) {
-  return p.M <= kFewRows ? launch_fp8_few(p, s) : launch_fp8_tc(p, s);
+  // 2048 rows and more are ten times what the small tiles are for
+  const bool large = p.M > 2048 || (p.M > 128 && estimate_fp8_tc(p) < estimate_fp8_mid(p));
+  return large ? launch_fp8_tc(p, s) : launch_fp8_mid(p, s);
 }
 
 // x, r, w, h of the norm; the outputs are the callers' to check

@@ -18,8 +18,12 @@ struct Fp8Params {
 
 __host__ __device__ __forceinline__ int fp8_groups_of(int K) { return (K + 127) / 128; }
 
-int launch_fp8_few(const Fp8Params &p, cudaStream_t s);
+// Tiles of up to 128 x 128, K divided (fp8_mid.cu), and pairs of CTAs on tiles of
+// 256 x 256 (fp8_tc.cu); and about how long they take, in microseconds.
+int launch_fp8_mid(const Fp8Params &p, cudaStream_t s);
 int launch_fp8_tc(const Fp8Params &p, cudaStream_t s);
+float estimate_fp8_mid(const Fp8Params &p);
+float estimate_fp8_tc(const Fp8Params &p);
 
 int launch_quant_fp8(const __half *x, long rows, int K, bool weights, uint8_t *q, uint8_t *scale,
                      cudaStream_t s);

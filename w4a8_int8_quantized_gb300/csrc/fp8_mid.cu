@@ -1,0 +1,500 @@
+// Products of 8-bit float rows that are bound by the weights' bytes or by few
+// tiles: up to a few hundred rows.  The arithmetic of fp8_tc.cu (block-scaled
+// tcgen05 MMAs, sums in fp32 from the first group to the last), in tiles of up
+// to 128 tokens x 128 columns, one tile a CTA, two CTAs an SM, and K divided
+// among the CTAs of a cluster where the tiles alone are too few.
+//
+// The stages (a ring in half an SM's shared memory) hold only the rows that
+// there are: with 40 tokens a stage is 5 KB of tokens and up to 16 KB of
+// weights.  The MMA takes 128 rows all the same; what the others hold reaches
+// only lanes that nobody reads.
+//
+// The weights do not come from the previous kernel: the first stages of them
+// are requested before it has finished, into the half of the SM that its CTAs
+// leave.
+//
+// Epilogue: a CTA writes its sums as fp32 over its stages; then all threads of
+// the cluster add the parts in ascending order of K, apply the gate and write
+// 8 columns each: 16 lanes have the 128 columns of a group of codes.
+#include <algorithm>
+#include <mutex>
+
+#include "fp8.cuh"
+#include "fp8_kernels.cuh"
+#include "fp8_mma.cuh"
+
+namespace w8a8 {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxStages = 12;
+constexpr int kScaleSets = 8;       // sets of scales in shared memory, and in tensor memory
+constexpr int kSetBytes = 2 * 512;  // 128 tokens, 128 columns
+constexpr uint32_t kTmemCols = 256, kScaleCol = 128;  // sums, then sets of 8 columns
+// half of an SM's 228 KB, less 1 KB that the system keeps for each CTA
+constexpr int kSmemBytes = 228 * 1024 / 2 - 1024;
+constexpr int kBars = 2 * (kMaxStages + kScaleSets) + 2;
+constexpr int kTail = kScaleSets * kSetBytes + kBars * 8 + 16;
+constexpr int kRegion = (kSmemBytes - 1024 - kTail) / 1024 * 1024;  // stages; 1 KB for alignment by hand
+
+enum Mode { kLinear = 0, kGatedHalf = 1, kGatedCodes = 2 };
+
+struct MidParams {
+  const uint8_t *sx, *sw[2];
+  int M, N, G;
+  int mr, bn;        // rows and columns (of both matrices, if gated) of a tile
+  int split, nx;     // CTAs of a cluster: parts of K, tiles of a group of codes
+  int stages;
+  int access[3];     // see scale_access()
+  bool gelu;
+  __half *y;
+  uint8_t *codes, *scales;
+  unsigned int *err;
+  long long wait_limit;
+  int skip_first_copy;
+};
+
+__device__ __forceinline__ float4 load_cluster(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr));
+  return v;
+}
+
+__device__ __forceinline__ void take(float (&to)[8], const float4 &lo, const float4 &hi) {
+  to[0] += lo.x;
+  to[1] += lo.y;
+  to[2] += lo.z;
+  to[3] += lo.w;
+  to[4] += hi.x;
+  to[5] += hi.y;
+  to[6] += hi.z;
+  to[7] += hi.w;
+}
+
+template <int MODE>
+__global__ void __launch_bounds__(kThreads, 2)
+    fp8_mid_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w0,
+                   const __grid_constant__ CUtensorMap map_w1, const MidParams p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+  uint8_t *sm = smem_raw + (base - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int S = p.stages, a_bytes = p.mr * kBlock, stage = a_bytes + p.bn * kBlock;
+  const int cols = MODE == kLinear ? p.bn : p.bn / 2;
+  const int team = p.split * p.nx, rank = static_cast<int>(blockIdx.x) % team;
+  const int part = rank / p.nx;
+  const long tile_n = static_cast<long>(blockIdx.x) / team * p.nx + rank % p.nx;
+  const int col0 = static_cast<int>(tile_n * cols), row0 = static_cast<int>(blockIdx.y) * p.mr;
+  const int all_sets = (p.G + kScaleBlocks - 1) / kScaleBlocks;
+  const int set0 = static_cast<int>(static_cast<long>(all_sets) * part / p.split);
+  const int nsets = static_cast<int>(static_cast<long>(all_sets) * (part + 1) / p.split) - set0;
+  const int kb0 = set0 * kScaleBlocks, nkb = min(nsets * kScaleBlocks, p.G - kb0);
+
+  const uint32_t sf = base + kRegion, bar0 = sf + kScaleSets * kSetBytes;
+  auto full = [&](int s) { return bar0 + 8u * s; };
+  auto empty = [&](int s) { return bar0 + 8u * (kMaxStages + s); };
+  auto sf_full = [&](int i) { return bar0 + 8u * (2 * kMaxStages + i); };
+  auto sf_empty = [&](int i) { return bar0 + 8u * (2 * kMaxStages + kScaleSets + i); };
+  const uint32_t acc_full = bar0 + 8u * (2 * (kMaxStages + kScaleSets)), drain = acc_full + 8u;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + kRegion + kScaleSets * kSetBytes + kBars * 8);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  const Waits wait{abort_flag, p.err, p.wait_limit};
+
+  if (threadIdx.x == 0) {
+    prefetch_map(&map_w0);
+    if (MODE != kLinear) prefetch_map(&map_w1);
+    prefetch_map(&map_x);
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    for (int i = 0; i < kScaleSets; ++i) {
+      mbar_init(sf_full(i), 2);
+      mbar_init(sf_empty(i), 1);
+    }
+    mbar_init(acc_full, 1);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"(kTmemCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  // Not before the tensor memory is ours: a CTA of the next kernel that got it
+  // first would wait for this one.
+  asm volatile("griddepcontrol.launch_dependents;");
+  bool ok = true;
+
+  if (warp == 0) {
+    // -------------------------------------------------------- code copies --
+    if (lane == 0) {
+      auto weights = [&](int s, int kb) {
+        const uint32_t b = base + s * stage + a_bytes;
+        mbar_arrive_expect_tx(full(s), stage);
+        tma_load_2d(b, &map_w0, full(s), (kb0 + kb) * kBlock, col0);
+        if (MODE != kLinear) tma_load_2d(b + cols * kBlock, &map_w1, full(s), (kb0 + kb) * kBlock, col0);
+      };
+      auto tokens = [&](int s, int kb) { tma_load_2d(base + s * stage, &map_x, full(s), (kb0 + kb) * kBlock, row0); };
+      // (test only) the first stage left unissued: the MMAs' wait for it gives up
+      const int from = p.skip_first_copy ? 1 : 0, ahead = min(S, nkb);
+      for (int kb = from; kb < ahead; ++kb) weights(kb, kb);
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      for (int kb = from; kb < ahead; ++kb) tokens(kb, kb);
+      int s = ahead == S ? 0 : ahead, kb = ahead;
+      uint32_t ph = 0;  // of the stage's last use
+      for (; kb < nkb; ++kb) {
+        if (!(ok = wait(empty(s), ph, kDevErrEmptyBarrier))) break;
+        weights(s, kb);
+        tokens(s, kb);
+        if (++s == S) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+      // every copy has landed before the CTA can leave
+      for (int i = max(from, kb - S); i < kb; ++i) wait_bar_teardown(full(i % S), (i / S) & 1);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------- MMAs ----
+    const uint32_t on = elect();
+    const uint32_t idesc = (1u << 23) | (static_cast<uint32_t>(p.bn >> 3) << 17) | (8u << 24);
+    const uint64_t desc0 = sw128_desc(base);
+    int s = 0;
+    uint32_t ph = 0, sfa = 0;
+    // the barriers of a step are looked at under the step before it
+    bool staged = false, scaled = false;
+    for (int kb = 0; kb < nkb; ++kb) {
+      const int id = kb % kScaleBlocks, at = kb / kScaleBlocks, set = at % kScaleSets;
+      if (id == 0) {
+        // a set that is there has its place in tensor memory free too: the
+        // places are as many, and its own in shared memory was
+        if (!__all_sync(0xffffffffu, scaled) &&
+            !(ok = wait.warp(sf_full(set), (at / kScaleSets) & 1u, kDevErrFullBarrier)))
+          break;
+        sfa = tmem + kScaleCol + set * 8;
+        copy_scales<1>(on, sfa, sf + set * kSetBytes);
+        copy_scales<1>(on, sfa + 4, sf + set * kSetBytes + 512);
+      }
+      if (!__all_sync(0xffffffffu, staged) && !(ok = wait.warp(full(s), ph, kDevErrFullBarrier))) break;
+      tc_fence_after();
+      const uint64_t a = desc0 + ((s * stage) >> 4), b = a + (a_bytes >> 4);
+      const uint32_t with_id = idesc | (static_cast<uint32_t>(id) << 29) | (static_cast<uint32_t>(id) << 4);
+      const uint32_t freed = empty(s);
+      if (++s == S) {
+        s = 0;
+        ph ^= 1u;
+      }
+#ifndef NOPEEK
+      staged = is_over(full(s), ph);
+      if (id == kScaleBlocks - 1) scaled = is_over(sf_full((at + 1) % kScaleSets), ((at + 1) / kScaleSets) & 1u);
+#endif
+#pragma unroll
+      for (int k = 0; k < kBlock / 32; ++k)
+        mma_scaled<1>(on, tmem, a + k * 2, b + k * 2, with_id, sfa, sfa + 4, kb > 0 || k > 0);
+      commit<1>(on, freed);
+      if (id == kScaleBlocks - 1) commit<1>(on, sf_empty(set));
+    }
+    if (ok) commit<1>(on, acc_full);
+    // every MMA has landed before tensor memory is freed
+    commit<1>(on, drain);
+    wait_bar_teardown(drain, 0);
+    __syncwarp();
+  } else if (warp < 4) {
+    // ------------------------------------------------------------ scales ----
+    // Set of 128 rows x 4 blocks: row r's word at (r % 32) 16 + (r / 32) 4.  Warp 2
+    // gathers the tokens' rows, warp 3 the weights', of which the gate's come
+    // first.
+    const bool mine = warp == 2;
+    if (mine) asm volatile("griddepcontrol.wait;" ::: "memory");
+    const uint8_t *at[4], *first[4];
+    int access[4];
+    long bytes[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = lane + 32 * i, which = mine ? 0 : MODE != kLinear && r >= cols ? 2 : 1;
+      const int row = mine ? row0 + r : col0 + (which == 2 ? r - cols : r);
+      const bool there = row < (mine ? p.M : p.N) && r < (mine ? p.mr : p.bn);
+      first[i] = mine ? p.sx : which == 2 ? p.sw[1] : p.sw[0];
+      access[i] = mine ? p.access[0] : which == 2 ? p.access[2] : p.access[1];
+      if (set0 % 4 != 0 && access[i] == 16) access[i] = 4;
+      bytes[i] = static_cast<long>(mine ? p.M : p.N) * p.G;
+      at[i] = there ? first[i] + static_cast<long>(row) * p.G + kb0 : nullptr;
+    }
+    const int left = all_sets - set0;
+    auto request = [&](uint32_t (&w)[4][kScaleBatch], int q) {
+      if (q >= nsets) return;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        fetch_scales(w[i], at[i] == nullptr ? nullptr : at[i] + 4 * q, left - q, access[i], first[i], bytes[i]);
+    };
+    auto hand_over = [&](const uint32_t (&w)[4][kScaleBatch], int q) {
+#pragma unroll
+      for (int j = 0; j < kScaleBatch; ++j) {
+        if (q + j >= nsets || !ok) break;
+        const int set = (q + j) % kScaleSets;
+        if (!(ok = wait.warp(sf_empty(set), (((q + j) / kScaleSets) & 1u) ^ 1u, kDevErrEmptyBarrier))) break;
+        *reinterpret_cast<uint4 *>(sm + kRegion + set * kSetBytes + (mine ? 0 : 512) + lane * 16) =
+            make_uint4(w[0][j], w[1][j], w[2][j], w[3][j]);
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sf_full(set));
+      }
+    };
+    uint32_t w0[4][kScaleBatch], w1[4][kScaleBatch];
+    request(w0, 0);
+    for (int q = 0; q < nsets && ok; q += 2 * kScaleBatch) {
+      request(w1, q + kScaleBatch);
+      hand_over(w0, q);
+      request(w0, q + 2 * kScaleBatch);
+      hand_over(w1, q + kScaleBatch);
+    }
+  } else if ((warp & 3) * 32 < p.mr) {
+    // ----------------------------------------- sums to shared memory --------
+    // Rows of bn + 4 floats: eight rows' 16-byte pieces fill all banks.
+    if (wait.warp(acc_full, 0, kDevErrAccumBarrier)) {
+      tc_fence_after();
+      const int row = (warp & 3) * 32 + lane;
+      const uint32_t from = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+      float *to = reinterpret_cast<float *>(sm) + row * (p.bn + 4);
+      for (int c = 0; c < p.bn; c += 32) {
+        uint32_t v[32];
+        tmem_ld32(from + c, v);  // behind bn: columns of this CTA's own tensor memory, not kept
+        tmem_wait_ld32(v);
+        if (row < p.mr) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (c + 4 * e < p.bn)
+              *reinterpret_cast<uint4 *>(to + c + 4 * e) = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+        }
+        __syncwarp();
+      }
+      tc_fence_before();
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  if (team > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  tc_fence_after();
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  // ------------------------------------------------------------- outputs ----
+  {
+    const int rows = min(p.mr, p.M - row0), per_tile = cols / 8, per_row = p.nx * per_tile;
+    const long group0 = static_cast<long>(blockIdx.x) / team * p.nx * cols;  // first column of the cluster
+    const int items = rows * per_row, stride = team * kThreads, pitch = (p.bn + 4) * 4;
+    int i = rank * kThreads + static_cast<int>(threadIdx.x);
+    int row = i / per_row, ch = i - row * per_row;
+    const int rows_on = stride / per_row, ch_on = stride - rows_on * per_row;
+    // whole warps: the lanes of a group of codes exchange their maxima
+    for (; (i & ~31) < items; i += stride, row += rows_on, ch += ch_on) {
+      if (ch >= per_row) {
+        ch -= per_row;
+        ++row;
+      }
+      const bool in = i < items;
+      const int x = ch >= per_tile ? 1 : 0;
+      const uint32_t at = (in ? row : 0) * pitch + (ch - x * per_tile) * 32;
+      float v[8], u[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = u[e] = 0.f;
+      if (team == 1) {
+        take(v, reinterpret_cast<const float4 *>(sm + at)[0], reinterpret_cast<const float4 *>(sm + at)[1]);
+        if (MODE != kLinear)
+          take(u, reinterpret_cast<const float4 *>(sm + at + cols * 4)[0], reinterpret_cast<const float4 *>(sm + at + cols * 4)[1]);
+      } else {
+        // parts of K in ascending order, two of them on their way at a time
+        for (int k = 0; k < p.split; k += 2) {
+          float4 w[2][4];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            if (k + e >= p.split) break;
+            uint32_t a;
+            asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(base + at), "r"((k + e) * p.nx + x));
+            w[e][0] = load_cluster(a);
+            w[e][1] = load_cluster(a + 16);
+            if (MODE != kLinear) {
+              w[e][2] = load_cluster(a + cols * 4);
+              w[e][3] = load_cluster(a + cols * 4 + 16);
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            if (k + e >= p.split) break;
+            take(v, w[e][0], w[e][1]);
+            if (MODE != kLinear) take(u, w[e][2], w[e][3]);
+          }
+        }
+      }
+      if (MODE != kLinear) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = p.gelu ? gated<true>(v[e], u[e]) : gated<false>(v[e], u[e]);
+      }
+      const long m = row0 + row, n = group0 + ch * 8;
+      if (MODE == kGatedCodes) {
+        float top = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[e]));
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const uint32_t byte = fp8_scale_byte(top);
+        const float s = fp8_scale_inverse(byte);
+        if (in && n < p.N) {  // N is a multiple of 16
+          *reinterpret_cast<uint2 *>(p.codes + m * p.N + n) =
+              make_uint2(fp8_pack4(v[0] * s, v[1] * s, v[2] * s, v[3] * s), fp8_pack4(v[4] * s, v[5] * s, v[6] * s, v[7] * s));
+          if (ch == 0) p.scales[m * ((p.N + 127) >> 7) + (n >> 7)] = static_cast<uint8_t>(byte);
+        }
+      } else if (in && n < p.N) {
+        __half *to = p.y + m * p.N + n;
+        if ((p.N & 7) == 0) {
+          *reinterpret_cast<uint4 *>(to) = make_uint4(half2_bits(v[0], v[1]), half2_bits(v[2], v[3]),
+                                                      half2_bits(v[4], v[5]), half2_bits(v[6], v[7]));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (n + e < p.N) to[e] = __float2half_rn(v[e]);
+        }
+      }
+    }
+  }
+  if (team > 1) {  // the others may still read this CTA's sums; nothing is handed over
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  }
+}
+
+// ------------------------------------------------------------ host side --
+
+struct Plan {
+  int mr, bn, split, nx;
+  float us;
+};
+
+// Microseconds of a call by a model fitted to 2850 timings (1 to 1000 rows, twelve
+// shapes of weights, all tiles and parts): its choice is on average 1 % and at most
+// 18 % slower than the best one.  A CTA takes 83 GB/s, or 0.23 us a K block (one
+// thread issues its MMAs; a little more where two CTAs share an SM); HBM gives
+// 6770 GB/s to all; more than two CTAs an SM wait for a place; the epilogue and the
+// joining of parts go with the tile's size.
+float estimate(const Fp8Params &f, int mr, int bn, int split, int nx) {
+  const int sets = (f.G + kScaleBlocks - 1) / kScaleBlocks;
+  const int blocks = std::min((sets + split - 1) / split * kScaleBlocks, f.G);
+  const int cols = f.w[1] == nullptr ? bn : bn / 2;
+  const long groups = (static_cast<long>(f.N) + cols * nx - 1) / (cols * nx);
+  const long ctas = groups * nx * ceil_div(f.M, 128) * split;
+  const float waves = static_cast<float>((ctas + 2 * kNumSMsGB300 - 1) / (2 * kNumSMsGB300));
+  const float block = std::max(ctas <= kNumSMsGB300 ? 0.23f : 0.263f, (mr + bn) * (kBlock / 83e3f));
+  const float hbm = static_cast<float>(f.N) * (f.w[1] == nullptr ? 1 : 2) * f.K / 6.77e6f;
+  const float tile = mr * bn / 16384.f;
+  const float join = split * nx == 1 ? 0.f : 0.5f + 3.4f * (split - 1) * tile;
+  return 3.9f + std::max(waves * blocks * block, hbm) + (waves - 1.f) * 3.6f + join + 5.7f * waves * tile;
+}
+
+// The tile and parts of K of the least estimate.
+Plan choose(const Fp8Params &f) {
+  Plan best = {};
+  const int tiles_m = ceil_div(f.M, 128), mr = (ceil_div(f.M, tiles_m) + 7) & ~7;
+  const int sets = (f.G + kScaleBlocks - 1) / kScaleBlocks, nx = f.codes != nullptr ? 2 : 1;
+  for (int bn = nx == 2 ? 128 : f.w[1] == nullptr ? 32 : 48; bn <= 128; bn += 16)
+    for (int split = 1; split * nx <= 8 && split <= sets; split *= 2) {
+      const float t = estimate(f, mr, bn, split, nx);
+      if (best.us == 0.f || t < best.us) best = {mr, bn, split, nx, t};
+    }
+  return best;
+}
+
+template <int MODE>
+int launch_t(const Fp8Params &f, const Plan &plan, cudaStream_t s) {
+  static bool ready[64] = {};
+  static std::mutex mu;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return W8A8_ERR_CUDA;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!ready[dev]) {
+      if (cudaFuncSetAttribute(fp8_mid_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) !=
+          cudaSuccess)
+        return W8A8_ERR_CUDA;
+      ready[dev] = true;
+    }
+  }
+  const int mt = ceil_div(f.M, plan.mr);
+  MidParams p = {};
+  p.sx = f.sx;
+  p.sw[0] = f.sw[0];
+  p.sw[1] = f.sw[1];
+  p.M = f.M;
+  p.N = f.N;
+  p.G = f.G;
+  p.mr = plan.mr;
+  p.bn = plan.bn;
+  p.split = plan.split;
+  p.nx = plan.nx;
+  // the last stage's MMAs read 128 rows from its start
+  const int stage = (p.mr + p.bn) * kBlock, spare = (128 - p.bn - p.mr) * kBlock;
+  const int fit = (kRegion - (spare > 0 ? spare : 0)) / stage;
+  p.stages = fit < kMaxStages ? fit : kMaxStages;
+  p.access[0] = scale_access(f.sx, f.G);
+  p.access[1] = scale_access(f.sw[0], f.G);
+  p.access[2] = scale_access(f.sw[1], f.G);
+  p.gelu = f.gelu;
+  p.y = f.y;
+  p.codes = f.codes;
+  p.scales = f.scales;
+  if ((p.err = device_error_word()) == nullptr) return W8A8_ERR_CUDA;
+  p.wait_limit = role_wait_limit();
+  p.skip_first_copy = skip_first_copy();
+
+  const int cols = MODE == kLinear ? p.bn : p.bn / 2, team = p.split * p.nx;
+  const long groups = (static_cast<long>(f.N) + cols * p.nx - 1) / (cols * p.nx);
+  if (groups * cols * p.nx > 0x7fffffffL || groups * team > 0x7fffffffL) return W8A8_ERR_INVALID_ARG;
+  CUtensorMap mx, mw0, mw1;
+  if (!make_map(&mx, f.x, f.M, f.K, 1, p.mr) || !make_map(&mw0, f.w[0], f.N, f.K, 1, cols)) return W8A8_ERR_CUDA;
+  mw1 = mw0;
+  if (MODE != kLinear && !make_map(&mw1, f.w[1], f.N, f.K, 1, cols)) return W8A8_ERR_CUDA;
+
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(groups * team), static_cast<unsigned>(mt));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = static_cast<unsigned>(team);
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = team > 1 ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, fp8_mid_kernel<MODE>, mx, mw0, mw1, p) != cudaSuccess) {
+    cudaGetLastError();
+    return W8A8_ERR_CUDA;
+  }
+  return launch_status();
+}
+
+}  // namespace
+
+float estimate_fp8_mid(const Fp8Params &f) { return choose(f).us; }
+
+int launch_fp8_mid(const Fp8Params &f, cudaStream_t s) {
+  const Plan plan = choose(f);
+  if (f.w[1] == nullptr) return launch_t<kLinear>(f, plan, s);
+  return f.codes != nullptr ? launch_t<kGatedCodes>(f, plan, s) : launch_t<kGatedHalf>(f, plan, s);
+}
+
+}  // namespace w8a8
