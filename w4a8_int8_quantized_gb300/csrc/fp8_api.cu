@@ -60,10 +60,23 @@ Fp8Params product(const uint8_t *x, const uint8_t *sx, const uint8_t *w, const u
   return p;
 }
 
-int launch_product(const Fp8Params &p, cudaStream_t s) {
-  // 2048 rows and more are ten times what the small tiles are for
-  const bool large = p.M > 2048 || (p.M > 128 && estimate_fp8_tc(p) < estimate_fp8_mid(p));
-  return large ? launch_fp8_tc(p, s) : launch_fp8_mid(p, s);
+// The product of p.x, p.sx, or of fp16 rows x: quantized into the room at p.x, p.sx
+// before it, or, if they are few, by the product itself.
+int launch_product(Fp8Params &p, cudaStream_t s, const __half *x = nullptr) {
+  // the small tiles are for a few hundred rows: 2048 are never theirs
+  bool small = p.M <= 2048;
+  Fp8Plan plan = {};
+  if (small) {
+    plan = plan_fp8_mid(p);
+    small = p.M <= 128 || plan.us <= estimate_fp8_tc(p);
+  }
+  if (x != nullptr) {
+    if (small && fp8_mid_quantizes(p, plan))
+      p.xh = x;
+    else
+      W8A8_TRY(launch_quant_fp8(x, p.M, p.K, false, const_cast<uint8_t *>(p.x), const_cast<uint8_t *>(p.sx), s));
+  }
+  return small ? launch_fp8_mid(p, plan, s) : launch_fp8_tc(p, s);
 }
 
 // x, r, w, h of the norm; the outputs are the callers' to check
@@ -189,10 +202,9 @@ int fp8_linear(const w8a8_half *x, const uint8_t *Wq, const uint8_t *scale_w, in
   W8A8_TRY(check_workspace(workspace, ws_bytes, held_bytes(M, K)));
   W8A8_TRY(check_device());
   uint8_t *xq = static_cast<uint8_t *>(workspace), *sx = xq + code_bytes(M, K);
-  W8A8_TRY(launch_quant_fp8(as_half(x), M, K, false, xq, sx, as_stream(stream)));
   Fp8Params p = product(xq, sx, Wq, scale_w, M, N, K);
   p.y = as_half(y);
-  return launch_product(p, as_stream(stream));
+  return launch_product(p, as_stream(stream), as_half(x));
 }
 
 size_t fp8_feed_forward_workspace_bytes(int M, int K, int F) {
@@ -217,14 +229,13 @@ int fp8_feed_forward(const w8a8_half *x, const uint8_t *Wg, const uint8_t *scale
   const cudaStream_t s = as_stream(stream);
   uint8_t *xq = static_cast<uint8_t *>(workspace), *sx = xq + code_bytes(M, K);
   uint8_t *hq = xq + held_bytes(M, K), *sh = hq + code_bytes(M, F);
-  W8A8_TRY(launch_quant_fp8(as_half(x), M, K, false, xq, sx, s));
   Fp8Params up = product(xq, sx, Wg, scale_g, M, F, K);
   up.w[1] = Wu;
   up.sw[1] = scale_u;
   up.gelu = activation == W8A8_GATE_GELU;
   up.codes = hq;
   up.scales = sh;
-  W8A8_TRY(launch_product(up, s));
+  W8A8_TRY(launch_product(up, s, as_half(x)));
   Fp8Params down = product(hq, sh, Wd, scale_d, M, N, F);
   down.y = as_half(y);
   return launch_product(down, s);

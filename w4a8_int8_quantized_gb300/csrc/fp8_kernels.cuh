@@ -9,6 +9,7 @@ namespace w8a8 {
 // as e4m3 codes with scales (codes, scales).
 struct Fp8Params {
   const uint8_t *x, *sx;        // e4m3 [M, K], e8m0 [M, G]
+  const __half *xh;             // or fp16 [M, K], quantized by the product (fp8_mid_quantizes())
   const uint8_t *w[2], *sw[2];  // e4m3 [N, K], e8m0 [N, G]
   int M, N, K, G;
   bool gelu;
@@ -18,12 +19,20 @@ struct Fp8Params {
 
 __host__ __device__ __forceinline__ int fp8_groups_of(int K) { return (K + 127) / 128; }
 
+// How fp8_mid.cu works on a product: rows and columns of a tile, parts of K, tiles
+// that share a group of codes; and about how long it takes, in microseconds.
+struct Fp8Plan {
+  int mr, bn, split, nx;
+  float us;
+};
+
 // Tiles of up to 128 x 128, K divided (fp8_mid.cu), and pairs of CTAs on tiles of
-// 256 x 256 (fp8_tc.cu); and about how long they take, in microseconds.
-int launch_fp8_mid(const Fp8Params &p, cudaStream_t s);
-int launch_fp8_tc(const Fp8Params &p, cudaStream_t s);
-float estimate_fp8_mid(const Fp8Params &p);
+// 256 x 256 (fp8_tc.cu).
+Fp8Plan plan_fp8_mid(const Fp8Params &p);
+bool fp8_mid_quantizes(const Fp8Params &p, const Fp8Plan &plan);  // a few fp16 rows: xh
+int launch_fp8_mid(const Fp8Params &p, const Fp8Plan &plan, cudaStream_t s);
 float estimate_fp8_tc(const Fp8Params &p);
+int launch_fp8_tc(const Fp8Params &p, cudaStream_t s);
 
 int launch_quant_fp8(const __half *x, long rows, int K, bool weights, uint8_t *q, uint8_t *scale,
                      cudaStream_t s);

@@ -40,11 +40,12 @@ constexpr int kRegion = (kSmemBytes - 1024 - kTail) / 1024 * 1024;  // stages; 1
 enum Mode { kLinear = 0, kGatedHalf = 1, kGatedCodes = 2 };
 
 struct MidParams {
+  const __half *x;   // QUANT: the tokens themselves
   const uint8_t *sx, *sw[2];
-  int M, N, G;
+  int M, N, K, G;
   int mr, bn;        // rows and columns (of both matrices, if gated) of a tile
   int split, nx;     // CTAs of a cluster: parts of K, tiles of a group of codes
-  int stages;
+  int stages, token_bytes;
   int access[3];     // see scale_access()
   bool gelu;
   __half *y;
@@ -73,7 +74,7 @@ __device__ __forceinline__ void take(float (&to)[8], const float4 &lo, const flo
   to[7] += hi.w;
 }
 
-template <int MODE>
+template <int MODE, bool QUANT>
 __global__ void __launch_bounds__(kThreads, 2)
     fp8_mid_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w0,
                    const __grid_constant__ CUtensorMap map_w1, const MidParams p) {
@@ -81,16 +82,18 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
   uint8_t *sm = smem_raw + (base - raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int S = p.stages, a_bytes = p.mr * kBlock, stage = a_bytes + p.bn * kBlock;
+  // QUANT: the tokens of all K blocks first, then the stages, of weights alone
+  const int S = p.stages, a_bytes = p.mr * kBlock, stage = (QUANT ? 0 : a_bytes) + p.bn * kBlock;
   const int cols = MODE == kLinear ? p.bn : p.bn / 2;
   const int team = p.split * p.nx, rank = static_cast<int>(blockIdx.x) % team;
   const int part = rank / p.nx;
   const long tile_n = static_cast<long>(blockIdx.x) / team * p.nx + rank % p.nx;
   const int col0 = static_cast<int>(tile_n * cols), row0 = static_cast<int>(blockIdx.y) * p.mr;
-  const int all_sets = (p.G + kScaleBlocks - 1) / kScaleBlocks;
-  const int set0 = static_cast<int>(static_cast<long>(all_sets) * part / p.split);
-  const int nsets = static_cast<int>(static_cast<long>(all_sets) * (part + 1) / p.split) - set0;
-  const int kb0 = set0 * kScaleBlocks, nkb = min(nsets * kScaleBlocks, p.G - kb0);
+  // K blocks of this part; its sets of scales are those of the whole row
+  const int kb0 = static_cast<int>(static_cast<long>(p.G) * part / p.split);
+  const int nkb = static_cast<int>(static_cast<long>(p.G) * (part + 1) / p.split) - kb0;
+  const int set0 = kb0 / kScaleBlocks, nsets = (kb0 + nkb + kScaleBlocks - 1) / kScaleBlocks - set0;
+  const uint32_t a_base = base, b_base = base + (QUANT ? p.token_bytes : a_bytes);
 
   const uint32_t sf = base + kRegion, bar0 = sf + kScaleSets * kSetBytes;
   auto full = [&](int s) { return bar0 + 8u * s; };
@@ -111,7 +114,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       mbar_init(empty(s), 1);
     }
     for (int i = 0; i < kScaleSets; ++i) {
-      mbar_init(sf_full(i), 2);
+      mbar_init(sf_full(i), QUANT ? 5 : 2);  // the warps that fill it
       mbar_init(sf_empty(i), 1);
     }
     mbar_init(acc_full, 1);
@@ -137,16 +140,18 @@ __global__ void __launch_bounds__(kThreads, 2)
     // -------------------------------------------------------- code copies --
     if (lane == 0) {
       auto weights = [&](int s, int kb) {
-        const uint32_t b = base + s * stage + a_bytes;
+        const uint32_t b = b_base + s * stage;
         mbar_arrive_expect_tx(full(s), stage);
         tma_load_2d(b, &map_w0, full(s), (kb0 + kb) * kBlock, col0);
         if (MODE != kLinear) tma_load_2d(b + cols * kBlock, &map_w1, full(s), (kb0 + kb) * kBlock, col0);
       };
-      auto tokens = [&](int s, int kb) { tma_load_2d(base + s * stage, &map_x, full(s), (kb0 + kb) * kBlock, row0); };
+      auto tokens = [&](int s, int kb) {
+        if (!QUANT) tma_load_2d(a_base + s * stage, &map_x, full(s), (kb0 + kb) * kBlock, row0);
+      };
       // (test only) the first stage left unissued: the MMAs' wait for it gives up
       const int from = p.skip_first_copy ? 1 : 0, ahead = min(S, nkb);
       for (int kb = from; kb < ahead; ++kb) weights(kb, kb);
-      asm volatile("griddepcontrol.wait;" ::: "memory");
+      if (!QUANT) asm volatile("griddepcontrol.wait;" ::: "memory");
       for (int kb = from; kb < ahead; ++kb) tokens(kb, kb);
       int s = ahead == S ? 0 : ahead, kb = ahead;
       uint32_t ph = 0;  // of the stage's last use
@@ -166,14 +171,14 @@ __global__ void __launch_bounds__(kThreads, 2)
     // ------------------------------------------------------------- MMAs ----
     const uint32_t on = elect();
     const uint32_t idesc = (1u << 23) | (static_cast<uint32_t>(p.bn >> 3) << 17) | (8u << 24);
-    const uint64_t desc0 = sw128_desc(base);
+    const uint64_t a0 = sw128_desc(a_base), b0 = sw128_desc(b_base);
     int s = 0;
     uint32_t ph = 0, sfa = 0;
     // the barriers of a step are looked at under the step before it
     bool staged = false, scaled = false;
     for (int kb = 0; kb < nkb; ++kb) {
-      const int id = kb % kScaleBlocks, at = kb / kScaleBlocks, set = at % kScaleSets;
-      if (id == 0) {
+      const int id = (kb0 + kb) % kScaleBlocks, at = (kb0 + kb) / kScaleBlocks - set0, set = at % kScaleSets;
+      if (id == 0 || kb == 0) {
         // a set that is there has its place in tensor memory free too: the
         // places are as many, and its own in shared memory was
         if (!__all_sync(0xffffffffu, scaled) &&
@@ -185,17 +190,15 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       if (!__all_sync(0xffffffffu, staged) && !(ok = wait.warp(full(s), ph, kDevErrFullBarrier))) break;
       tc_fence_after();
-      const uint64_t a = desc0 + ((s * stage) >> 4), b = a + (a_bytes >> 4);
+      const uint64_t a = a0 + (((QUANT ? kb * a_bytes : s * stage)) >> 4), b = b0 + ((s * stage) >> 4);
       const uint32_t with_id = idesc | (static_cast<uint32_t>(id) << 29) | (static_cast<uint32_t>(id) << 4);
       const uint32_t freed = empty(s);
       if (++s == S) {
         s = 0;
         ph ^= 1u;
       }
-#ifndef NOPEEK
       staged = is_over(full(s), ph);
       if (id == kScaleBlocks - 1) scaled = is_over(sf_full((at + 1) % kScaleSets), ((at + 1) / kScaleSets) & 1u);
-#endif
 #pragma unroll
       for (int k = 0; k < kBlock / 32; ++k)
         mma_scaled<1>(on, tmem, a + k * 2, b + k * 2, with_id, sfa, sfa + 4, kb > 0 || k > 0);
@@ -207,13 +210,14 @@ __global__ void __launch_bounds__(kThreads, 2)
     commit<1>(on, drain);
     wait_bar_teardown(drain, 0);
     __syncwarp();
-  } else if (warp < 4) {
+  } else if (warp == 3 || (warp == 2 && !QUANT)) {
     // ------------------------------------------------------------ scales ----
     // Set of 128 rows x 4 blocks: row r's word at (r % 32) 16 + (r / 32) 4.  Warp 2
     // gathers the tokens' rows, warp 3 the weights', of which the gate's come
     // first.
-    const bool mine = warp == 2;
+    const bool mine = warp == 2;  // the tokens' rows
     if (mine) asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int all_sets = (p.G + kScaleBlocks - 1) / kScaleBlocks;
     const uint8_t *at[4], *first[4];
     int access[4];
     long bytes[4];
@@ -226,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       access[i] = mine ? p.access[0] : which == 2 ? p.access[2] : p.access[1];
       if (set0 % 4 != 0 && access[i] == 16) access[i] = 4;
       bytes[i] = static_cast<long>(mine ? p.M : p.N) * p.G;
-      at[i] = there ? first[i] + static_cast<long>(row) * p.G + kb0 : nullptr;
+      at[i] = there ? first[i] + static_cast<long>(row) * p.G + set0 * kScaleBlocks : nullptr;
     }
     const int left = all_sets - set0;
     auto request = [&](uint32_t (&w)[4][kScaleBatch], int q) {
@@ -256,10 +260,59 @@ __global__ void __launch_bounds__(kThreads, 2)
       request(w0, q + 2 * kScaleBatch);
       hand_over(w1, q + kScaleBatch);
     }
-  } else if ((warp & 3) * 32 < p.mr) {
+  } else if (warp >= 4) {
+    if (QUANT) {
+      // ------------------------------------------- quantizing the tokens ----
+      // Half a warp a token and K block, as the quantizer's kernel does it: 8
+      // elements a lane; codes at their place in the swizzled tile, the scale
+      // at its own among the set's bytes.
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      constexpr int AHEAD = 8, TEAMS = 8;
+      const int units = p.M * nkb, l = lane & 15;
+      for (int u0 = (warp - 4) * 2 + (lane >> 4); (u0 & ~1) < units; u0 += AHEAD * TEAMS) {
+        uint4 x[AHEAD];
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+          const int u = u0 + j * TEAMS, kb = u / p.M, k = (kb0 + kb) * kBlock + l * 8;
+          x[j] = make_uint4(0, 0, 0, 0);
+          if (u < units && k < p.K) x[j] = *reinterpret_cast<const uint4 *>(p.x + static_cast<long>(u - kb * p.M) * p.K + k);
+        }
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+          const int u = u0 + j * TEAMS, kb = u / p.M, row = u - kb * p.M;
+          if ((u & ~1) >= units) break;
+          const __half2 *h = reinterpret_cast<const __half2 *>(&x[j]);
+          float v[8], top = 0.f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 f = __half22float2(h[e]);
+            v[2 * e] = f.x;
+            v[2 * e + 1] = f.y;
+            top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+          }
+#pragma unroll
+          for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          const uint32_t byte = fp8_scale_byte(top);
+          const float m = fp8_scale_inverse(byte);
+          if (u < units) {
+            *reinterpret_cast<uint2 *>(sm + kb * a_bytes + row * 128 + (((l >> 1) ^ (row & 7)) << 4) + (l & 1) * 8) =
+                make_uint2(fp8_pack4(v[0] * m, v[1] * m, v[2] * m, v[3] * m),
+                           fp8_pack4(v[4] * m, v[5] * m, v[6] * m, v[7] * m));
+            const int gb = kb0 + kb;
+            if (l == 0)
+              sm[kRegion + (gb / kScaleBlocks - set0) * kSetBytes + row * 16 + gb % kScaleBlocks] =
+                  static_cast<uint8_t>(byte);
+          }
+        }
+      }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane < nsets) mbar_arrive(sf_full(lane));  // no more sets than places
+      __syncwarp();
+    }
     // ----------------------------------------- sums to shared memory --------
     // Rows of bn + 4 floats: eight rows' 16-byte pieces fill all banks.
-    if (wait.warp(acc_full, 0, kDevErrAccumBarrier)) {
+    if ((warp & 3) * 32 < p.mr && wait.warp(acc_full, 0, kDevErrAccumBarrier)) {
       tc_fence_after();
       const int row = (warp & 3) * 32 + lane;
       const uint32_t from = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
@@ -378,11 +431,6 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 // ------------------------------------------------------------ host side --
 
-struct Plan {
-  int mr, bn, split, nx;
-  float us;
-};
-
 // Microseconds of a call by a model fitted to 2850 timings (1 to 1000 rows, twelve
 // shapes of weights, all tiles and parts): its choice is on average 1 % and at most
 // 18 % slower than the best one.  A CTA takes 83 GB/s, or 0.23 us a K block (one
@@ -390,8 +438,7 @@ struct Plan {
 // 6770 GB/s to all; more than two CTAs an SM wait for a place; the epilogue and the
 // joining of parts go with the tile's size.
 float estimate(const Fp8Params &f, int mr, int bn, int split, int nx) {
-  const int sets = (f.G + kScaleBlocks - 1) / kScaleBlocks;
-  const int blocks = std::min((sets + split - 1) / split * kScaleBlocks, f.G);
+  const int blocks = ceil_div(f.G, split);
   const int cols = f.w[1] == nullptr ? bn : bn / 2;
   const long groups = (static_cast<long>(f.N) + cols * nx - 1) / (cols * nx);
   const long ctas = groups * nx * ceil_div(f.M, 128) * split;
@@ -403,21 +450,8 @@ float estimate(const Fp8Params &f, int mr, int bn, int split, int nx) {
   return 3.9f + std::max(waves * blocks * block, hbm) + (waves - 1.f) * 3.6f + join + 5.7f * waves * tile;
 }
 
-// The tile and parts of K of the least estimate.
-Plan choose(const Fp8Params &f) {
-  Plan best = {};
-  const int tiles_m = ceil_div(f.M, 128), mr = (ceil_div(f.M, tiles_m) + 7) & ~7;
-  const int sets = (f.G + kScaleBlocks - 1) / kScaleBlocks, nx = f.codes != nullptr ? 2 : 1;
-  for (int bn = nx == 2 ? 128 : f.w[1] == nullptr ? 32 : 48; bn <= 128; bn += 16)
-    for (int split = 1; split * nx <= 8 && split <= sets; split *= 2) {
-      const float t = estimate(f, mr, bn, split, nx);
-      if (best.us == 0.f || t < best.us) best = {mr, bn, split, nx, t};
-    }
-  return best;
-}
-
-template <int MODE>
-int launch_t(const Fp8Params &f, const Plan &plan, cudaStream_t s) {
+template <int MODE, bool QUANT>
+int launch_t(const Fp8Params &f, const Fp8Plan &plan, cudaStream_t s) {
   static bool ready[64] = {};
   static std::mutex mu;
   int dev = 0;
@@ -425,7 +459,7 @@ int launch_t(const Fp8Params &f, const Plan &plan, cudaStream_t s) {
   {
     std::lock_guard<std::mutex> lock(mu);
     if (!ready[dev]) {
-      if (cudaFuncSetAttribute(fp8_mid_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) !=
+      if (cudaFuncSetAttribute(fp8_mid_kernel<MODE, QUANT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) !=
           cudaSuccess)
         return W8A8_ERR_CUDA;
       ready[dev] = true;
@@ -438,15 +472,22 @@ int launch_t(const Fp8Params &f, const Plan &plan, cudaStream_t s) {
   p.sw[1] = f.sw[1];
   p.M = f.M;
   p.N = f.N;
+  p.K = f.K;
   p.G = f.G;
   p.mr = plan.mr;
   p.bn = plan.bn;
   p.split = plan.split;
   p.nx = plan.nx;
-  // the last stage's MMAs read 128 rows from its start
-  const int stage = (p.mr + p.bn) * kBlock, spare = (128 - p.bn - p.mr) * kBlock;
-  const int fit = (kRegion - (spare > 0 ? spare : 0)) / stage;
-  p.stages = fit < kMaxStages ? fit : kMaxStages;
+  if (QUANT) {
+    p.x = f.xh;
+    p.token_bytes = ceil_div(f.G, p.split) * p.mr * kBlock;
+    p.stages = (kRegion - p.token_bytes) / (p.bn * kBlock);
+  } else {
+    // the last stage's MMAs read 128 rows from its start
+    const int spare = (128 - p.bn - p.mr) * kBlock;
+    p.stages = (kRegion - (spare > 0 ? spare : 0)) / ((p.mr + p.bn) * kBlock);
+  }
+  if (p.stages > kMaxStages) p.stages = kMaxStages;
   p.access[0] = scale_access(f.sx, f.G);
   p.access[1] = scale_access(f.sw[0], f.G);
   p.access[2] = scale_access(f.sw[1], f.G);
@@ -462,8 +503,9 @@ int launch_t(const Fp8Params &f, const Plan &plan, cudaStream_t s) {
   const long groups = (static_cast<long>(f.N) + cols * p.nx - 1) / (cols * p.nx);
   if (groups * cols * p.nx > 0x7fffffffL || groups * team > 0x7fffffffL) return W8A8_ERR_INVALID_ARG;
   CUtensorMap mx, mw0, mw1;
-  if (!make_map(&mx, f.x, f.M, f.K, 1, p.mr) || !make_map(&mw0, f.w[0], f.N, f.K, 1, cols)) return W8A8_ERR_CUDA;
-  mw1 = mw0;
+  if (!make_map(&mw0, f.w[0], f.N, f.K, 1, cols)) return W8A8_ERR_CUDA;
+  mx = mw1 = mw0;
+  if (!QUANT && !make_map(&mx, f.x, f.M, f.K, 1, p.mr)) return W8A8_ERR_CUDA;
   if (MODE != kLinear && !make_map(&mw1, f.w[1], f.N, f.K, 1, cols)) return W8A8_ERR_CUDA;
 
   cudaLaunchConfig_t cfg = {};
@@ -480,7 +522,7 @@ int launch_t(const Fp8Params &f, const Plan &plan, cudaStream_t s) {
   at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = team > 1 ? 2 : 1;
-  if (cudaLaunchKernelEx(&cfg, fp8_mid_kernel<MODE>, mx, mw0, mw1, p) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, fp8_mid_kernel<MODE, QUANT>, mx, mw0, mw1, p) != cudaSuccess) {
     cudaGetLastError();
     return W8A8_ERR_CUDA;
   }
@@ -489,12 +531,29 @@ int launch_t(const Fp8Params &f, const Plan &plan, cudaStream_t s) {
 
 }  // namespace
 
-float estimate_fp8_mid(const Fp8Params &f) { return choose(f).us; }
+Fp8Plan plan_fp8_mid(const Fp8Params &f) {
+  Fp8Plan best = {};
+  const int tiles_m = ceil_div(f.M, 128), mr = (ceil_div(f.M, tiles_m) + 7) & ~7;
+  const int nx = f.codes != nullptr ? 2 : 1;
+  for (int bn = nx == 2 ? 128 : f.w[1] == nullptr ? 32 : 48; bn <= 128; bn += 16)
+    for (int split = 1; split * nx <= 8 && split <= f.G; split *= 2) {
+      const float t = estimate(f, mr, bn, split, nx);
+      if (best.us == 0.f || t < best.us) best = {mr, bn, split, nx, t};
+    }
+  return best;
+}
 
-int launch_fp8_mid(const Fp8Params &f, cudaStream_t s) {
-  const Plan plan = choose(f);
-  if (f.w[1] == nullptr) return launch_t<kLinear>(f, plan, s);
-  return f.codes != nullptr ? launch_t<kGatedCodes>(f, plan, s) : launch_t<kGatedHalf>(f, plan, s);
+bool fp8_mid_quantizes(const Fp8Params &f, const Fp8Plan &plan) {
+  // every part's sets have places of their own, and a thread's share of the work
+  // is two rounds of requests
+  const int blocks = ceil_div(f.G, plan.split);
+  return f.M <= 32 && f.M * blocks <= 128 && (blocks + 2 * kScaleBlocks - 2) / kScaleBlocks <= kScaleSets;
+}
+
+int launch_fp8_mid(const Fp8Params &f, const Fp8Plan &plan, cudaStream_t s) {
+  if (f.w[1] == nullptr) return f.xh != nullptr ? launch_t<kLinear, true>(f, plan, s) : launch_t<kLinear, false>(f, plan, s);
+  if (f.codes == nullptr) return launch_t<kGatedHalf, false>(f, plan, s);
+  return f.xh != nullptr ? launch_t<kGatedCodes, true>(f, plan, s) : launch_t<kGatedCodes, false>(f, plan, s);
 }
 
 }  // namespace w8a8
