@@ -68,7 +68,7 @@ int launch_product(Fp8Params &p, cudaStream_t s, const __half *x = nullptr) {
   Fp8Plan plan = {};
   if (small) {
     plan = plan_fp8_mid(p);
-    small = p.M <= 128 || plan.us <= estimate_fp8_tc(p);
+    small = p.M <= 128 || plan.split > 1 || plan.us <= estimate_fp8_tc(p);
   }
   if (x != nullptr) {
     if (small && fp8_mid_quantizes(p, plan))

@@ -27,7 +27,7 @@ struct Fp8Plan {
 };
 
 // Tiles of up to 128 x 128, K divided (fp8_mid.cu), and pairs of CTAs on tiles of
-// 256 x 256 (fp8_tc.cu).
+// 256 x 256 (fp8_tc.cu), which is for undivided K alone.
 Fp8Plan plan_fp8_mid(const Fp8Params &p);
 bool fp8_mid_quantizes(const Fp8Params &p, const Fp8Plan &plan);  // a few fp16 rows: xh
 int launch_fp8_mid(const Fp8Params &p, const Fp8Plan &plan, cudaStream_t s);

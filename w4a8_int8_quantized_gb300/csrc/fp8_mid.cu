@@ -105,26 +105,20 @@ __global__ void __launch_bounds__(kThreads, 2)
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   const Waits wait{abort_flag, p.err, p.wait_limit};
 
-  if (threadIdx.x == 0) {
+  // a thread a barrier: full, empty, the scales' full and empty, the sums, the drain
+  if (threadIdx.x < kBars) {
+    const int i = static_cast<int>(threadIdx.x) - 2 * kMaxStages;
+    mbar_init(bar0 + 8u * threadIdx.x, i >= 0 && i < kScaleSets ? (QUANT ? 5 : 2) : 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  } else if (threadIdx.x == kThreads - 1) {
     prefetch_map(&map_w0);
     if (MODE != kLinear) prefetch_map(&map_w1);
-    prefetch_map(&map_x);
-    for (int s = 0; s < S; ++s) {
-      mbar_init(full(s), 1);
-      mbar_init(empty(s), 1);
-    }
-    for (int i = 0; i < kScaleSets; ++i) {
-      mbar_init(sf_full(i), QUANT ? 5 : 2);  // the warps that fill it
-      mbar_init(sf_empty(i), 1);
-    }
-    mbar_init(acc_full, 1);
-    mbar_init(drain, 1);
+    if (!QUANT) prefetch_map(&map_x);
     *abort_flag = 0;
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
-                 "r"(kTmemCols));
+                 "n"(kTmemCols));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   tc_fence_before();
@@ -202,8 +196,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
       for (int k = 0; k < kBlock / 32; ++k)
         mma_scaled<1>(on, tmem, a + k * 2, b + k * 2, with_id, sfa, sfa + 4, kb > 0 || k > 0);
-      commit<1>(on, freed);
-      if (id == kScaleBlocks - 1) commit<1>(on, sf_empty(set));
+      if (kb + S < nkb) commit<1>(on, freed);  // else it is not filled again
+      if (id == kScaleBlocks - 1 && at + kScaleSets < nsets) commit<1>(on, sf_empty(set));
     }
     if (ok) commit<1>(on, acc_full);
     // every MMA has landed before tensor memory is freed
@@ -341,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncthreads();
   tc_fence_after();
   if (warp == 1)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmemCols));
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // ------------------------------------------------------------- outputs ----
@@ -431,23 +425,28 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 // ------------------------------------------------------------ host side --
 
-// Microseconds of a call by a model fitted to 2850 timings (1 to 1000 rows, twelve
-// shapes of weights, all tiles and parts): its choice is on average 1 % and at most
-// 18 % slower than the best one.  A CTA takes 83 GB/s, or 0.23 us a K block (one
-// thread issues its MMAs; a little more where two CTAs share an SM); HBM gives
-// 6770 GB/s to all; more than two CTAs an SM wait for a place; the epilogue and the
-// joining of parts go with the tile's size.
+// CTAs of this kernel that run at once, by the cluster's size: two an SM, less what
+// clusters leave of the processor clusters (from cudaOccupancyMaxActiveClusters, which
+// counts one an SM for a kernel with tcgen05 instructions; two were seen to run).
+constexpr int kResident[9] = {0, 304, 304, 276, 288, 280, 276, 210, 240};
+
+// Microseconds of a call by a model fitted to 6040 timings (1 to 1000 rows, twelve
+// shapes of weights, all tiles and parts): its choice takes on average 1.4 % and at
+// most 15 % longer than the best one.  A CTA takes 77 GB/s, or 0.27 us a K block (one
+// thread issues its MMAs), an SM 137 GB/s; HBM gives 6200 GB/s to all; the epilogue
+// and the joining of parts go with the tile's size.
 float estimate(const Fp8Params &f, int mr, int bn, int split, int nx) {
-  const int blocks = ceil_div(f.G, split);
-  const int cols = f.w[1] == nullptr ? bn : bn / 2;
+  const int blocks = ceil_div(f.G, split), cols = f.w[1] == nullptr ? bn : bn / 2, team = split * nx;
   const long groups = (static_cast<long>(f.N) + cols * nx - 1) / (cols * nx);
-  const long ctas = groups * nx * ceil_div(f.M, 128) * split;
-  const float waves = static_cast<float>((ctas + 2 * kNumSMsGB300 - 1) / (2 * kNumSMsGB300));
-  const float block = std::max(ctas <= kNumSMsGB300 ? 0.23f : 0.263f, (mr + bn) * (kBlock / 83e3f));
-  const float hbm = static_cast<float>(f.N) * (f.w[1] == nullptr ? 1 : 2) * f.K / 6.77e6f;
+  const long ctas = groups * team * ceil_div(f.M, 128);
+  const float waves = static_cast<float>((ctas + kResident[team] - 1) / kResident[team]);
+  const float bytes = (mr + bn) * (kBlock * 1e-3f);  // of a stage, in KB
+  const float block = std::max(ctas <= kNumSMsGB300 ? 0.27f : 0.32f, bytes / 77.f);
+  const float sm = static_cast<float>(ctas) * blocks * bytes / (kNumSMsGB300 * 137.f);
+  const float hbm = static_cast<float>(f.N) * (f.w[1] == nullptr ? 1 : 2) * f.K / 6.2e6f;
   const float tile = mr * bn / 16384.f;
-  const float join = split * nx == 1 ? 0.f : 0.5f + 3.4f * (split - 1) * tile;
-  return 3.9f + std::max(waves * blocks * block, hbm) + (waves - 1.f) * 3.6f + join + 5.7f * waves * tile;
+  const float join = team == 1 ? 0.f : 0.24f + 0.06f * team + 2.2f * (split - 1) * tile;
+  return 2.5f + std::max(std::max(waves * blocks * block, hbm), sm) + (waves - 1.f) * 3.6f + join + 2.2f * waves * tile;
 }
 
 template <int MODE, bool QUANT>
@@ -460,7 +459,9 @@ int launch_t(const Fp8Params &f, const Fp8Plan &plan, cudaStream_t s) {
     std::lock_guard<std::mutex> lock(mu);
     if (!ready[dev]) {
       if (cudaFuncSetAttribute(fp8_mid_kernel<MODE, QUANT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) !=
-          cudaSuccess)
+              cudaSuccess ||
+          cudaFuncSetAttribute(fp8_mid_kernel<MODE, QUANT>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                               cudaSharedmemCarveoutMaxShared) != cudaSuccess)
         return W8A8_ERR_CUDA;
       ready[dev] = true;
     }
@@ -531,16 +532,37 @@ int launch_t(const Fp8Params &f, const Fp8Plan &plan, cudaStream_t s) {
 
 }  // namespace
 
-Fp8Plan plan_fp8_mid(const Fp8Params &f) {
+namespace {
+
+// The best tile for these parts of K.
+Fp8Plan best_tile(const Fp8Params &f, int split) {
   Fp8Plan best = {};
   const int tiles_m = ceil_div(f.M, 128), mr = (ceil_div(f.M, tiles_m) + 7) & ~7;
   const int nx = f.codes != nullptr ? 2 : 1;
-  for (int bn = nx == 2 ? 128 : f.w[1] == nullptr ? 32 : 48; bn <= 128; bn += 16)
-    for (int split = 1; split * nx <= 8 && split <= f.G; split *= 2) {
-      const float t = estimate(f, mr, bn, split, nx);
-      if (best.us == 0.f || t < best.us) best = {mr, bn, split, nx, t};
-    }
+  for (int bn = nx == 2 ? 128 : f.w[1] == nullptr ? 32 : 48; bn <= 128; bn += 16) {
+    const float t = estimate(f, mr, bn, split, nx);
+    if (best.us == 0.f || t < best.us) best = {mr, bn, split, nx, t};
+  }
   return best;
+}
+
+}  // namespace
+
+Fp8Plan plan_fp8_mid(const Fp8Params &f) {
+  // The parts of K decide the order of a sum, so they are the same for a class of
+  // batches, whose result for a row then does not depend on the others: those that
+  // suit the class's largest (2 % slower on average than each batch's own, at most
+  // 25 %).  Undivided, both kernels give the same sums.
+  Fp8Params typical = f;
+  typical.M = f.M <= 16 ? 16 : f.M <= 64 ? 64 : f.M <= 128 ? 128 : f.M <= 384 ? 384 : 1024;
+  const int most = f.M > 1024 ? 1 : std::min(f.codes != nullptr ? 4 : 8, f.G);
+  Fp8Plan best = {};
+  if (typical.M > 128) best.us = estimate_fp8_tc(typical), best.split = 1;
+  for (int split = 1; split <= most; ++split) {
+    const Fp8Plan plan = best_tile(typical, split);
+    if (best.us == 0.f || plan.us < best.us) best = plan;
+  }
+  return best_tile(f, best.split);
 }
 
 bool fp8_mid_quantizes(const Fp8Params &f, const Fp8Plan &plan) {
