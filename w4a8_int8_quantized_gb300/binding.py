@@ -564,23 +564,34 @@ def kv_cache_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tenso
 # A decoding step's calls again: plain comparisons first, the words only when
 # one fails.
 
+_Tensor = torch.Tensor
 _E4M3, _E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
 _CODES = {"int8": (0, torch.int8), "half": (1, _HALF), "fp8": (2, _E4M3)}
 _GATES = {"silu": 0, "gelu": 1}
 
 
-def _rows_of(t, dtype, name: str, device=None, rows=None, cols=None):
-    """Sizes of t, a contiguous [rows, cols] of this type (None: any) on the device
-    (None: any CUDA device, which has to be the current one)."""
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == 2 and t.is_cuda
-            and t.is_contiguous() and (device is None or t.device == device)):
-        r, c = t.shape
-        if (rows is None or r == rows) and (cols is None or c == cols):
-            return r, c
+def _fits(t, dtype, device, shape) -> bool:
+    return (isinstance(t, _Tensor) and t.dtype is dtype and t.device == device and t.shape == shape
+            and t.is_contiguous())
+
+
+def _refuse(t, dtype, name: str, device, shape):
+    """The error for a tensor that does not fit; shape's None: any."""
     _need(t, dtype, name)
     if device is not None and t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
-    raise ValueError(f"{name} must have shape {(rows, cols)} (None: any), got {tuple(t.shape)}")
+    raise ValueError(f"{name} must have shape {shape} (None: any), got {tuple(t.shape)}")
+
+
+def _rows_of(t, dtype, name: str, device=None, cols=None):
+    """Sizes of t, a contiguous [rows, cols] of this type (None: any) on the device
+    (None: any CUDA device, which has to be the current one)."""
+    if (isinstance(t, _Tensor) and t.dtype is dtype and t.is_contiguous()
+            and (t.is_cuda if device is None else t.device == device)):
+        shape = t.shape
+        if len(shape) == 2 and (cols is None or shape[1] == cols):
+            return shape
+    _refuse(t, dtype, name, device, (None, cols))
 
 
 def _current(device) -> int:
@@ -595,21 +606,30 @@ def _given(t, dtype, name: str, device, rows: int, cols: int):
     """t, checked, or a new [rows, cols] for it."""
     if t is None:
         return torch.empty((rows, cols), dtype=dtype, device=device)
-    _rows_of(t, dtype, name, device, rows, cols)
+    if not _fits(t, dtype, device, (rows, cols)):
+        _refuse(t, dtype, name, device, (rows, cols))
     return t
 
 
-def _held(q, scale, name: str, device=None, rows=None, cols=None):
+def _like(t, x, name: str):
+    """t, checked, or a new tensor, like x."""
+    if t is None:
+        return torch.empty_like(x)
+    if not _fits(t, x.dtype, x.device, x.shape):
+        _refuse(t, x.dtype, name, x.device, tuple(x.shape))
+    return t
+
+
+def _held(q, scale, name: str, device=None, cols=None):
     """Sizes of rows of 8-bit floats: e4m3 codes and their e8m0 scales."""
-    r, c = _rows_of(q, _E4M3, name, device, rows, cols)
-    _rows_of(scale, _E8M0, "the scales of " + name, q.device, r, (c + 127) >> 7)
-    return r, c
+    r, c = shape = _rows_of(q, _E4M3, name, device, cols)
+    if not _fits(scale, _E8M0, q.device, (r, (c + 127) >> 7)):
+        _refuse(scale, _E8M0, "the scales of " + name, q.device, (r, (c + 127) >> 7))
+    return shape
 
 
-def _scratch(workspace, need: int, device):
-    if workspace is None:
-        return torch.empty(need or 1, dtype=torch.uint8, device=device)
-    if not (isinstance(workspace, torch.Tensor) and workspace.dtype is torch.uint8
+def _scratch(workspace, device):
+    if not (isinstance(workspace, _Tensor) and workspace.dtype is torch.uint8
             and workspace.device == device and workspace.is_contiguous()):
         raise ValueError(f"workspace must be a contiguous torch.uint8 tensor on {device}")
     return workspace
@@ -618,16 +638,15 @@ def _scratch(workspace, need: int, device):
 def _norm_args(x, weight, residual, residual_out):
     M, K = _rows_of(x, _HALF, "x")
     device = x.device
-    if not (isinstance(weight, torch.Tensor) and weight.dtype is _HALF and weight.device == device
-            and weight.dim() == 1 and weight.shape[0] == K and weight.is_contiguous()):
-        _need(weight, _HALF, "weight", (K,))
-        raise ValueError(f"weight must be on {device}, got {weight.device}")
+    if not _fits(weight, _HALF, device, (K,)):
+        _refuse(weight, _HALF, "weight", device, (K,))
     if residual is None:
         if residual_out is not None:
             raise ValueError("residual_out without a residual")
         return M, K, device, 0, None, 0
-    _rows_of(residual, _HALF, "residual", device, M, K)
-    residual_out = _given(residual_out, _HALF, "residual_out", device, M, K)
+    if not _fits(residual, _HALF, device, x.shape):
+        _refuse(residual, _HALF, "residual", device, (M, K))
+    residual_out = _like(residual_out, x, "residual_out")
     return M, K, device, residual.data_ptr(), residual_out, residual_out.data_ptr()
 
 
@@ -637,7 +656,7 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual=None, eps: float = 
     With a residual [M, K], of h = fp16(x + residual): (y, h).  residual_out may
     be the residual (or x) itself."""
     M, K, device, r_at, h, h_at = _norm_args(x, weight, residual, residual_out)
-    y = _given(y, _HALF, "y", device, M, K)
+    y = _like(y, x, "y")
     status = (_lib or load()).rms_norm(x.data_ptr(), r_at, weight.data_ptr(), M, K, eps, h_at,
                                        y.data_ptr(), _current(device))
     if status:
@@ -703,7 +722,7 @@ def fp8_gemm(xq, scale_a, Wq, scale_w, y=None):
     """Product of 8-bit float rows: xq [M, K] x Wq [N, K]^T -> fp16 y [M, N]."""
     M, K = _held(xq, scale_a, "xq")
     device = xq.device
-    N, _ = _held(Wq, scale_w, "Wq", device, None, K)
+    N, _ = _held(Wq, scale_w, "Wq", device, K)
     y = _given(y, _HALF, "y", device, M, N)
     status = (_lib or load()).fp8_gemm(xq.data_ptr(), scale_a.data_ptr(), Wq.data_ptr(),
                                        scale_w.data_ptr(), M, N, K, y.data_ptr(), _current(device))
@@ -727,8 +746,9 @@ def fp8_gated_gemm(xq, scale_a, Wg, scale_g, Wu, scale_u, activation: str = "sil
     gate = _gate(activation)
     M, K = _held(xq, scale_a, "xq")
     device = xq.device
-    F, _ = _held(Wg, scale_g, "Wg", device, None, K)
-    _held(Wu, scale_u, "Wu", device, F, K)
+    F, _ = _held(Wg, scale_g, "Wg", device, K)
+    if _held(Wu, scale_u, "Wu", device, K)[0] != F:
+        raise ValueError(f"Wu must have as many rows as Wg, {F}, got {Wu.shape[0]}")
     h = _given(h, _E4M3 if codes else _HALF, "h", device, M, F)
     if codes:
         scale_h = _given(scale_h, _E8M0, "scale_h", device, M, (F + 127) >> 7)
@@ -754,12 +774,12 @@ def fp8_linear(x, Wq, scale_w, workspace=None, y=None):
     product with Wq [N, K] -> fp16 y [M, N]."""
     M, K = _rows_of(x, _HALF, "x")
     device = x.device
-    N, _ = _held(Wq, scale_w, "Wq", device, None, K)
+    N, _ = _held(Wq, scale_w, "Wq", device, K)
     lib = _lib or load()
     if workspace is None:
-        workspace = _scratch(None, lib.fp8_linear_workspace_bytes(M, K), device)
+        workspace = torch.empty(lib.fp8_linear_workspace_bytes(M, K) or 1, dtype=torch.uint8, device=device)
     else:
-        _scratch(workspace, 0, device)
+        _scratch(workspace, device)
     y = _given(y, _HALF, "y", device, M, N)
     status = lib.fp8_linear(x.data_ptr(), Wq.data_ptr(), scale_w.data_ptr(), M, N, K,
                             workspace.data_ptr(), workspace.numel(), y.data_ptr(),
@@ -781,14 +801,15 @@ def fp8_feed_forward(x, Wg, scale_g, Wu, scale_u, Wd, scale_d, activation: str =
     gate = _gate(activation)
     M, K = _rows_of(x, _HALF, "x")
     device = x.device
-    F, _ = _held(Wg, scale_g, "Wg", device, None, K)
-    _held(Wu, scale_u, "Wu", device, F, K)
-    N, _ = _held(Wd, scale_d, "Wd", device, None, F)
+    F, _ = _held(Wg, scale_g, "Wg", device, K)
+    if _held(Wu, scale_u, "Wu", device, K)[0] != F:
+        raise ValueError(f"Wu must have as many rows as Wg, {F}, got {Wu.shape[0]}")
+    N, _ = _held(Wd, scale_d, "Wd", device, F)
     lib = _lib or load()
     if workspace is None:
-        workspace = _scratch(None, lib.fp8_feed_forward_workspace_bytes(M, K, F), device)
+        workspace = torch.empty(lib.fp8_feed_forward_workspace_bytes(M, K, F) or 1, dtype=torch.uint8, device=device)
     else:
-        _scratch(workspace, 0, device)
+        _scratch(workspace, device)
     y = _given(y, _HALF, "y", device, M, N)
     status = lib.fp8_feed_forward(
         x.data_ptr(), Wg.data_ptr(), scale_g.data_ptr(), Wu.data_ptr(), scale_u.data_ptr(),

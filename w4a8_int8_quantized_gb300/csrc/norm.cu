@@ -98,13 +98,14 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormParams p) {
   __shared__ float2 red[2][kMaxThreads / 32];
   const int nvec = p.K >> 3, t = threadIdx.x, T = blockDim.x, lane = t & 31;
   const int width = FORMAT == kFp8 ? kFp8Group / 8 : p.gs >> 3;  // lanes of a group; 0: the row
+  // everything is read after the previous kernel: its output may be any of it
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   uint4 w[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     w[i] = make_uint4(0, 0, 0, 0);
     if (NORM && AHEAD && i * T + t < nvec) w[i] = p.w[i * T + t];
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
 
   auto load = [&](long row, uint4 (&x)[V], uint4 (&r)[V]) {
 #pragma unroll
