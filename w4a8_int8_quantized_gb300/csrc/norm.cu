@@ -11,7 +11,10 @@
 // in fp32 (11 + 11 bits) and v is rounded once, so the codes are those of the
 // fp32 value; it is never rounded to fp16 on the way.  max|v| of a row or
 // group is max|h w| / rms (rounding is monotonic), so one reduction gives the
-// sum of squares and the maximum together.
+// sum of squares and the maximum together.  An INT8 code v / (max|v| / 127) is
+// round(h w 127 / max|h w|), rounded once behind the factor 127 / max|h w|
+// (2^-24): 1 / rms cancels, and only a quotient within 2^-16 of a tie can go
+// either way.
 //
 // Design (HBM-bound, one pass): a block of T threads owns a row, V 16-byte
 // vectors a thread in registers.  A persistent grid: a block fetches its next
@@ -39,23 +42,30 @@ struct NormParams {
   float eps;
 };
 
-// Codes of eight fp32 values by the rule of the fp16 quantizer (v / s rounded
-// to nearest even): v * (1 / s) decides, but within 2^-14 of a tie the IEEE
-// quotient does.  |v| <= max|v| = 127 s up to rounding, so no clamp.
-__device__ __forceinline__ void quant8(const float (&v)[8], float s, float rcp, float (&q)[8]) {
-  bool any_near = false;
-  float t[8];
+// a b + c of two lanes, each rounded once
+__device__ __forceinline__ float2 fma2_rn(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n.reg .b64 a, b, c, d;\n"
+      "mov.b64 a, {%2, %3};\n"
+      "mov.b64 b, {%4, %5};\n"
+      "mov.b64 c, {%6, %7};\n"
+      "fma.rn.f32x2 d, a, b, c;\n"
+      "mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
+// 1.5 2^23: x + kRound is x rounded to an integer, in the low mantissa bits
+constexpr float kRound = 12582912.f;
+
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+__device__ __forceinline__ float most_of(const float2 (&p)[4]) {
+  float m = 0.f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    t[j] = v[j] * rcp;
-    q[j] = rintf(t[j]);
-    any_near |= near_half(t[j], q[j]);
-  }
-  if (any_near) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (near_half(t[j], q[j])) q[j] = rintf(__fdiv_rn(v[j], s));
-  }
+  for (int j = 0; j < 4; ++j) m = fmaxf(m, fmaxf(fabsf(p[j].x), fabsf(p[j].y)));
+  return m;
 }
 
 __device__ __forceinline__ uint4 hadd8(const uint4 &a, const uint4 &b) {
@@ -69,20 +79,10 @@ __device__ __forceinline__ uint4 hadd8(const uint4 &a, const uint4 &b) {
 
 // h w of eight elements (h alone without a norm), in fp32: exact
 template <bool NORM>
-__device__ __forceinline__ void products(const uint4 &h, const uint4 &w, float (&p)[8]) {
+__device__ __forceinline__ void products(const uint4 &h, const uint4 &w, float2 (&p)[4]) {
   const __half2 *a = reinterpret_cast<const __half2 *>(&h), *b = reinterpret_cast<const __half2 *>(&w);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float2 x = __half22float2(a[j]);
-    if (NORM) {
-      const float2 y = __half22float2(b[j]);
-      p[2 * j] = x.x * y.x;
-      p[2 * j + 1] = x.y * y.y;
-    } else {
-      p[2 * j] = x.x;
-      p[2 * j + 1] = x.y;
-    }
-  }
+  for (int j = 0; j < 4; ++j) p[j] = NORM ? mul2_rn(__half22float2(a[j]), __half22float2(b[j])) : __half22float2(a[j]);
 }
 
 constexpr int kMaxThreads = 512;
@@ -91,20 +91,20 @@ constexpr int kMaxThreads = 512;
 // they read what it writes); never when the codes are weights, which the
 // few-row kernels request before they wait.
 template <int FORMAT, bool NORM, bool RES, bool EARLY, int V>
-__global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormParams p) {
+__global__ void __launch_bounds__(kMaxThreads, V <= 4 ? 2 : 1) norm_kernel(const NormParams par) {
   // a second row in registers only where it fits
   constexpr bool AHEAD = V <= 2;
   if (EARLY) asm volatile("griddepcontrol.launch_dependents;");
   __shared__ float2 red[2][kMaxThreads / 32];
-  const int nvec = p.K >> 3, t = threadIdx.x, T = blockDim.x, lane = t & 31;
-  const int width = FORMAT == kFp8 ? kFp8Group / 8 : p.gs >> 3;  // lanes of a group; 0: the row
+  const int nvec = par.K >> 3, t = threadIdx.x, T = blockDim.x, lane = t & 31;
+  const int width = FORMAT == kFp8 ? kFp8Group / 8 : par.gs >> 3;  // lanes of a group; 0: the row
   // everything is read after the previous kernel: its output may be any of it
   asm volatile("griddepcontrol.wait;" ::: "memory");
   uint4 w[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     w[i] = make_uint4(0, 0, 0, 0);
-    if (NORM && AHEAD && i * T + t < nvec) w[i] = p.w[i * T + t];
+    if (NORM && AHEAD && i * T + t < nvec) w[i] = par.w[i * T + t];
   }
 
   auto load = [&](long row, uint4 (&x)[V], uint4 (&r)[V]) {
@@ -113,9 +113,9 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormParams p) {
       const int vi = i * T + t;
       x[i] = make_uint4(0, 0, 0, 0);
       if (RES) r[i] = make_uint4(0, 0, 0, 0);
-      if (row < p.rows && vi < nvec) {
-        x[i] = __ldcs(p.x + row * nvec + vi);
-        if (RES) r[i] = __ldcs(p.r + row * nvec + vi);
+      if (row < par.rows && vi < nvec) {
+        x[i] = __ldcs(par.x + row * nvec + vi);
+        if (RES) r[i] = __ldcs(par.r + row * nvec + vi);
       }
     }
   };
@@ -123,15 +123,17 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormParams p) {
   uint4 x[V], r[V];
   if (AHEAD) load(blockIdx.x, x, r);
   int parity = 0;
-  for (long row = blockIdx.x; row < p.rows; row += gridDim.x, parity ^= 1) {
+  for (long row = blockIdx.x; row < par.rows; row += gridDim.x, parity ^= 1) {
     if (!AHEAD) load(row, x, r);
     uint4 h[V];
-    float sum = 0.f, top = 0.f;
+    float2 p[V][4];  // kept between the passes where there is room (AHEAD)
+    float2 sums = make_float2(0.f, 0.f);
+    float top = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       h[i] = RES ? hadd8(x[i], r[i]) : x[i];
       const int vi = i * T + t;
-      if (RES && vi < nvec) p.h[row * nvec + vi] = h[i];
+      if (RES && vi < nvec) par.h[row * nvec + vi] = h[i];
     }
     if (AHEAD) load(row + gridDim.x, x, r);
     float inv = 1.f;
@@ -142,16 +144,15 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormParams p) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float2 f = __half22float2(a[j]);
-          sum = fmaf(f.x, f.x, fmaf(f.y, f.y, sum));
+          sums = fma2_rn(f, f, sums);
         }
         if (FORMAT < kFp8 && width == 0) {
-          if (!AHEAD) w[i] = i * T + t < nvec ? __ldg(p.w + i * T + t) : make_uint4(0, 0, 0, 0);
-          float q[8];
-          products<true>(h[i], w[i], q);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(q[j]));
+          if (!AHEAD) w[i] = i * T + t < nvec ? __ldg(par.w + i * T + t) : make_uint4(0, 0, 0, 0);
+          products<true>(h[i], w[i], p[i]);
+          top = fmaxf(top, most_of(p[i]));
         }
       }
+      float sum = sums.x + sums.y;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
         sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -167,14 +168,13 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormParams p) {
           top = fmaxf(top, red[parity][i].y);
         }
       }
-      const float mean = sum / static_cast<float>(p.K) + p.eps;
+      const float mean = sum / static_cast<float>(par.K) + par.eps;
       inv = mean > 0.f ? 1.f / sqrtf(mean) : mean == 0.f ? 0.f : mean;  // a row of zeros, eps 0: zeros
     }
-    float s = 1.f, rcp = 1.f;
+    float c = 0.f;  // INT8: code = round(p c), c = 127 / max|p|
     if (FORMAT < kFp8 && width == 0) {
-      s = __fdiv_rn(top * inv, 127.f);
-      rcp = s == 0.f ? 0.f : __frcp_rn(s);
-      if (t == 0) static_cast<float *>(p.scale)[row] = s;
+      c = top == 0.f ? 0.f : __fdiv_rn(127.f, top);
+      if (t == 0) static_cast<float *>(par.scale)[row] = __fdiv_rn(top * inv, 127.f);
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -183,51 +183,59 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormParams p) {
       // whole warp: those past it stay for the exchange
       if (i * T + (t & ~31) >= nvec) break;
       const bool in = vi < nvec;
-      if (NORM && !AHEAD) w[i] = in ? __ldg(p.w + vi) : make_uint4(0, 0, 0, 0);
-      float v[8];
-      products<NORM>(h[i], w[i], v);
-      float most = 0.f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (NORM) v[j] *= inv;
-        most = fmaxf(most, fabsf(v[j]));
+      if (!(AHEAD && FORMAT < kFp8 && width == 0)) {
+        if (NORM && !AHEAD) w[i] = in ? __ldg(par.w + vi) : make_uint4(0, 0, 0, 0);
+        products<NORM>(h[i], w[i], p[i]);
       }
       if (FORMAT == kFp8) {
+        float most = most_of(p[i]);
 #pragma unroll
         for (int o = kFp8Group / 16; o > 0; o >>= 1)
           most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-        const uint32_t byte = fp8_scale_byte(most);
-        const float m = fp8_scale_inverse(byte);
+        // v / 2^e is rounded once: the power of two joins 1 / rms exactly
+        const uint32_t byte = fp8_scale_byte(most * inv);
+        const float2 m = both(inv * fp8_scale_inverse(byte));
+        float2 q[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) q[j] = mul2_rn(p[i][j], m);
         if (in) {
-          static_cast<uint2 *>(p.out)[row * nvec + vi] =
-              make_uint2(fp8_pack4(v[0] * m, v[1] * m, v[2] * m, v[3] * m),
-                         fp8_pack4(v[4] * m, v[5] * m, v[6] * m, v[7] * m));
+          static_cast<uint2 *>(par.out)[row * nvec + vi] = make_uint2(fp8_pack4(q[0].x, q[0].y, q[1].x, q[1].y),
+                                                                    fp8_pack4(q[2].x, q[2].y, q[3].x, q[3].y));
           if ((lane & 15) == 0)
-            static_cast<uint8_t *>(p.scale)[row * ((nvec + 15) >> 4) + (vi >> 4)] =
-                static_cast<uint8_t>(byte);
+            static_cast<uint8_t *>(par.scale)[row * ((nvec + 15) >> 4) + (vi >> 4)] = static_cast<uint8_t>(byte);
         }
       } else if (FORMAT == kValues) {
         uint4 o;
         __half2 *a = reinterpret_cast<__half2 *>(&o);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) a[j] = __floats2half2_rn(v[2 * j], v[2 * j + 1]);
-        if (in) static_cast<uint4 *>(p.out)[row * nvec + vi] = o;
+        for (int j = 0; j < 4; ++j) a[j] = __float22half2_rn(mul2_rn(p[i][j], both(inv)));
+        if (in) static_cast<uint4 *>(par.out)[row * nvec + vi] = o;
       } else {
         if (width != 0) {
+          float most = most_of(p[i]);
           for (int o = width >> 1; o > 0; o >>= 1)
             most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-          s = __fdiv_rn(most, 127.f);
-          rcp = s == 0.f ? 0.f : __frcp_rn(s);
+          c = most == 0.f ? 0.f : __fdiv_rn(127.f, most);
           if (in && (lane & (width - 1)) == 0)
-            static_cast<float *>(p.scale)[row * (p.K / p.gs) + (vi << 3) / p.gs] = s;
+            static_cast<float *>(par.scale)[row * (par.K / par.gs) + (vi << 3) / par.gs] = __fdiv_rn(most * inv, 127.f);
         }
-        float q[8];
-        quant8(v, s, rcp, q);
+        float2 q[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) q[j] = fma2_rn(p[i][j], both(c), both(kRound));
         if (in) {
-          if (FORMAT == kHalf)
-            static_cast<uint4 *>(p.out)[row * nvec + vi] = pack_h8(q);
-          else
-            static_cast<uint2 *>(p.out)[row * nvec + vi] = pack_i8x8(q);
+          if (FORMAT == kHalf) {
+            uint4 o;
+            __half2 *a = reinterpret_cast<__half2 *>(&o);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) a[j] = __float22half2_rn(sub2_rn(q[j], both(kRound)));
+            static_cast<uint4 *>(par.out)[row * nvec + vi] = o;
+          } else {
+            auto low = [](const float2 &a, const float2 &b) {  // four low bytes
+              const uint32_t ab = __byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040);
+              return __byte_perm(ab, __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040), 0x5410);
+            };
+            static_cast<uint2 *>(par.out)[row * nvec + vi] = make_uint2(low(q[0], q[1]), low(q[2], q[3]));
+          }
         }
       }
     }
