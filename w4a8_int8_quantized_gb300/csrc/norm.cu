@@ -90,8 +90,11 @@ constexpr int kMaxThreads = 512;
 // EARLY: the kernels that follow may start (they wait for this grid before
 // they read what it writes); never when the codes are weights, which the
 // few-row kernels request before they wait.
-template <int FORMAT, bool NORM, bool RES, bool EARLY, int V>
-__global__ void __launch_bounds__(kMaxThreads, V <= 4 ? 2 : 1) norm_kernel(const NormParams par) {
+//
+// T threads at most.  Registers for three blocks of 256 an SM or two of 512 (17089
+// x 4096 to INT8 codes: 80 us; held to 64 registers 82, free 82).
+template <int FORMAT, bool NORM, bool RES, bool EARLY, int V, int MOST>
+__global__ void __launch_bounds__(MOST, V > 4 ? 1 : MOST == 256 ? 3 : 2) norm_kernel(const NormParams par) {
   // a second row in registers only where it fits
   constexpr bool AHEAD = V <= 2;
   if (EARLY) asm volatile("griddepcontrol.launch_dependents;");
@@ -242,7 +245,7 @@ __global__ void __launch_bounds__(kMaxThreads, V <= 4 ? 2 : 1) norm_kernel(const
   }
 }
 
-template <int FORMAT, bool NORM, bool RES, bool EARLY, int V>
+template <int FORMAT, bool NORM, bool RES, bool EARLY, int V, int MOST>
 int launch_v(const NormParams &p, int T, cudaStream_t s) {
   // blocks that are resident at once, per device and block size
   static int resident[64][kMaxThreads / 32] = {};
@@ -256,7 +259,7 @@ int launch_v(const NormParams &p, int T, cudaStream_t s) {
     if (known == 0) {
       int sms = 0, occ = 0;
       if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-          cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, norm_kernel<FORMAT, NORM, RES, EARLY, V>,
+          cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, norm_kernel<FORMAT, NORM, RES, EARLY, V, MOST>,
                                                         T, 0) != cudaSuccess || occ < 1)
         return W8A8_ERR_CUDA;
       known = sms * occ;
@@ -272,7 +275,7 @@ int launch_v(const NormParams &p, int T, cudaStream_t s) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, norm_kernel<FORMAT, NORM, RES, EARLY, V>, p) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, norm_kernel<FORMAT, NORM, RES, EARLY, V, MOST>, p) != cudaSuccess) {
     cudaGetLastError();
     return W8A8_ERR_CUDA;
   }
@@ -288,10 +291,10 @@ int launch_f(const NormParams &p, cudaStream_t s) {
   if (V == 1 && nvec > 128) V = 2;
   const int T = ((nvec + V - 1) / V + 31) & ~31;
   switch (V) {
-    case 1: return launch_v<FORMAT, NORM, RES, EARLY, 1>(p, T, s);
-    case 2: return launch_v<FORMAT, NORM, RES, EARLY, 2>(p, T, s);
-    case 4: return launch_v<FORMAT, NORM, RES, EARLY, 4>(p, T, s);
-    case 8: return launch_v<FORMAT, NORM, RES, EARLY, 8>(p, T, s);
+    case 1: return launch_v<FORMAT, NORM, RES, EARLY, 1, 256>(p, T, s);
+    case 2: return T <= 256 ? launch_v<FORMAT, NORM, RES, EARLY, 2, 256>(p, T, s) : launch_v<FORMAT, NORM, RES, EARLY, 2, 512>(p, T, s);
+    case 4: return launch_v<FORMAT, NORM, RES, EARLY, 4, 512>(p, T, s);
+    case 8: return launch_v<FORMAT, NORM, RES, EARLY, 8, 512>(p, T, s);
     default: return W8A8_ERR_INVALID_ARG;  // K > 32768
   }
 }
