@@ -368,7 +368,9 @@ int kv_cache_attention(const w8a8_half *q, long long q_token_stride, long long q
  *   h = fp16_rn(x + residual)            (h = x without a residual)
  *   v = h * weight / sqrt(mean(h^2) + eps)
  * v is an fp32 value (h * weight is exact, the sums are fp32); it is rounded
- * once, to fp16 or to codes.  A row of zeros with eps 0 gives zeros.  No
+ * once, to fp16 or to codes (INT8: 127 v / max|v|, rounded to the nearest; a
+ * quotient within 2^-16 of a tie may go either way).  A row of zeros with eps 0
+ * gives zeros.  No
  * counterpart on the method's pages, which start at the layer's input: an
  * addition of this library.  The conventions at the top of this file hold;
  * x, residual, weight and all outputs are 16-byte aligned, K is a multiple of
@@ -418,7 +420,9 @@ int rms_norm_quantize(const w8a8_half *x, const w8a8_half *residual, const w8a8_
  * The conventions at the top of this file hold, with K (and F) a multiple of
  * 16, code pointers 16-byte aligned and scale pointers at any address.  Sums
  * are fp32 (the products of two codes are exact), rounded once to the output's
- * type; their order depends on the sizes, not on timing. */
+ * type.  Their order depends on N, K and the class of M (up to 16, 64, 128, 384,
+ * 1024 rows, more), not on timing: within a class a row's result does not depend
+ * on the other rows of the batch.  No output may overlap an input. */
 
 /* fp16 rows to codes and scales.
  *   x   fp16 [M, K];  xq e4m3 [M, K] (out);  scale_a e8m0 [M, ceil(K/128)] (out) */
@@ -433,8 +437,8 @@ int quantize_weight_fp8(const w8a8_half *W, int N, int K, uint8_t *Wq, uint8_t *
  *   xq e4m3 [M, K], scale_a e8m0 [M, ceil(K/128)]; Wq e4m3 [N, K], scale_w e8m0
  *   [N, ceil(K/128)]; y fp16 [M, N] (out)
  * All products here are launched with programmatic stream serialization, and
- * the few-row kernels may read the weights (only these and their scales) before
- * the previous kernel on the stream has finished: see w8a8_mv. */
+ * may read the weights (only these and their scales) before the previous kernel
+ * on the stream has finished: see w8a8_mv. */
 int fp8_gemm(const uint8_t *xq, const uint8_t *scale_a, const uint8_t *Wq, const uint8_t *scale_w,
              int M, int N, int K, w8a8_half *y, w8a8_stream_t stream);
 
@@ -457,7 +461,9 @@ int fp8_gated_gemm(const uint8_t *xq, const uint8_t *scale_a, const uint8_t *Wg,
 /* Bytes of workspace of fp8_linear() (0 for invalid sizes). */
 size_t fp8_linear_workspace_bytes(int M, int K);
 
-/* The whole layer: quantize_act_fp8 into the workspace, then fp8_gemm.
+/* The whole layer: quantize_act_fp8 into the workspace, then fp8_gemm; for a few
+ * rows one kernel that does both, which leaves the workspace alone (it is checked
+ * all the same).  The result is that of the two calls, bit for bit.
  *   x fp16 [M, K]; Wq, scale_w as fp8_gemm; y fp16 [M, N] (out)
  *   workspace  at least fp8_linear_workspace_bytes(M, K), 256-byte aligned, else
  *              W8A8_ERR_WORKSPACE; its content does not matter */
@@ -468,7 +474,7 @@ int fp8_linear(const w8a8_half *x, const uint8_t *Wq, const uint8_t *scale_w, in
 size_t fp8_feed_forward_workspace_bytes(int M, int K, int F);
 
 /* The whole gated feed-forward block: quantize_act_fp8, fp8_gated_gemm to codes,
- * fp8_gemm: y = ((act(x Wg^T) * (x Wu^T)) as codes) Wd^T.
+ * fp8_gemm (the first two as one kernel for a few rows, with the same result): y = ((act(x Wg^T) * (x Wu^T)) as codes) Wd^T.
  *   x fp16 [M, K]; Wg, Wu e4m3 [F, K]; Wd e4m3 [N, F]; y fp16 [M, N] (out)
  *   workspace  at least fp8_feed_forward_workspace_bytes(M, K, F), 256-byte
  *              aligned, else W8A8_ERR_WORKSPACE; its content does not matter */

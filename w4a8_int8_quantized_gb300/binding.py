@@ -570,12 +570,12 @@ _CODES = {"int8": (0, torch.int8), "half": (1, _HALF), "fp8": (2, _E4M3)}
 _GATES = {"silu": 0, "gelu": 1}
 
 
-def _fits(t, dtype, device, shape) -> bool:
+def _matches(t, dtype, device, shape) -> bool:
     return (isinstance(t, _Tensor) and t.dtype is dtype and t.device == device and t.shape == shape
             and t.is_contiguous())
 
 
-def _refuse(t, dtype, name: str, device, shape):
+def _not_that(t, dtype, name: str, device, shape):
     """The error for a tensor that does not fit; shape's None: any."""
     _need(t, dtype, name)
     if device is not None and t.device != device:
@@ -591,7 +591,7 @@ def _rows_of(t, dtype, name: str, device=None, cols=None):
         shape = t.shape
         if len(shape) == 2 and (cols is None or shape[1] == cols):
             return shape
-    _refuse(t, dtype, name, device, (None, cols))
+    _not_that(t, dtype, name, device, (None, cols))
 
 
 def _current(device) -> int:
@@ -606,8 +606,8 @@ def _given(t, dtype, name: str, device, rows: int, cols: int):
     """t, checked, or a new [rows, cols] for it."""
     if t is None:
         return torch.empty((rows, cols), dtype=dtype, device=device)
-    if not _fits(t, dtype, device, (rows, cols)):
-        _refuse(t, dtype, name, device, (rows, cols))
+    if not _matches(t, dtype, device, (rows, cols)):
+        _not_that(t, dtype, name, device, (rows, cols))
     return t
 
 
@@ -615,16 +615,16 @@ def _like(t, x, name: str):
     """t, checked, or a new tensor, like x."""
     if t is None:
         return torch.empty_like(x)
-    if not _fits(t, x.dtype, x.device, x.shape):
-        _refuse(t, x.dtype, name, x.device, tuple(x.shape))
+    if not _matches(t, x.dtype, x.device, x.shape):
+        _not_that(t, x.dtype, name, x.device, tuple(x.shape))
     return t
 
 
 def _held(q, scale, name: str, device=None, cols=None):
     """Sizes of rows of 8-bit floats: e4m3 codes and their e8m0 scales."""
     r, c = shape = _rows_of(q, _E4M3, name, device, cols)
-    if not _fits(scale, _E8M0, q.device, (r, (c + 127) >> 7)):
-        _refuse(scale, _E8M0, "the scales of " + name, q.device, (r, (c + 127) >> 7))
+    if not _matches(scale, _E8M0, q.device, (r, (c + 127) >> 7)):
+        _not_that(scale, _E8M0, "the scales of " + name, q.device, (r, (c + 127) >> 7))
     return shape
 
 
@@ -638,14 +638,14 @@ def _scratch(workspace, device):
 def _norm_args(x, weight, residual, residual_out):
     M, K = _rows_of(x, _HALF, "x")
     device = x.device
-    if not _fits(weight, _HALF, device, (K,)):
-        _refuse(weight, _HALF, "weight", device, (K,))
+    if not _matches(weight, _HALF, device, (K,)):
+        _not_that(weight, _HALF, "weight", device, (K,))
     if residual is None:
         if residual_out is not None:
             raise ValueError("residual_out without a residual")
         return M, K, device, 0, None, 0
-    if not _fits(residual, _HALF, device, x.shape):
-        _refuse(residual, _HALF, "residual", device, (M, K))
+    if not _matches(residual, _HALF, device, x.shape):
+        _not_that(residual, _HALF, "residual", device, (M, K))
     residual_out = _like(residual_out, x, "residual_out")
     return M, K, device, residual.data_ptr(), residual_out, residual_out.data_ptr()
 
