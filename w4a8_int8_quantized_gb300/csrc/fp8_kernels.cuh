@@ -19,10 +19,10 @@ struct Fp8Params {
 
 __host__ __device__ __forceinline__ int fp8_groups_of(int K) { return (K + 127) / 128; }
 
-// How fp8_mid.cu works on a product: rows and columns of a tile, parts of K, tiles
-// that share a group of codes; and about how long it takes, in microseconds.
+// How fp8_mid.cu works on a product: CTAs that share a tile, tokens of each and
+// columns of the tile, parts of K, tiles that share a group of codes; and about how long it takes, in microseconds.
 struct Fp8Plan {
-  int mr, bn, split, nx;
+  int cg, mr, bn, split, nx;
   float us;
 };
 

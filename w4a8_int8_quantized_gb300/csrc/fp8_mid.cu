@@ -4,6 +4,12 @@
 // to 128 tokens x 128 columns, one tile a CTA, two CTAs an SM, and K divided
 // among the CTAs of a cluster where the tiles alone are too few.
 //
+// Above 128 rows a tile may be a pair's (cta_group::2): 256 tokens x up to 160
+// columns, each CTA fetching its own tokens and half of the weights.  What an SM
+// takes in is the limit there: 512 rows of 10240 x 2560 take 22.9 us in single CTAs
+// and 15.9 in pairs, 131 rows 10.1 and 11.6 (a cluster more to start), so the
+// estimate decides.
+//
 // The stages (a ring in half an SM's shared memory) hold only the rows that
 // there are: with 40 tokens a stage is 5 KB of tokens and up to 16 KB of
 // weights.  The MMA takes 128 rows all the same; what the others hold reaches
@@ -29,13 +35,22 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxStages = 12;
 constexpr int kScaleSets = 8;       // sets of scales in shared memory, and in tensor memory
-constexpr int kSetBytes = 2 * 512;  // 128 tokens, 128 columns
-constexpr uint32_t kTmemCols = 256, kScaleCol = 128;  // sums, then sets of 8 columns
 // half of an SM's 228 KB, less 1 KB that the system keeps for each CTA
 constexpr int kSmemBytes = 228 * 1024 / 2 - 1024;
 constexpr int kBars = 2 * (kMaxStages + kScaleSets) + 2;
-constexpr int kTail = kScaleSets * kSetBytes + kBars * 8 + 16;
-constexpr int kRegion = (kSmemBytes - 1024 - kTail) / 1024 * 1024;  // stages; 1 KB for alignment by hand
+constexpr uint32_t kTmemCols = 256;
+
+// CG: CTAs that share a tile.  Columns up to kMostCols, of which 128 and 32 (pairs)
+// in sets of scales of their own; behind them the scales in tensor memory.
+template <int CG>
+struct Room {
+  static constexpr int MOST_COLS = CG == 2 ? 160 : 128, SFB = CG == 2 ? 2 : 1;
+  static constexpr int SET_BYTES = 512 * (1 + SFB), SET_COLS = 4 * (1 + SFB);
+  static constexpr int TAIL = kScaleSets * SET_BYTES + kBars * 8 + 16;
+  static constexpr int REGION = (kSmemBytes - 1024 - TAIL) / 1024 * 1024;  // stages; 1 KB for alignment by hand
+  static_assert(MOST_COLS + kScaleSets * SET_COLS <= kTmemCols, "tensor memory");
+};
+
 
 enum Mode { kLinear = 0, kGatedHalf = 1, kGatedCodes = 2 };
 
@@ -74,7 +89,7 @@ __device__ __forceinline__ void take(float (&to)[8], const float4 &lo, const flo
   to[7] += hi.w;
 }
 
-template <int MODE, bool QUANT>
+template <int CG, int MODE, bool QUANT>
 __global__ void __launch_bounds__(kThreads, 2)
     fp8_mid_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w0,
                    const __grid_constant__ CUtensorMap map_w1, const MidParams p) {
@@ -82,13 +97,17 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
   uint8_t *sm = smem_raw + (base - raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kRegion = Room<CG>::REGION, kSetBytes = Room<CG>::SET_BYTES, SFB = Room<CG>::SFB;
+  constexpr uint32_t kScaleCol = Room<CG>::MOST_COLS;
   // QUANT: the tokens of all K blocks first, then the stages, of weights alone
-  const int S = p.stages, a_bytes = p.mr * kBlock, stage = (QUANT ? 0 : a_bytes) + p.bn * kBlock;
+  const int S = p.stages, a_bytes = p.mr * kBlock, stage = (QUANT ? 0 : a_bytes) + p.bn / CG * kBlock;
   const int cols = MODE == kLinear ? p.bn : p.bn / 2;
-  const int team = p.split * p.nx, rank = static_cast<int>(blockIdx.x) % team;
-  const int part = rank / p.nx;
-  const long tile_n = static_cast<long>(blockIdx.x) / team * p.nx + rank % p.nx;
-  const int col0 = static_cast<int>(tile_n * cols), row0 = static_cast<int>(blockIdx.y) * p.mr;
+  // a cluster: parts of K, each of nx tiles, each of one CTA or a pair
+  const int team = p.split * p.nx * CG, rank = static_cast<int>(blockIdx.x) % team;
+  const int half = CG == 2 ? rank & 1 : 0, leader = rank - half;
+  const int part = rank / (p.nx * CG), xi = rank / CG - part * p.nx;
+  const long tile_n = static_cast<long>(blockIdx.x) / team * p.nx + xi;
+  const int col0 = static_cast<int>(tile_n * cols), row0 = (static_cast<int>(blockIdx.y) * CG + half) * p.mr;
   // K blocks of this part; its sets of scales are those of the whole row
   const int kb0 = static_cast<int>(static_cast<long>(p.G) * part / p.split);
   const int nkb = static_cast<int>(static_cast<long>(p.G) * (part + 1) / p.split) - kb0;
@@ -108,7 +127,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   // a thread a barrier: full, empty, the scales' full and empty, the sums, the drain
   if (threadIdx.x < kBars) {
     const int i = static_cast<int>(threadIdx.x) - 2 * kMaxStages;
-    mbar_init(bar0 + 8u * threadIdx.x, i >= 0 && i < kScaleSets ? (QUANT ? 5 : 2) : 1);
+    mbar_init(bar0 + 8u * threadIdx.x, i >= 0 && i < kScaleSets ? (QUANT ? 5 : CG == 2 && half == 0 ? 3 : 2) : 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   } else if (threadIdx.x == kThreads - 1) {
     prefetch_map(&map_w0);
@@ -117,12 +136,21 @@ __global__ void __launch_bounds__(kThreads, 2)
     *abort_flag = 0;
   }
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
-                 "n"(kTmemCols));
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    if (CG == 2) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                   "n"(kTmemCols));
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                   "n"(kTmemCols));
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
   }
   tc_fence_before();
-  __syncthreads();
+  if (CG == 2)
+    cluster_sync();  // the other half's barriers are ready
+  else
+    __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   // Not before the tensor memory is ours: a CTA of the next kernel that got it
@@ -135,12 +163,27 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (lane == 0) {
       auto weights = [&](int s, int kb) {
         const uint32_t b = b_base + s * stage;
-        mbar_arrive_expect_tx(full(s), stage);
-        tma_load_2d(b, &map_w0, full(s), (kb0 + kb) * kBlock, col0);
-        if (MODE != kLinear) tma_load_2d(b + cols * kBlock, &map_w1, full(s), (kb0 + kb) * kBlock, col0);
+        const int k = (kb0 + kb) * kBlock;
+        if (CG == 2) {
+          // all of a pair's bytes count in its first CTA
+          if (half == 0) mbar_arrive_expect_tx(full(s), 2 * stage);
+          const uint32_t bar = in_leader(full(s), leader);
+          if (MODE == kLinear)
+            load_tile(b, &map_w0, bar, k, col0 + half * (p.bn / 2));
+          else
+            load_tile(b, half == 0 ? &map_w0 : &map_w1, bar, k, col0);
+        } else {
+          mbar_arrive_expect_tx(full(s), stage);
+          tma_load_2d(b, &map_w0, full(s), k, col0);
+          if (MODE != kLinear) tma_load_2d(b + cols * kBlock, &map_w1, full(s), k, col0);
+        }
       };
       auto tokens = [&](int s, int kb) {
-        if (!QUANT) tma_load_2d(a_base + s * stage, &map_x, full(s), (kb0 + kb) * kBlock, row0);
+        if (QUANT) return;
+        if (CG == 2)
+          load_tile(a_base + s * stage, &map_x, in_leader(full(s), leader), (kb0 + kb) * kBlock, row0);
+        else
+          tma_load_2d(a_base + s * stage, &map_x, full(s), (kb0 + kb) * kBlock, row0);
       };
       // (test only) the first stage left unissued: the MMAs' wait for it gives up
       const int from = p.skip_first_copy ? 1 : 0, ahead = min(S, nkb);
@@ -158,13 +201,29 @@ __global__ void __launch_bounds__(kThreads, 2)
           ph ^= 1u;
         }
       }
-      // every copy has landed before the CTA can leave
-      for (int i = max(from, kb - S); i < kb; ++i) wait_bar_teardown(full(i % S), (i / S) & 1);
+      // every copy has landed before the CTA can leave: a pair's at the first's barriers
+      if (half == 0)
+        for (int i = max(from, kb - S); i < kb; ++i) wait_bar_teardown(full(i % S), (i / S) & 1);
+      if (CG == 2 && (!ok || p.skip_first_copy)) {
+        // of a stage that only one of them issued no barrier tells: copies land
+        // within microseconds
+        const long long t0 = clock64();
+        while (clock64() - t0 < 1000000) {
+        }
+      }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------- MMAs ----
+    if (CG == 2 && half == 1) {
+      // passes on that its scales are there (as in fp8_tc.cu)
+      for (int q = 0; q < nsets && ok; ++q) {
+        if (!(ok = wait.warp(sf_full(q % kScaleSets), (q / kScaleSets) & 1u, kDevErrFullBarrier))) break;
+        if (lane == 0) arrive_cluster(in_leader(sf_full(q % kScaleSets), leader));
+        __syncwarp();
+      }
+    } else {
     const uint32_t on = elect();
-    const uint32_t idesc = (1u << 23) | (static_cast<uint32_t>(p.bn >> 3) << 17) | (8u << 24);
+    const uint32_t idesc = (1u << 23) | (static_cast<uint32_t>(p.bn >> 3) << 17) | (static_cast<uint32_t>(8 * CG) << 24);
     const uint64_t a0 = sw128_desc(a_base), b0 = sw128_desc(b_base);
     int s = 0;
     uint32_t ph = 0, sfa = 0;
@@ -178,9 +237,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (!__all_sync(0xffffffffu, scaled) &&
             !(ok = wait.warp(sf_full(set), (at / kScaleSets) & 1u, kDevErrFullBarrier)))
           break;
-        sfa = tmem + kScaleCol + set * 8;
-        copy_scales<1>(on, sfa, sf + set * kSetBytes);
-        copy_scales<1>(on, sfa + 4, sf + set * kSetBytes + 512);
+        sfa = tmem + kScaleCol + set * Room<CG>::SET_COLS;
+#pragma unroll
+        for (int i = 0; i < 1 + SFB; ++i) copy_scales<CG>(on, sfa + 4 * i, sf + set * kSetBytes + 512 * i);
       }
       if (!__all_sync(0xffffffffu, staged) && !(ok = wait.warp(full(s), ph, kDevErrFullBarrier))) break;
       tc_fence_after();
@@ -195,28 +254,30 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (id == kScaleBlocks - 1) scaled = is_over(sf_full((at + 1) % kScaleSets), ((at + 1) / kScaleSets) & 1u);
 #pragma unroll
       for (int k = 0; k < kBlock / 32; ++k)
-        mma_scaled<1>(on, tmem, a + k * 2, b + k * 2, with_id, sfa, sfa + 4, kb > 0 || k > 0);
-      if (kb + S < nkb) commit<1>(on, freed);  // else it is not filled again
-      if (id == kScaleBlocks - 1 && at + kScaleSets < nsets) commit<1>(on, sf_empty(set));
+        mma_scaled<CG>(on, tmem, a + k * 2, b + k * 2, with_id, sfa, sfa + 4, kb > 0 || k > 0);
+      if (kb + S < nkb) commit<CG>(on, freed, leader);  // else it is not filled again
+      if (id == kScaleBlocks - 1 && at + kScaleSets < nsets) commit<CG>(on, sf_empty(set), leader);
     }
-    if (ok) commit<1>(on, acc_full);
+    if (ok) commit<CG>(on, acc_full, leader);
     // every MMA has landed before tensor memory is freed
-    commit<1>(on, drain);
+    commit<CG>(on, drain, leader);
     wait_bar_teardown(drain, 0);
     __syncwarp();
+    }
   } else if (warp == 3 || (warp == 2 && !QUANT)) {
     // ------------------------------------------------------------ scales ----
     // Set of 128 rows x 4 blocks: row r's word at (r % 32) 16 + (r / 32) 4.  Warp 2
     // gathers the tokens' rows, warp 3 the weights', of which the gate's come
-    // first.
+    // first (a pair's columns from 128 on in a second set).
     const bool mine = warp == 2;  // the tokens' rows
     if (mine) asm volatile("griddepcontrol.wait;" ::: "memory");
     const int all_sets = (p.G + kScaleBlocks - 1) / kScaleBlocks;
-    const uint8_t *at[4], *first[4];
-    int access[4];
-    long bytes[4];
+    constexpr int R = 3 + SFB;  // rows of a lane
+    const uint8_t *at[R], *first[R];
+    int access[R];
+    long bytes[R];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < R; ++i) {
       const int r = lane + 32 * i, which = mine ? 0 : MODE != kLinear && r >= cols ? 2 : 1;
       const int row = mine ? row0 + r : col0 + (which == 2 ? r - cols : r);
       const bool there = row < (mine ? p.M : p.N) && r < (mine ? p.mr : p.bn);
@@ -227,26 +288,27 @@ __global__ void __launch_bounds__(kThreads, 2)
       at[i] = there ? first[i] + static_cast<long>(row) * p.G + set0 * kScaleBlocks : nullptr;
     }
     const int left = all_sets - set0;
-    auto request = [&](uint32_t (&w)[4][kScaleBatch], int q) {
+    auto request = [&](uint32_t (&w)[R][kScaleBatch], int q) {
       if (q >= nsets) return;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < R; ++i)
         fetch_scales(w[i], at[i] == nullptr ? nullptr : at[i] + 4 * q, left - q, access[i], first[i], bytes[i]);
     };
-    auto hand_over = [&](const uint32_t (&w)[4][kScaleBatch], int q) {
+    auto hand_over = [&](const uint32_t (&w)[R][kScaleBatch], int q) {
 #pragma unroll
       for (int j = 0; j < kScaleBatch; ++j) {
         if (q + j >= nsets || !ok) break;
         const int set = (q + j) % kScaleSets;
         if (!(ok = wait.warp(sf_empty(set), (((q + j) / kScaleSets) & 1u) ^ 1u, kDevErrEmptyBarrier))) break;
-        *reinterpret_cast<uint4 *>(sm + kRegion + set * kSetBytes + (mine ? 0 : 512) + lane * 16) =
-            make_uint4(w[0][j], w[1][j], w[2][j], w[3][j]);
+        uint8_t *to = sm + kRegion + set * kSetBytes + (mine ? 0 : 512) + lane * 16;
+        *reinterpret_cast<uint4 *>(to) = make_uint4(w[0][j], w[1][j], w[2][j], w[3][j]);
+        if (R == 5 && !mine) *reinterpret_cast<uint32_t *>(to + 512) = w[R - 1][j];
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(sf_full(set));
       }
     };
-    uint32_t w0[4][kScaleBatch], w1[4][kScaleBatch];
+    uint32_t w0[R][kScaleBatch], w1[R][kScaleBatch];
     request(w0, 0);
     for (int q = 0; q < nsets && ok; q += 2 * kScaleBatch) {
       request(w1, q + kScaleBatch);
@@ -329,21 +391,31 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   __syncwarp();
   tc_fence_before();
-  if (team > 1)
+  const int out_team = p.split * p.nx, out_rank = rank / CG;  // who writes together
+  if (out_team > 1) {
     cluster_sync();
-  else
+  } else {
     __syncthreads();
+    if (CG == 2) {  // both are done with the tensor memory; nothing is handed over
+      asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+      asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    }
+  }
   tc_fence_after();
-  if (warp == 1)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmemCols));
+  if (warp == 1) {
+    if (CG == 2)
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmemCols));
+    else
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmemCols));
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // ------------------------------------------------------------- outputs ----
   {
     const int rows = min(p.mr, p.M - row0), per_tile = cols / 8, per_row = p.nx * per_tile;
     const long group0 = static_cast<long>(blockIdx.x) / team * p.nx * cols;  // first column of the cluster
-    const int items = rows * per_row, stride = team * kThreads, pitch = (p.bn + 4) * 4;
-    int i = rank * kThreads + static_cast<int>(threadIdx.x);
+    const int items = rows * per_row, stride = out_team * kThreads, pitch = (p.bn + 4) * 4;
+    int i = out_rank * kThreads + static_cast<int>(threadIdx.x);
     int row = i / per_row, ch = i - row * per_row;
     const int rows_on = stride / per_row, ch_on = stride - rows_on * per_row;
     // whole warps: the lanes of a group of codes exchange their maxima
@@ -358,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       float v[8], u[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = u[e] = 0.f;
-      if (team == 1) {
+      if (out_team == 1) {
         take(v, reinterpret_cast<const float4 *>(sm + at)[0], reinterpret_cast<const float4 *>(sm + at)[1]);
         if (MODE != kLinear)
           take(u, reinterpret_cast<const float4 *>(sm + at + cols * 4)[0], reinterpret_cast<const float4 *>(sm + at + cols * 4)[1]);
@@ -370,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           for (int e = 0; e < 2; ++e) {
             if (k + e >= p.split) break;
             uint32_t a;
-            asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(base + at), "r"((k + e) * p.nx + x));
+            asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(base + at), "r"(((k + e) * p.nx + x) * CG + half));
             w[e][0] = load_cluster(a);
             w[e][1] = load_cluster(a + 16);
             if (MODE != kLinear) {
@@ -430,26 +502,28 @@ __global__ void __launch_bounds__(kThreads, 2)
 // counts one an SM for a kernel with tcgen05 instructions; two were seen to run).
 constexpr int kResident[9] = {0, 304, 304, 276, 288, 280, 276, 210, 240};
 
-// Microseconds of a call by a model fitted to 6040 timings (1 to 1000 rows, twelve
-// shapes of weights, all tiles and parts): its choice takes on average 1.4 % and at
-// most 15 % longer than the best one.  A CTA takes 77 GB/s, or 0.27 us a K block (one
-// thread issues its MMAs), an SM 137 GB/s; HBM gives 6200 GB/s to all; the epilogue
-// and the joining of parts go with the tile's size.
-float estimate(const Fp8Params &f, int mr, int bn, int split, int nx) {
-  const int blocks = ceil_div(f.G, split), cols = f.w[1] == nullptr ? bn : bn / 2, team = split * nx;
+// Microseconds of a call by a model fitted to 11600 timings (1 to 1000 rows, twelve
+// shapes of weights, all tiles and parts, single CTAs and pairs): its choice takes on
+// average 2 % and at most 27 % longer than the best one.  A CTA takes 77 GB/s, or
+// 0.27 us a K block (one thread issues its MMAs; a pair a little more), an SM 137
+// GB/s; HBM gives 6200 GB/s to all; the epilogue and the joining of parts go with the
+// tile's size.
+float estimate(const Fp8Params &f, int cg, int mr, int bn, int split, int nx) {
+  const int blocks = ceil_div(f.G, split), cols = f.w[1] == nullptr ? bn : bn / 2, team = split * nx * cg;
   const long groups = (static_cast<long>(f.N) + cols * nx - 1) / (cols * nx);
-  const long ctas = groups * team * ceil_div(f.M, 128);
+  const long ctas = groups * team * ceil_div(f.M, 128 * cg);
   const float waves = static_cast<float>((ctas + kResident[team] - 1) / kResident[team]);
-  const float bytes = (mr + bn) * (kBlock * 1e-3f);  // of a stage, in KB
-  const float block = std::max(ctas <= kNumSMsGB300 ? 0.27f : 0.32f, bytes / 77.f);
+  const float bytes = (mr + bn / cg) * (kBlock * 1e-3f);  // of a stage, in KB
+  const float block = std::max((ctas <= kNumSMsGB300 ? 0.27f : 0.32f) * (cg == 2 ? 1.18f : 1.f), bytes / 77.f);
   const float sm = static_cast<float>(ctas) * blocks * bytes / (kNumSMsGB300 * 137.f);
   const float hbm = static_cast<float>(f.N) * (f.w[1] == nullptr ? 1 : 2) * f.G * kBlock / 6.2e6f;
   const float tile = mr * bn / 16384.f;
   const float join = team == 1 ? 0.f : 0.24f + 0.06f * team + 2.2f * (split - 1) * tile;
-  return 2.5f + std::max(std::max(waves * blocks * block, hbm), sm) + (waves - 1.f) * 3.6f + join + 2.2f * waves * tile;
+  return 2.5f + std::max(std::max(waves * blocks * block, hbm), sm) + (waves - 1.f) * 3.6f + join +
+         (cg == 2 ? 2.9f : 2.2f) * waves * tile;
 }
 
-template <int MODE, bool QUANT>
+template <int CG, int MODE, bool QUANT>
 int launch_t(const Fp8Params &f, const Fp8Plan &plan, cudaStream_t s) {
   static bool ready[64] = {};
   static std::mutex mu;
@@ -458,15 +532,16 @@ int launch_t(const Fp8Params &f, const Fp8Plan &plan, cudaStream_t s) {
   {
     std::lock_guard<std::mutex> lock(mu);
     if (!ready[dev]) {
-      if (cudaFuncSetAttribute(fp8_mid_kernel<MODE, QUANT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) !=
+      if (cudaFuncSetAttribute(fp8_mid_kernel<CG, MODE, QUANT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) !=
               cudaSuccess ||
-          cudaFuncSetAttribute(fp8_mid_kernel<MODE, QUANT>, cudaFuncAttributePreferredSharedMemoryCarveout,
+          cudaFuncSetAttribute(fp8_mid_kernel<CG, MODE, QUANT>, cudaFuncAttributePreferredSharedMemoryCarveout,
                                cudaSharedmemCarveoutMaxShared) != cudaSuccess)
         return W8A8_ERR_CUDA;
       ready[dev] = true;
     }
   }
-  const int mt = ceil_div(f.M, plan.mr);
+  const int mt = ceil_div(f.M, plan.mr * CG);
+  constexpr int kRegion = Room<CG>::REGION;
   MidParams p = {};
   p.sx = f.sx;
   p.sw[0] = f.sw[0];
@@ -485,8 +560,8 @@ int launch_t(const Fp8Params &f, const Fp8Plan &plan, cudaStream_t s) {
     p.stages = (kRegion - p.token_bytes) / (p.bn * kBlock);
   } else {
     // the last stage's MMAs read 128 rows from its start
-    const int spare = (128 - p.bn - p.mr) * kBlock;
-    p.stages = (kRegion - (spare > 0 ? spare : 0)) / ((p.mr + p.bn) * kBlock);
+    const int rows = p.mr + p.bn / CG, spare = (128 - rows) * kBlock;
+    p.stages = (kRegion - (spare > 0 ? spare : 0)) / (rows * kBlock);
   }
   if (p.stages > kMaxStages) p.stages = kMaxStages;
   p.access[0] = scale_access(f.sx, f.G);
@@ -500,14 +575,14 @@ int launch_t(const Fp8Params &f, const Fp8Plan &plan, cudaStream_t s) {
   p.wait_limit = role_wait_limit();
   p.skip_first_copy = skip_first_copy();
 
-  const int cols = MODE == kLinear ? p.bn : p.bn / 2, team = p.split * p.nx;
+  const int cols = MODE == kLinear ? p.bn : p.bn / 2, team = p.split * p.nx * CG, wrows = MODE == kLinear ? p.bn / CG : cols;
   const long groups = (static_cast<long>(f.N) + cols * p.nx - 1) / (cols * p.nx);
   if (groups * cols * p.nx > 0x7fffffffL || groups * team > 0x7fffffffL) return W8A8_ERR_INVALID_ARG;
   CUtensorMap mx, mw0, mw1;
-  if (!make_map(&mw0, f.w[0], f.N, f.K, 1, cols)) return W8A8_ERR_CUDA;
+  if (!make_map(&mw0, f.w[0], f.N, f.K, 1, wrows)) return W8A8_ERR_CUDA;
   mx = mw1 = mw0;
   if (!QUANT && !make_map(&mx, f.x, f.M, f.K, 1, p.mr)) return W8A8_ERR_CUDA;
-  if (MODE != kLinear && !make_map(&mw1, f.w[1], f.N, f.K, 1, cols)) return W8A8_ERR_CUDA;
+  if (MODE != kLinear && !make_map(&mw1, f.w[1], f.N, f.K, 1, wrows)) return W8A8_ERR_CUDA;
 
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(groups * team), static_cast<unsigned>(mt));
@@ -523,7 +598,7 @@ int launch_t(const Fp8Params &f, const Fp8Plan &plan, cudaStream_t s) {
   at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = team > 1 ? 2 : 1;
-  if (cudaLaunchKernelEx(&cfg, fp8_mid_kernel<MODE, QUANT>, mx, mw0, mw1, p) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, fp8_mid_kernel<CG, MODE, QUANT>, mx, mw0, mw1, p) != cudaSuccess) {
     cudaGetLastError();
     return W8A8_ERR_CUDA;
   }
@@ -537,11 +612,15 @@ namespace {
 // The best tile for these parts of K.
 Fp8Plan best_tile(const Fp8Params &f, int split) {
   Fp8Plan best = {};
-  const int tiles_m = ceil_div(f.M, 128), mr = (ceil_div(f.M, tiles_m) + 7) & ~7;
   const int nx = f.codes != nullptr ? 2 : 1;
-  for (int bn = nx == 2 ? 128 : f.w[1] == nullptr ? 32 : 48; bn <= 128; bn += 16) {
-    const float t = estimate(f, mr, bn, split, nx);
-    if (best.us == 0.f || t < best.us) best = {mr, bn, split, nx, t};
+  for (int cg = 1; cg <= (f.M > 128 ? 2 : 1); ++cg) {
+    if (split * nx * cg > 8) break;
+    const int tiles_m = ceil_div(f.M, 128 * cg), mr = (ceil_div(f.M, tiles_m * cg) + 7) & ~7;
+    const int most = nx == 2 ? 128 : cg == 2 ? Room<2>::MOST_COLS : Room<1>::MOST_COLS;
+    for (int bn = nx == 2 ? 128 : f.w[1] == nullptr ? 32 : 48; bn <= most; bn += 16) {
+      const float t = estimate(f, cg, mr, bn, split, nx);
+      if (best.us == 0.f || t < best.us) best = {cg, mr, bn, split, nx, t};
+    }
   }
   return best;
 }
@@ -587,9 +666,14 @@ bool fp8_mid_quantizes(const Fp8Params &f, const Fp8Plan &plan) {
 }
 
 int launch_fp8_mid(const Fp8Params &f, const Fp8Plan &plan, cudaStream_t s) {
-  if (f.w[1] == nullptr) return f.xh != nullptr ? launch_t<kLinear, true>(f, plan, s) : launch_t<kLinear, false>(f, plan, s);
-  if (f.codes == nullptr) return launch_t<kGatedHalf, false>(f, plan, s);
-  return f.xh != nullptr ? launch_t<kGatedCodes, true>(f, plan, s) : launch_t<kGatedCodes, false>(f, plan, s);
+  const bool pair = plan.cg == 2;
+  if (f.w[1] == nullptr) {
+    if (f.xh != nullptr) return launch_t<1, kLinear, true>(f, plan, s);
+    return pair ? launch_t<2, kLinear, false>(f, plan, s) : launch_t<1, kLinear, false>(f, plan, s);
+  }
+  if (f.codes == nullptr) return pair ? launch_t<2, kGatedHalf, false>(f, plan, s) : launch_t<1, kGatedHalf, false>(f, plan, s);
+  if (f.xh != nullptr) return launch_t<1, kGatedCodes, true>(f, plan, s);
+  return pair ? launch_t<2, kGatedCodes, false>(f, plan, s) : launch_t<1, kGatedCodes, false>(f, plan, s);
 }
 
 }  // namespace w8a8

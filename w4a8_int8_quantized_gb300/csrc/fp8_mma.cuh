@@ -60,17 +60,43 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
 // All MMAs issued so far arrive on this barrier when they are done, in both
 // CTAs of a pair.
 template <int CG>
-__device__ __forceinline__ void commit(uint32_t on, uint32_t bar) {
+__device__ __forceinline__ void commit(uint32_t on, uint32_t bar, uint32_t leader = 0) {
   if (CG == 2)
     asm volatile(
         "{\n.reg .pred q;\nsetp.ne.b32 q, %2, 0;\n"
         "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], "
-        "%1;\n}\n" ::"r"(bar), "h"(static_cast<uint16_t>(3)), "r"(on) : "memory");
+        "%1;\n}\n" ::"r"(bar), "h"(static_cast<uint16_t>(3u << leader)), "r"(on) : "memory");
   else
     asm volatile("{\n.reg .pred q;\nsetp.ne.b32 q, %1, 0;\n"
                  "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar),
                  "r"(on)
                  : "memory");
+}
+
+// this address in the pair's first CTA (by its rank in the cluster)
+__device__ __forceinline__ uint32_t in_leader(uint32_t addr, uint32_t leader = 0) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(leader));
+  return r;
+}
+
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// The same for reads of tensor memory that have completed (tcgen05.wait::ld and
+// the fence before it order them): nothing else to release.
+__device__ __forceinline__ void arrive_read(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// A tile whose bytes count at a barrier of the pair's first CTA
+__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+      : "memory");
 }
 
 __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
