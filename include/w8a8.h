@@ -421,7 +421,7 @@ int rms_norm_quantize(const w8a8_half *x, const w8a8_half *residual, const w8a8_
  * 16, code pointers 16-byte aligned and scale pointers at any address.  Sums
  * are fp32 (the products of two codes are exact), rounded once to the output's
  * type.  Their order depends on N, K and the class of M (up to 16, 64, 128, 384,
- * 1024 rows, more), not on timing: within a class a row's result does not depend
+ * 1024, 2560, 8192 rows, more), not on timing: within a class a row's result does not depend
  * on the other rows of the batch.  No output may overlap an input. */
 
 /* fp16 rows to codes and scales.

@@ -63,8 +63,8 @@ Fp8Params product(const uint8_t *x, const uint8_t *sx, const uint8_t *w, const u
 // The product of p.x, p.sx, or of fp16 rows x: quantized into the room at p.x, p.sx
 // before it, or, if they are few, by the product itself.
 int launch_product(Fp8Params &p, cudaStream_t s, const __half *x = nullptr) {
-  // the small tiles are for a few hundred rows: 2048 are never theirs
-  bool small = p.M <= 2048;
+  // the small tiles are for a few hundred rows, or for few columns
+  bool small = p.M <= 8192;
   Fp8Plan plan = {};
   if (small) {
     plan = plan_fp8_mid(p);

@@ -103,14 +103,14 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int S = p.stages, a_bytes = p.mr * kBlock, stage = (QUANT ? 0 : a_bytes) + p.bn / CG * kBlock;
   const int cols = MODE == kLinear ? p.bn : p.bn / 2;
   // a cluster: parts of K, each of nx tiles, each of one CTA or a pair
-  const int team = p.split * p.nx * CG, rank = static_cast<int>(blockIdx.x) % team;
+  // (32-bit divisions: 64-bit ones took a third of the start)
+  const int team = p.split * p.nx * CG, cluster = static_cast<int>(blockIdx.x / static_cast<unsigned>(team));
+  const int rank = static_cast<int>(blockIdx.x) - cluster * team;
   const int half = CG == 2 ? rank & 1 : 0, leader = rank - half;
-  const int part = rank / (p.nx * CG), xi = rank / CG - part * p.nx;
-  const long tile_n = static_cast<long>(blockIdx.x) / team * p.nx + xi;
-  const int col0 = static_cast<int>(tile_n * cols), row0 = (static_cast<int>(blockIdx.y) * CG + half) * p.mr;
+  const int part = rank / (p.nx * CG), xi = rank / CG - part * p.nx, tile_n = cluster * p.nx + xi;
+  const int col0 = tile_n * cols, row0 = (static_cast<int>(blockIdx.y) * CG + half) * p.mr;
   // K blocks of this part; its sets of scales are those of the whole row
-  const int kb0 = static_cast<int>(static_cast<long>(p.G) * part / p.split);
-  const int nkb = static_cast<int>(static_cast<long>(p.G) * (part + 1) / p.split) - kb0;
+  const int kb0 = p.G * part / p.split, nkb = p.G * (part + 1) / p.split - kb0;
   const int set0 = kb0 / kScaleBlocks, nsets = (kb0 + nkb + kScaleBlocks - 1) / kScaleBlocks - set0;
   const uint32_t a_base = base, b_base = base + (QUANT ? p.token_bytes : a_bytes);
 
@@ -373,10 +373,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int row = (warp & 3) * 32 + lane;
       const uint32_t from = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
       float *to = reinterpret_cast<float *>(sm) + row * (p.bn + 4);
-      for (int c = 0; c < p.bn; c += 32) {
-        uint32_t v[32];
-        tmem_ld32(from + c, v);  // behind bn: columns of this CTA's own tensor memory, not kept
-        tmem_wait_ld32(v);
+      // behind bn: columns of this CTA's own tensor memory, not kept
+      auto keep = [&](const uint32_t (&v)[32], int c) {
         if (row < p.mr) {
 #pragma unroll
           for (int e = 0; e < 8; ++e)
@@ -384,6 +382,15 @@ __global__ void __launch_bounds__(kThreads, 2)
               *reinterpret_cast<uint4 *>(to + c + 4 * e) = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
         }
         __syncwarp();
+      };
+      for (int c = 0; c < p.bn; c += 64) {
+        uint32_t v[32], w[32];
+        tmem_ld32(from + c, v);
+        if (c + 32 < p.bn) tmem_ld32(from + c + 32, w);
+        tmem_wait_ld32(v);
+        tmem_wait_ld32(w);
+        keep(v, c);
+        if (c + 32 < p.bn) keep(w, c + 32);
       }
       tc_fence_before();
     }
@@ -413,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   // ------------------------------------------------------------- outputs ----
   {
     const int rows = min(p.mr, p.M - row0), per_tile = cols / 8, per_row = p.nx * per_tile;
-    const long group0 = static_cast<long>(blockIdx.x) / team * p.nx * cols;  // first column of the cluster
+    const int group0 = cluster * p.nx * cols;  // first column of the cluster
     const int items = rows * per_row, stride = out_team * kThreads, pitch = (p.bn + 4) * 4;
     int i = out_rank * kThreads + static_cast<int>(threadIdx.x);
     int row = i / per_row, ch = i - row * per_row;
@@ -477,14 +484,28 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (ch == 0) p.scales[m * ((p.N + 127) >> 7) + (n >> 7)] = static_cast<uint8_t>(byte);
         }
       } else if (in && n < p.N) {
+        // as wide as the address allows: rows may start at any half
         __half *to = p.y + m * p.N + n;
-        if ((p.N & 7) == 0) {
-          *reinterpret_cast<uint4 *>(to) = make_uint4(half2_bits(v[0], v[1]), half2_bits(v[2], v[3]),
-                                                      half2_bits(v[4], v[5]), half2_bits(v[6], v[7]));
-        } else {
+        const uint32_t w[4] = {half2_bits(v[0], v[1]), half2_bits(v[2], v[3]), half2_bits(v[4], v[5]), half2_bits(v[6], v[7])};
+        const uint32_t low = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(to)) & 15u;
+        if (n + 8 > p.N) {
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             if (n + e < p.N) to[e] = __float2half_rn(v[e]);
+        } else if (low == 0) {
+          *reinterpret_cast<uint4 *>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else if ((low & 7u) == 0) {
+          reinterpret_cast<uint2 *>(to)[0] = make_uint2(w[0], w[1]);
+          reinterpret_cast<uint2 *>(to)[1] = make_uint2(w[2], w[3]);
+        } else if ((low & 3u) == 0) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) reinterpret_cast<uint32_t *>(to)[e] = w[e];
+        } else {
+          to[0] = __float2half_rn(v[0]);
+#pragma unroll
+          for (int e = 0; e < 3; ++e)
+            *reinterpret_cast<uint32_t *>(to + 1 + 2 * e) = __funnelshift_r(w[e], w[e + 1], 16);
+          to[7] = __float2half_rn(v[7]);
         }
       }
     }
@@ -631,8 +652,8 @@ Fp8Plan find_plan(const Fp8Params &f) {
   // suit the class's largest (2 % slower on average than each batch's own, at most
   // 25 %).  Undivided, both kernels give the same sums.
   Fp8Params typical = f;
-  typical.M = f.M <= 16 ? 16 : f.M <= 64 ? 64 : f.M <= 128 ? 128 : f.M <= 384 ? 384 : 1024;
-  const int most = f.M > 1024 ? 1 : std::min(f.codes != nullptr ? 4 : 8, f.G);
+  typical.M = f.M <= 16 ? 16 : f.M <= 64 ? 64 : f.M <= 128 ? 128 : f.M <= 384 ? 384 : f.M <= 1024 ? 1024 : f.M <= 2560 ? 2560 : 8192;
+  const int most = f.M > 8192 ? 1 : std::min(f.codes != nullptr ? 4 : 8, f.G);
   Fp8Plan best = {};
   if (typical.M > 128) best.us = estimate_fp8_tc(typical), best.split = 1;
   for (int split = 1; split <= most; ++split) {
