@@ -288,27 +288,27 @@ __global__ void __launch_bounds__(kThreads, 2)
       at[i] = there ? first[i] + static_cast<long>(row) * p.G + set0 * kScaleBlocks : nullptr;
     }
     const int left = all_sets - set0;
-    auto request = [&](uint32_t (&w)[R][kScaleBatch], int q) {
+    auto request = [&](ScaleRow (&w)[R], int q) {
       if (q >= nsets) return;
 #pragma unroll
       for (int i = 0; i < R; ++i)
-        fetch_scales(w[i], at[i] == nullptr ? nullptr : at[i] + 4 * q, left - q, access[i], first[i], bytes[i]);
+        w[i].request(at[i] == nullptr ? nullptr : at[i] + 4 * q, left - q, access[i], first[i], bytes[i]);
     };
-    auto hand_over = [&](const uint32_t (&w)[R][kScaleBatch], int q) {
+    auto hand_over = [&](const ScaleRow (&w)[R], int q) {
 #pragma unroll
       for (int j = 0; j < kScaleBatch; ++j) {
         if (q + j >= nsets || !ok) break;
         const int set = (q + j) % kScaleSets;
         if (!(ok = wait.warp(sf_empty(set), (((q + j) / kScaleSets) & 1u) ^ 1u, kDevErrEmptyBarrier))) break;
         uint8_t *to = sm + kRegion + set * kSetBytes + (mine ? 0 : 512) + lane * 16;
-        *reinterpret_cast<uint4 *>(to) = make_uint4(w[0][j], w[1][j], w[2][j], w[3][j]);
-        if (R == 5 && !mine) *reinterpret_cast<uint32_t *>(to + 512) = w[R - 1][j];
+        *reinterpret_cast<uint4 *>(to) = make_uint4(w[0].get(j), w[1].get(j), w[2].get(j), w[3].get(j));
+        if (R == 5 && !mine) *reinterpret_cast<uint32_t *>(to + 512) = w[R - 1].get(j);
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(sf_full(set));
       }
     };
-    uint32_t w0[R][kScaleBatch], w1[R][kScaleBatch];
+    ScaleRow w0[R], w1[R];
     request(w0, 0);
     for (int q = 0; q < nsets && ok; q += 2 * kScaleBatch) {
       request(w1, q + kScaleBatch);

@@ -177,37 +177,43 @@ __device__ __forceinline__ uint32_t word_within(uintptr_t at, uintptr_t first, u
   return w;
 }
 
-// Words q .. q + 3 of a row of scales that start at `at` (nullptr: no such row,
-// 1.0), as far as the row has them (`left` words).  `access`: see scale_access();
-// all rows are [first, first + bytes).  Behind a row's last byte come the next
-// row's, which no MMA uses.
-__device__ __forceinline__ void fetch_scales(uint32_t (&w)[kScaleBatch], const uint8_t *at, int left, int access,
-                                             const uint8_t *first, long bytes) {
-  if (at == nullptr) {
+// Four words of a row of scales, requested and taken apart, so that the loads can
+// be under way.  Rows may start at any address: five words around them, shifted.
+struct ScaleRow {
+  uint32_t w[kScaleBatch + 1], shift;
+  // from `at` (nullptr: no such row, 1.0), as far as the row has them (`left`
+  // words).  `access`: see scale_access(); all rows are [first, first + bytes).
+  // Behind a row's last byte come the next row's, which no MMA uses.
+  __device__ __forceinline__ void request(const uint8_t *at, int left, int access, const uint8_t *first, long bytes) {
+    shift = 0;
+    if (at == nullptr) {
 #pragma unroll
-    for (int j = 0; j < kScaleBatch; ++j) w[j] = 0x7f7f7f7fu;
-  } else if (access == 16 && left >= kScaleBatch) {
-    const uint4 v = *reinterpret_cast<const uint4 *>(at);
-    w[0] = v.x;
-    w[1] = v.y;
-    w[2] = v.z;
-    w[3] = v.w;
-  } else if (access >= 4) {
+      for (int j = 0; j <= kScaleBatch; ++j) w[j] = 0x7f7f7f7fu;
+    } else if (access == 16 && left >= kScaleBatch) {
+      const uint4 v = *reinterpret_cast<const uint4 *>(at);
+      w[0] = v.x;
+      w[1] = v.y;
+      w[2] = v.z;
+      w[3] = v.w;
+    } else if (access >= 4) {
 #pragma unroll
-    for (int j = 0; j < kScaleBatch; ++j)
-      if (j < left) w[j] = *reinterpret_cast<const uint32_t *>(at + 4 * j);
-  } else {
-    // any address: the words around it, shifted
-    const uintptr_t a = reinterpret_cast<uintptr_t>(at), lo = reinterpret_cast<uintptr_t>(first), end = lo + bytes;
-    const uintptr_t word = a & ~static_cast<uintptr_t>(3);
-    const uint32_t shift = (static_cast<uint32_t>(a) & 3u) * 8u;
-    uint32_t v[kScaleBatch + 1];
+      for (int j = 0; j < kScaleBatch; ++j)
+        if (j < left) w[j] = *reinterpret_cast<const uint32_t *>(at + 4 * j);
+    } else {
+      const uintptr_t a = reinterpret_cast<uintptr_t>(at), lo = reinterpret_cast<uintptr_t>(first), end = lo + bytes;
+      const uintptr_t word = a & ~static_cast<uintptr_t>(3);
+      shift = (static_cast<uint32_t>(a) & 3u) * 8u;
+      if (word >= lo && word + 4 * (kScaleBatch + 1) <= end) {
 #pragma unroll
-    for (int j = 0; j <= kScaleBatch; ++j) v[j] = j <= left ? word_within(word + 4 * j, lo, end) : 0x7f7f7f7fu;
+        for (int j = 0; j <= kScaleBatch; ++j) w[j] = *reinterpret_cast<const uint32_t *>(word + 4 * j);
+      } else {
 #pragma unroll
-    for (int j = 0; j < kScaleBatch; ++j) w[j] = __funnelshift_r(v[j], v[j + 1], shift);
+        for (int j = 0; j <= kScaleBatch; ++j) w[j] = j <= left ? word_within(word + 4 * j, lo, end) : 0x7f7f7f7fu;
+      }
+    }
   }
-}
+  __device__ __forceinline__ uint32_t get(int j) const { return __funnelshift_r(w[j], w[j + 1], shift); }
+};
 
 // Bytes that a load of rows of G scales may take at once: 16, 4 or 1.
 inline int scale_access(const uint8_t *at, int G) {

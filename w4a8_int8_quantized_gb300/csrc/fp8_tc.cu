@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint8_t *const from[2] = {warp == 2 ? p.sx : p.sw[0], MODE == kLinear ? p.sw[0] : p.sw[1]};
     const int rows[2] = {warp == 2 ? p.M : p.N, p.N};
     const int access[2] = {warp == 2 ? p.access[0] : p.access[1], MODE == kLinear ? p.access[1] : p.access[2]};
-    typedef uint32_t Batch[PARTS][4][BATCH];
+    typedef ScaleRow Batch[PARTS][4];
     int nt = first, nq = 0;  // the next batch to request
     auto request = [&](Batch &w) {
       if (nt >= p.ntiles) return;
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 4; ++i) {
           const int r = r0[e] + 32 * i;
           const uint8_t *at = r < rows[e] ? from[e] + static_cast<long>(r) * p.G + 4 * nq : nullptr;
-          fetch_scales(w[e][i], at, nsets - nq, access[e], from[e], static_cast<long>(rows[e]) * p.G);
+          w[e][i].request(at, nsets - nq, access[e], from[e], static_cast<long>(rows[e]) * p.G);
         }
       }
       if ((nq += BATCH) >= nsets) {
@@ -360,10 +360,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int set = sets % kScaleSets;
         if (!(ok = wait.warp(sf_empty(set), ((sets / kScaleSets) & 1u) ^ 1u, kDevErrEmptyBarrier))) break;
         uint8_t *to = sm + kOffScales + set * kSetBytes + lane * 16;
-        *reinterpret_cast<uint4 *>(to + (warp == 2 ? 0 : 512)) = make_uint4(w[0][0][j], w[0][1][j], w[0][2][j], w[0][3][j]);
+        *reinterpret_cast<uint4 *>(to + (warp == 2 ? 0 : 512)) = make_uint4(w[0][0].get(j), w[0][1].get(j), w[0][2].get(j), w[0][3].get(j));
         if (two)
           *reinterpret_cast<uint4 *>(to + 1024) =
-              make_uint4(w[PARTS - 1][0][j], w[PARTS - 1][1][j], w[PARTS - 1][2][j], w[PARTS - 1][3][j]);
+              make_uint4(w[PARTS - 1][0].get(j), w[PARTS - 1][1].get(j), w[PARTS - 1][2].get(j), w[PARTS - 1][3].get(j));
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(sf_full(set));
