@@ -43,14 +43,28 @@ __device__ __forceinline__ uint32_t fp8_pack4(float a, float b, float c, float d
 
 // act(g) u, with act(g) = g / (1 + exp(-t)): t = g is SiLU; t = 2 sqrt(2 / pi)
 // (g + 0.044715 g^3) is GELU in its tanh form, since (1 + tanh z) / 2 = 1 / (1 +
-// exp(-2 z)).  exp and the quotient are the approximate ones (a few 2^-22
+// exp(-2 z)).  exp and the reciprocal are the approximate ones (a few 2^-22
 // relative for |t| below 16, and where |t| is larger the exponential hardly
 // counts or the value is below 1e-6 of g): far inside one rounding to fp16 or
 // e4m3, which follows.  exp(-t) = inf gives 0.
 template <bool GELU>
 __device__ __forceinline__ float gated(float g, float u) {
   const float t = GELU ? 1.5957691216057308f * fmaf(0.044715f * g * g, g, g) : g;
-  return __fdividef(g, 1.f + __expf(-t)) * u;
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-t)));
+  return g * r * u;
+}
+
+// The same for N pairs; which function is decided once.
+template <int N>
+__device__ __forceinline__ void gate_all(bool gelu, const float (&g)[N], const float (&u)[N], float (&h)[N]) {
+  if (gelu) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) h[e] = gated<true>(g[e], u[e]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; ++e) h[e] = gated<false>(g[e], u[e]);
+  }
 }
 
 }  // namespace w8a8

@@ -466,8 +466,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       }
       if (MODE != kLinear) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = p.gelu ? gated<true>(v[e], u[e]) : gated<false>(v[e], u[e]);
+        gate_all<8>(p.gelu, v, u, v);
       }
       const long m = row0 + row, n = group0 + ch * 8;
       if (MODE == kGatedCodes) {

@@ -44,7 +44,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kRows = 128;      // tokens of a CTA's part of a tile
-constexpr int kScaleSets = 4;   // sets in shared memory (two of them in tensor memory)
+constexpr int kScaleSets = 8;   // sets in shared memory (two of them in tensor memory)
+constexpr int kScaleLag = 4;    // sets whose copies are under way
 
 enum Mode { kLinear = 0, kGatedHalf = 1, kGatedCodes = 2 };
 
@@ -52,10 +53,10 @@ constexpr int kCols = 256;      // columns of a tile's accumulator
 constexpr int kTileRows = 2 * kRows;
 constexpr int kTileBytes = kRows * kBlock;  // what a CTA fetches of either operand: 128 rows
 constexpr int kStage = 2 * kTileBytes;
-constexpr int kStages = 6;
+constexpr int kStages = 5;
 constexpr int kSetBytes = 3 * 512;          // scales of 128 tokens and of 256 columns
-constexpr int kOffOut = kStages * kStage;   // 4 warps x 32 rows x 128 bytes
-constexpr int kOffScales = kOffOut + 4 * 4096;
+constexpr int kOffOut = kStages * kStage;   // 4 warps x 2 x 32 rows x 128 bytes
+constexpr int kOffScales = kOffOut + 4 * 8192;
 constexpr int kOffBars = kOffScales + kScaleSets * kSetBytes;
 constexpr int kBars = 2 * (kStages + kScaleSets) + 2 + 1 + 1;
 constexpr int kSmemBytes = kOffBars + kBars * 8 + 16 + 1024;  // + alignment by hand
@@ -85,9 +86,11 @@ __device__ __forceinline__ void store_tile(const CUtensorMap *map, uint32_t src,
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 
-// The shared memory that this thread's stores read may be written again.
+// The shared memory that this thread's stores but the last MOST read may be
+// written again.
+template <int MOST>
 __device__ __forceinline__ void stores_read() {
-  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(MOST) : "memory");
 }
 
 struct Tile {
@@ -320,75 +323,134 @@ __global__ void __launch_bounds__(kThreads, 1)
     // lane l gathers rows l, l + 32, l + 64, l + 96.  Warp 2 takes the tokens'
     // set and the second set of weights, warp 3 the first one.
     //
-    // A load queues behind the stages that this SM has requested, up to 192 KB,
-    // and touches 32 lines, of which few fit beside the stages: so up to four
-    // sets of a tile are requested at once (a line is fetched once for them),
-    // a batch ahead.  What does not exist is 1.0; behind a row's last block
-    // comes the next row's, which no MMA uses.
+    // What is requested queues behind the stages that this SM has requested, up to
+    // 160 KB.  So rows of whole words go by asynchronous copies, four sets ahead
+    // (4000 x 8192 x 512: 20 us, 3000 x 4096 x 2048: 21.6; by registers, a batch of up
+    // to four sets of a tile ahead, 28.5 and 24.5, and no better two batches ahead).
+    // Rows at any address go by registers.  What does not exist is 1.0; behind a
+    // row's last block comes the next row's, which no MMA uses.
     constexpr int BATCH = kScaleBatch, PARTS = 2;
     const bool two = warp == 2;
     const uint8_t *const from[2] = {warp == 2 ? p.sx : p.sw[0], MODE == kLinear ? p.sw[0] : p.sw[1]};
     const int rows[2] = {warp == 2 ? p.M : p.N, p.N};
     const int access[2] = {warp == 2 ? p.access[0] : p.access[1], MODE == kLinear ? p.access[1] : p.access[2]};
-    typedef ScaleRow Batch[PARTS][4];
-    int nt = first, nq = 0;  // the next batch to request
-    auto request = [&](Batch &w) {
-      if (nt >= p.ntiles) return;
-      const Tile tl = tile_at(p, nt);
-      const int col = tl.n * COLS, row = tl.m * (kTileRows) + static_cast<int>(rank) * kRows;
-      const int r0[2] = {lane + (warp == 2 ? row : col), lane + (MODE == kLinear ? col + 128 : col)};
-#pragma unroll
-      for (int e = 0; e < PARTS; ++e) {
-        if (e == 1 && !two) continue;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = r0[e] + 32 * i;
-          const uint8_t *at = r < rows[e] ? from[e] + static_cast<long>(r) * p.G + 4 * nq : nullptr;
-          w[e][i].request(at, nsets - nq, access[e], from[e], static_cast<long>(rows[e]) * p.G);
-        }
-      }
-      if ((nq += BATCH) >= nsets) {
-        nq = 0;
-        nt += step;
-      }
-    };
-    int sets = 0;
-    auto hand_over = [&](const Batch &w, int count) {
-#pragma unroll
-      for (int j = 0; j < BATCH; ++j) {
-        if (j >= count || !ok) break;
-        const int set = sets % kScaleSets;
-        if (!(ok = wait.warp(sf_empty(set), ((sets / kScaleSets) & 1u) ^ 1u, kDevErrEmptyBarrier))) break;
-        uint8_t *to = sm + kOffScales + set * kSetBytes + lane * 16;
-        *reinterpret_cast<uint4 *>(to + (warp == 2 ? 0 : 512)) = make_uint4(w[0][0].get(j), w[0][1].get(j), w[0][2].get(j), w[0][3].get(j));
-        if (two)
-          *reinterpret_cast<uint4 *>(to + 1024) =
-              make_uint4(w[PARTS - 1][0].get(j), w[PARTS - 1][1].get(j), w[PARTS - 1][2].get(j), w[PARTS - 1][3].get(j));
+    if (access[0] >= 4 && (!two || access[1] >= 4)) {
+      int sets = 0;
+      auto hand_over = [&](int n) {
         fence_proxy_async();
         __syncwarp();
-        if (lane == 0) mbar_arrive(sf_full(set));
-        ++sets;
+        if (lane == 0) mbar_arrive(sf_full(n % kScaleSets));
+      };
+      for (int t = first; t < p.ntiles && ok; t += step) {
+        const Tile tl = tile_at(p, t);
+        const int col = tl.n * COLS, row = tl.m * kTileRows + static_cast<int>(rank) * kRows;
+        const int r0[2] = {lane + (warp == 2 ? row : col), lane + (MODE == kLinear ? col + 128 : col)};
+        const uint8_t *at[PARTS][4];
+#pragma unroll
+        for (int e = 0; e < PARTS; ++e)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = r0[e] + 32 * i;
+            at[e][i] = (e == 0 || two) && r < rows[e] ? from[e] + static_cast<long>(r) * p.G : nullptr;
+          }
+        for (int q = 0; q < nsets; ++q, ++sets) {
+          const int set = sets % kScaleSets;
+          if (!(ok = wait.warp(sf_empty(set), ((sets / kScaleSets) & 1u) ^ 1u, kDevErrEmptyBarrier))) break;
+          uint8_t *to = sm + kOffScales + set * kSetBytes + lane * 16;
+#pragma unroll
+          for (int e = 0; e < PARTS; ++e) {
+            if (e == 1 && !two) continue;
+            uint8_t *const place = to + (e == 1 ? 1024 : warp == 2 ? 0 : 512);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (at[e][i] != nullptr)
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(place + 4 * i)),
+                             "l"(at[e][i] + 4 * q)
+                             : "memory");
+              else
+                *reinterpret_cast<uint32_t *>(place + 4 * i) = 0x7f7f7f7fu;
+            }
+          }
+          asm volatile("cp.async.commit_group;" ::: "memory");
+          if (sets >= kScaleLag) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kScaleLag) : "memory");
+            hand_over(sets - kScaleLag);
+          }
+        }
       }
-    };
-    Batch w0, w1;
-    request(w0);
-    for (int t = first, q = 0; t < p.ntiles && ok;) {
-      auto turn = [&](Batch &now, Batch &next) {
-        request(next);
-        hand_over(now, min(BATCH, nsets - q));
-        if ((q += BATCH) >= nsets) {
-          q = 0;
-          t += step;
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      if (ok)
+        for (int n = max(0, sets - kScaleLag); n < sets; ++n) hand_over(n);
+    } else {
+      typedef ScaleRow Batch[PARTS][4];
+      int nt = first, nq = 0;  // the next batch to request
+      auto request = [&](Batch &w) {
+        if (nt >= p.ntiles) return;
+        const Tile tl = tile_at(p, nt);
+        const int col = tl.n * COLS, row = tl.m * (kTileRows) + static_cast<int>(rank) * kRows;
+        const int r0[2] = {lane + (warp == 2 ? row : col), lane + (MODE == kLinear ? col + 128 : col)};
+#pragma unroll
+        for (int e = 0; e < PARTS; ++e) {
+          if (e == 1 && !two) continue;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = r0[e] + 32 * i;
+            const uint8_t *at = r < rows[e] ? from[e] + static_cast<long>(r) * p.G + 4 * nq : nullptr;
+            w[e][i].request(at, nsets - nq, access[e], from[e], static_cast<long>(rows[e]) * p.G);
+          }
+        }
+        if ((nq += BATCH) >= nsets) {
+          nq = 0;
+          nt += step;
         }
       };
-      turn(w0, w1);
-      if (t >= p.ntiles || !ok) break;
-      turn(w1, w0);
+      int sets = 0;
+      auto hand_over = [&](const Batch &w, int count) {
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) {
+          if (j >= count || !ok) break;
+          const int set = sets % kScaleSets;
+          if (!(ok = wait.warp(sf_empty(set), ((sets / kScaleSets) & 1u) ^ 1u, kDevErrEmptyBarrier))) break;
+          uint8_t *to = sm + kOffScales + set * kSetBytes + lane * 16;
+          *reinterpret_cast<uint4 *>(to + (warp == 2 ? 0 : 512)) = make_uint4(w[0][0].get(j), w[0][1].get(j), w[0][2].get(j), w[0][3].get(j));
+          if (two)
+            *reinterpret_cast<uint4 *>(to + 1024) =
+                make_uint4(w[PARTS - 1][0].get(j), w[PARTS - 1][1].get(j), w[PARTS - 1][2].get(j), w[PARTS - 1][3].get(j));
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(sf_full(set));
+          ++sets;
+        }
+      };
+      Batch w0, w1;
+      request(w0);
+      for (int t = first, q = 0; t < p.ntiles && ok;) {
+        auto turn = [&](Batch &now, Batch &next) {
+          request(next);
+          hand_over(now, min(BATCH, nsets - q));
+          if ((q += BATCH) >= nsets) {
+            q = 0;
+            t += step;
+          }
+        };
+        turn(w0, w1);
+        if (t >= p.ntiles || !ok) break;
+        turn(w1, w0);
+      }
     }
   } else {
     // ---------------------------------------------------------- epilogue ----
     const int q = warp & 3;
-    uint8_t *buf = sm + kOffOut + q * 4096, *mine = buf + lane * 128;
+    // two buffers in turn: a store reads its own for several hundred cycles
+    uint8_t *buf = sm + kOffOut + q * 8192, *mine = buf + lane * 128;
+    int turn = 0;
+    auto next_buffer = [&]() {
+      if (lane == 0) stores_read<1>();
+      __syncwarp();
+      turn ^= 1;
+      buf = sm + kOffOut + q * 8192 + turn * 4096;
+      mine = buf + lane * 128;
+    };
     const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
     auto put = [&](int chunk, uint4 v) {
       *reinterpret_cast<uint4 *>(mine + ((chunk ^ (lane & 7)) << 4)) = v;
@@ -421,8 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_wait_ld32(v);
           tmem_wait_ld32(w);
           if (i == 0) release();
-          if (lane == 0) stores_read();
-          __syncwarp();
+          next_buffer();
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             auto f = [](uint32_t x) { return __uint_as_float(x); };
@@ -448,18 +509,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_wait_ld32(g);
           tmem_wait_ld32(u);
           if (i == 0) release();
+          float a[32], b[32], o[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            a[e] = __uint_as_float(g[e]);
+            b[e] = __uint_as_float(u[e]);
+          }
+          gate_all<32>(p.gelu, a, b, o);
           float *hi = h + (MODE == kGatedCodes ? 32 * i : 0);
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
-            const float a = __uint_as_float(g[e]), b = __uint_as_float(u[e]);
-            hi[e] = p.gelu ? gated<true>(a, b) : gated<false>(a, b);
-            if (MODE == kGatedCodes) top = fmaxf(top, fabsf(hi[e]));
+            hi[e] = o[e];
+            if (MODE == kGatedCodes) top = fmaxf(top, fabsf(o[e]));
           }
           if (MODE == kGatedHalf) {
-            if ((i & 1) == 0) {
-              if (lane == 0) stores_read();
-              __syncwarp();
-            }
+            if ((i & 1) == 0) next_buffer();
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               put(4 * (c & 1) + e,
@@ -476,8 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float m = fp8_scale_inverse(byte);
           if (row0 + lane < p.M)
             p.scales[(row0 + lane) * fp8_groups_of(p.N) + tl.n] = static_cast<uint8_t>(byte);
-          if (lane == 0) stores_read();
-          __syncwarp();
+          next_buffer();
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int c = r == 0 ? 3 - i : i;
@@ -501,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    if (lane == 0) stores_read();
+    if (lane == 0) stores_read<0>();
     tc_fence_before();
   }
 
