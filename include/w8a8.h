@@ -139,9 +139,14 @@ int w8a8_gemm(const int8_t *xq, const float *scale_a, const int8_t *Wq,
  * Ordering: the matrix-vector kernel is launched with programmatic stream
  * serialization, and it may start reading Wq (only Wq) before the previous
  * kernel on the stream has finished when that kernel lets its dependents
- * start early (executes griddepcontrol.launch_dependents).  Do not write Wq
- * in such a kernel right before this call; the library's own kernels that
- * write weights never let dependents start early.  The same holds for
+ * start early (executes griddepcontrol.launch_dependents).  A kernel that does
+ * so, and every kernel behind it that does so too, may still be running then.
+ * So do not write Wq in such a kernel of your own, unless one that does not
+ * (or an event, a copy, a synchronisation) lies between it and this call.
+ * Every entry point of this library that gives codes in a weight's format
+ * (INT8, packed INT4, e4m3), of weights or of activations, writes them without
+ * letting dependents start early: they may be the Wq of any later call on the
+ * stream.  The same holds for
  * w4a8_gemm and linear with M == 1. */
 int w8a8_mv(const int8_t *xq, const float *scale_a, const int8_t *Wq,
             const float *scale_w, int M, int N, int K, int group_size,
@@ -381,7 +386,9 @@ int kv_cache_attention(const w8a8_half *q, long long q_token_stride, long long q
  *   eps          >= 0, finite
  *   residual_out fp16 [M, K] (out) h; may be residual or x itself; NULL if
  *                and only if residual is NULL
- * Other overlaps of an output with an input are not allowed. */
+ * Other overlaps of an output with an input are not allowed.
+ * Ordering: with fp16 outputs (values, or codes as halves) the kernel lets the
+ * next kernel on the stream start early, as quantize_act_per_token_h does. */
 
 /* Code formats of rms_norm_quantize(). */
 #define W8A8_CODES_INT8 0 /* int8, scales as quantize_act_per_token */
@@ -438,7 +445,9 @@ int quantize_weight_fp8(const w8a8_half *W, int N, int K, uint8_t *Wq, uint8_t *
  *   [N, ceil(K/128)]; y fp16 [M, N] (out)
  * All products here are launched with programmatic stream serialization, and
  * may read the weights (only these and their scales) before the previous kernel
- * on the stream has finished: see w8a8_mv. */
+ * on the stream has finished, under the rule of w8a8_mv: codes that any entry
+ * point of this library wrote earlier on the stream may be the weights, so
+ * products of two activations need nothing more. */
 int fp8_gemm(const uint8_t *xq, const uint8_t *scale_a, const uint8_t *Wq, const uint8_t *scale_w,
              int M, int N, int K, w8a8_half *y, w8a8_stream_t stream);
 

@@ -719,7 +719,9 @@ def quantize_weight_fp8(W: torch.Tensor, Wq=None, scale_w=None):
 
 
 def fp8_gemm(xq, scale_a, Wq, scale_w, y=None):
-    """Product of 8-bit float rows: xq [M, K] x Wq [N, K]^T -> fp16 y [M, N]."""
+    """Product of 8-bit float rows: xq [M, K] x Wq [N, K]^T -> fp16 y [M, N].  Wq may
+    be codes of quantize_weight_fp8() or, for a product of two activations, of any
+    other call of this library before it on the stream."""
     M, K = _held(xq, scale_a, "xq")
     device = xq.device
     N, _ = _held(Wq, scale_w, "Wq", device, K)

@@ -57,6 +57,7 @@ Fp8Params product(const uint8_t *x, const uint8_t *sx, const uint8_t *w, const u
   p.N = N;
   p.K = K;
   p.G = fp8_groups_of(K);
+  p.early = true;
   return p;
 }
 
@@ -74,7 +75,7 @@ int launch_product(Fp8Params &p, cudaStream_t s, const __half *x = nullptr) {
     if (small && fp8_mid_quantizes(p, plan))
       p.xh = x;
     else
-      W8A8_TRY(launch_quant_fp8(x, p.M, p.K, false, const_cast<uint8_t *>(p.x), const_cast<uint8_t *>(p.sx), s));
+      W8A8_TRY(launch_quant_fp8(x, p.M, p.K, true, const_cast<uint8_t *>(p.x), const_cast<uint8_t *>(p.sx), s));
   }
   return small ? launch_fp8_mid(p, plan, s) : launch_fp8_tc(p, s);
 }
@@ -124,7 +125,7 @@ int rms_norm_quantize(const w8a8_half *x, const w8a8_half *residual, const w8a8_
                                group_size, as_half(residual_out), q, scale, as_stream(stream));
 }
 
-static int quantize_fp8(const w8a8_half *x, int rows, int K, bool weights, uint8_t *q, uint8_t *scale,
+static int quantize_fp8(const w8a8_half *x, int rows, int K, uint8_t *q, uint8_t *scale,
                         w8a8_stream_t stream) {
   if (rows < 0) return W8A8_ERR_INVALID_ARG;
   W8A8_TRY(check_row(K));
@@ -132,17 +133,17 @@ static int quantize_fp8(const w8a8_half *x, int rows, int K, bool weights, uint8
   W8A8_TRY(check_ptrs({x, q}, 16));
   W8A8_TRY(check_ptrs({scale}, 1));
   W8A8_TRY(check_device());
-  return launch_quant_fp8(as_half(x), rows, K, weights, q, scale, as_stream(stream));
+  return launch_quant_fp8(as_half(x), rows, K, false, q, scale, as_stream(stream));
 }
 
 int quantize_weight_fp8(const w8a8_half *W, int N, int K, uint8_t *Wq, uint8_t *scale_w,
                         w8a8_stream_t stream) {
-  return quantize_fp8(W, N, K, true, Wq, scale_w, stream);
+  return quantize_fp8(W, N, K, Wq, scale_w, stream);
 }
 
 int quantize_act_fp8(const w8a8_half *x, int M, int K, uint8_t *xq, uint8_t *scale_a,
                      w8a8_stream_t stream) {
-  return quantize_fp8(x, M, K, false, xq, scale_a, stream);
+  return quantize_fp8(x, M, K, xq, scale_a, stream);
 }
 
 int fp8_gemm(const uint8_t *xq, const uint8_t *scale_a, const uint8_t *Wq, const uint8_t *scale_w,
@@ -185,6 +186,7 @@ int fp8_gated_gemm(const uint8_t *xq, const uint8_t *scale_a, const uint8_t *Wg,
   p.y = as_half(h);
   p.codes = hq;
   p.scales = scale_h;
+  p.early = h != nullptr;
   return launch_product(p, as_stream(stream));
 }
 

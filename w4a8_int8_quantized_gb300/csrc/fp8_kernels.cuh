@@ -13,6 +13,7 @@ struct Fp8Params {
   const uint8_t *w[2], *sw[2];  // e4m3 [N, K], e8m0 [N, G]
   int M, N, K, G;
   bool gelu;
+  bool early;                   // the next kernel may start at once: not before a caller's codes (see norm.cu)
   __half *y;                    // fp16 [M, N]
   uint8_t *codes, *scales;      // e4m3 [M, N], e8m0 [M, ceil(N / 128)]
 };
@@ -34,7 +35,8 @@ int launch_fp8_mid(const Fp8Params &p, const Fp8Plan &plan, cudaStream_t s);
 float estimate_fp8_tc(const Fp8Params &p);
 int launch_fp8_tc(const Fp8Params &p, cudaStream_t s);
 
-int launch_quant_fp8(const __half *x, long rows, int K, bool weights, uint8_t *q, uint8_t *scale,
+// early: the next kernel may start at once (see norm.cu): for codes that only this library reads
+int launch_quant_fp8(const __half *x, long rows, int K, bool early, uint8_t *q, uint8_t *scale,
                      cudaStream_t s);
 int launch_rms_norm(const __half *x, const __half *r, const __half *w, int M, int K, float eps,
                     __half *h, __half *y, cudaStream_t s);

@@ -62,7 +62,7 @@ struct MidParams {
   int split, nx;     // CTAs of a cluster: parts of K, tiles of a group of codes
   int stages, token_bytes;
   int access[3];     // see scale_access()
-  bool gelu;
+  bool gelu, early;
   __half *y;
   uint8_t *codes, *scales;
   unsigned int *err;
@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t tmem = *tmem_slot;
   // Not before the tensor memory is ours: a CTA of the next kernel that got it
   // first would wait for this one.
-  asm volatile("griddepcontrol.launch_dependents;");
+  if (p.early) asm volatile("griddepcontrol.launch_dependents;");
   bool ok = true;
 
   if (warp == 0) {
@@ -588,6 +588,7 @@ int launch_t(const Fp8Params &f, const Fp8Plan &plan, cudaStream_t s) {
   p.access[1] = scale_access(f.sw[0], f.G);
   p.access[2] = scale_access(f.sw[1], f.G);
   p.gelu = f.gelu;
+  p.early = f.early;
   p.y = f.y;
   p.codes = f.codes;
   p.scales = f.scales;

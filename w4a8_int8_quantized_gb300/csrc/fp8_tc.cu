@@ -70,7 +70,7 @@ struct TcParams {
   int M, N, G, nkb, ntiles, mtiles, ntn;  // N: columns of the output
   int m_first;      // tiles walk the tokens first
   int access[3];    // bytes that a load of sx, sw[0], sw[1] may take at once: 16, 4 or 1
-  bool gelu;
+  bool gelu, early;
   __half *y;        // stored directly (no map) where the rows are not 16-byte multiples
   uint8_t *scales;
   unsigned int *err;
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   // not before the tensor memory is ours: a CTA of the next kernel that got it
   // first would wait for this one
-  asm volatile("griddepcontrol.launch_dependents;");
+  if (p.early) asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   const int first = blockIdx.x / 2, step = gridDim.x / 2;
@@ -620,6 +620,7 @@ int launch_t(const Fp8Params &f, cudaStream_t s) {
   p.access[1] = scale_access(f.sw[0], f.G);
   p.access[2] = scale_access(f.sw[1], f.G);
   p.gelu = f.gelu;
+  p.early = f.early;
   p.scales = f.scales;
   if ((p.err = device_error_word()) == nullptr) return W8A8_ERR_CUDA;
   p.wait_limit = role_wait_limit();

@@ -54,8 +54,9 @@
 //    U loads per lane before griddepcontrol.wait.  Only reads of Wq come
 //    before the wait; x, the scales and every write come after it.  Wq must
 //    therefore not be written by a kernel that lets this one start early
-//    (one that executes griddepcontrol.launch_dependents); the library's
-//    kernels that write weights do not.
+//    (one that executes griddepcontrol.launch_dependents), with nothing but
+//    other such kernels between; the library's kernels that write 8-bit codes
+//    for a caller, weights or activations, do not.
 #include <mutex>
 
 #include "common.cuh"

@@ -88,8 +88,10 @@ __device__ __forceinline__ void products(const uint4 &h, const uint4 &w, float2 
 constexpr int kMaxThreads = 512;
 
 // EARLY: the kernels that follow may start (they wait for this grid before
-// they read what it writes); never when the codes are weights, which the
-// few-row kernels request before they wait.
+// they read what it writes).  Never where a caller gets 8-bit codes: they have a
+// weight's type and format (a product of two activations reads them as one), and
+// the few-row products request weights before they wait.  Nor may a kernel between
+// the two, which starts only when this grid has ended, pass an early start on.
 //
 // T threads at most.  Registers for three blocks of 256 an SM or two of 512 (17089
 // x 4096 to INT8 codes: 80 us; held to 64 registers 82, free 82).
@@ -317,8 +319,9 @@ NormParams params(const __half *x, const __half *r, const __half *w, long rows, 
 
 template <int FORMAT>
 int launch_n(const NormParams &p, cudaStream_t s) {
-  return p.r != nullptr ? launch_f<FORMAT, true, true, true>(p, s)
-                        : launch_f<FORMAT, true, false, true>(p, s);
+  constexpr bool EARLY = FORMAT == kValues || FORMAT == kHalf;  // fp16: nothing that a product takes for weights
+  return p.r != nullptr ? launch_f<FORMAT, true, true, EARLY>(p, s)
+                        : launch_f<FORMAT, true, false, EARLY>(p, s);
 }
 
 }  // namespace
@@ -339,10 +342,10 @@ int launch_rms_norm_quant(const __half *x, const __half *r, const __half *w, int
   }
 }
 
-int launch_quant_fp8(const __half *x, long rows, int K, bool weights, uint8_t *q, uint8_t *scale,
+int launch_quant_fp8(const __half *x, long rows, int K, bool early, uint8_t *q, uint8_t *scale,
                      cudaStream_t s) {
   const NormParams p = params(x, nullptr, nullptr, rows, K, 0.f, 0, nullptr, q, scale);
-  return weights ? launch_f<kFp8, false, false, false>(p, s) : launch_f<kFp8, false, false, true>(p, s);
+  return early ? launch_f<kFp8, false, false, true>(p, s) : launch_f<kFp8, false, false, false>(p, s);
 }
 
 }  // namespace w8a8
