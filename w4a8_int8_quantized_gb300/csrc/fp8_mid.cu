@@ -135,6 +135,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (!QUANT) prefetch_map(&map_x);
     *abort_flag = 0;
   }
+  __syncwarp();  // whole warps again: what follows is for all lanes at once (.aligned)
   if (warp == 1) {
     if (CG == 2) {
       asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
@@ -509,6 +510,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
   }
+  __syncwarp();
   if (team > 1) {  // the others may still read this CTA's sums; nothing is handed over
     asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
