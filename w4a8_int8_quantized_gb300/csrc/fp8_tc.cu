@@ -184,6 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  __syncwarp();  // whole warps again: what follows is for all lanes at once (.aligned)
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
                  "r"(kTmemCols));
@@ -470,6 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) arrive_read(in_leader(acc_free));
+        __syncwarp();  // the next load from tensor memory is the whole warp's
       };
       if (MODE == kLinear) {
 #pragma unroll 1
