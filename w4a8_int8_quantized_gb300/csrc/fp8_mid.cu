@@ -222,6 +222,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (lane == 0) arrive_cluster(in_leader(sf_full(q % kScaleSets), leader));
         __syncwarp();
       }
+      // the first CTA's last commit arrives here too, before this CTA may leave
+      wait_bar_teardown(drain, 0);
+      __syncwarp();
     } else {
     const uint32_t on = elect();
     const uint32_t idesc = (1u << 23) | (static_cast<uint32_t>(p.bn >> 3) << 17) | (static_cast<uint32_t>(8 * CG) << 24);

@@ -317,6 +317,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) arrive_cluster(in_leader(sf_full(set)));
           __syncwarp();
         }
+      // the first CTA's last commit arrives here too, before this CTA may leave
+      wait_bar_teardown(drain, 0);
+      __syncwarp();
     }
   } else if (warp < 4) {
     // ------------------------------------------------------------ scales ----
