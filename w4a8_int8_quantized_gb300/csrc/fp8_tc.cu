@@ -124,16 +124,16 @@ __device__ __forceinline__ void put_half(const TcParams &p, const CUtensorMap *m
       for (int r = 0; r < 32; ++r, to += p.N) *reinterpret_cast<uint32_t *>(to) = word(r);
       return;
     }
-    // Every other row starts between two words: halves there.  (Words that straddle
-    // two lanes' halves took 181 us for 12703 x 7009 x 512, halves throughout 79.)
-    const int odd = static_cast<int>(reinterpret_cast<uintptr_t>(to) >> 1) & 1;
+    // The first row starts at a word (y is 16-byte aligned, row0 and col0 are even),
+    // every other one between two words: halves there.  (Words that straddle two
+    // lanes' halves took 181 us for 12703 x 7009 x 512, halves throughout 79.)
 #pragma unroll 4
     for (int k = 0; k < 16; ++k, to += 2 * static_cast<long>(p.N)) {
-      const uint32_t a = word(2 * k + odd), b = word(2 * k + 1 - odd);
-      uint16_t *const odd_row = to + (odd ? 0 : p.N);
-      *reinterpret_cast<uint32_t *>(to + (odd ? p.N : 0)) = a;
-      odd_row[0] = static_cast<uint16_t>(b);
-      odd_row[1] = static_cast<uint16_t>(b >> 16);
+      const uint32_t a = word(2 * k), b = word(2 * k + 1);
+      uint16_t *const next = to + p.N;
+      *reinterpret_cast<uint32_t *>(to) = a;
+      next[0] = static_cast<uint16_t>(b);
+      next[1] = static_cast<uint16_t>(b >> 16);
     }
     return;
   }
