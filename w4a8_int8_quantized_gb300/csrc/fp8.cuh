@@ -27,8 +27,7 @@ __device__ __forceinline__ uint32_t fp8_scale_byte(float a) {
   return a == 0.f ? 127u : static_cast<uint32_t>(e < 1 ? 1 : e);
 }
 
-// 2^(byte - 127) and its reciprocal, for bytes 1 .. 253
-__device__ __forceinline__ float fp8_scale(uint32_t byte) { return __uint_as_float(byte << 23); }
+// 1 / 2^(byte - 127), for bytes 1 .. 253
 __device__ __forceinline__ float fp8_scale_inverse(uint32_t byte) {
   return __uint_as_float((254u - byte) << 23);
 }
