@@ -261,8 +261,9 @@ int w8a8_gemm_i32(const int8_t *xq, const void *Wq, int M, int N, int K,
                   w8a8_stream_t stream);
 
 /* Test hook of the failure path (the method has no counterpart): sets, for
- * the launches of the tensor-core GEMM and of the cache attention that
- * follow (every entry point that runs them), the limit of their bounded
+ * the launches of the tensor-core GEMM, of the cache attention and of the
+ * 8-bit float products that follow (every entry point that runs them), the
+ * limit of their bounded
  * device-side waits in SM clock cycles (0 = the default, about 2 s) and,
  * with skip_first_copy = 1, leaves the first weight-staging copy, or copy or
  * hand-over of keys, of each CTA out, so that the wait for it
@@ -427,8 +428,9 @@ int rms_norm_quantize(const w8a8_half *x, const w8a8_half *residual, const w8a8_
  * The conventions at the top of this file hold, with K (and F) a multiple of
  * 16, code pointers 16-byte aligned and scale pointers at any address.  Sums
  * are fp32 (the products of two codes are exact), rounded once to the output's
- * type.  Their order depends on N, K and the class of M (up to 16, 64, 128, 384,
- * 1024, 2560, 8192 rows, more), not on timing: within a class a row's result does not depend
+ * type.  Their order depends on N, K, the class of M (up to 16, 64, 128, 384,
+ * 1024, 2560, 8192 rows, more) and, for the gated pair, on the form of the output
+ * (fp16 or codes), not on timing: within a class a row's result does not depend
  * on the other rows of the batch.  No output may overlap an input. */
 
 /* fp16 rows to codes and scales.
@@ -452,7 +454,7 @@ int fp8_gemm(const uint8_t *xq, const uint8_t *scale_a, const uint8_t *Wq, const
              int M, int N, int K, w8a8_half *y, w8a8_stream_t stream);
 
 /* Activations of the gated block. */
-#define W8A8_GATE_SILU 0 /* g / (1 + exp(-g)) */
+#define W8A8_GATE_SILU 0 /* g / (1 + exp(-g)); 0 for g below -87 */
 #define W8A8_GATE_GELU 1 /* g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2 */
 
 /* Both projections of a gated feed-forward block, the activation and the

@@ -45,7 +45,11 @@ __device__ __forceinline__ uint32_t fp8_pack4(float a, float b, float c, float d
 // exp(-2 z)).  exp and the reciprocal are the approximate ones (a few 2^-22
 // relative for |t| below 16, and where |t| is larger the exponential hardly
 // counts or the value is below 1e-6 of g): far inside one rounding to fp16 or
-// e4m3, which follows.  exp(-t) = inf gives 0.
+// e4m3, which follows.  From exp(-t) = 2^126 on (t below -87) the reciprocal, and
+// with it the value, is 0.  Measured: with expf and a rounded division 2049 x 14336
+// x 4096 to codes has the same errors against 64 bits (1.7e-5 of the codes beside a
+// border, 3.06e-4 on the whole; they are the tensor core's sums) and takes 193 us
+// instead of 159.
 template <bool GELU>
 __device__ __forceinline__ float gated(float g, float u) {
   const float t = GELU ? 1.5957691216057308f * fmaf(0.044715f * g * g, g, g) : g;

@@ -1,5 +1,6 @@
 // Products of 8-bit float rows that are bound by the weights' bytes or by few
-// tiles: up to a few hundred rows.  The arithmetic of fp8_tc.cu (block-scaled
+// tiles: up to about a thousand rows, and up to 8192 where the columns are few.  The
+// arithmetic of fp8_tc.cu (block-scaled
 // tcgen05 MMAs, sums in fp32 from the first group to the last), in tiles of up
 // to 128 tokens x 128 columns, one tile a CTA, two CTAs an SM, and K divided
 // among the CTAs of a cluster where the tiles alone are too few.
@@ -654,8 +655,9 @@ Fp8Plan best_tile(const Fp8Params &f, int split) {
 Fp8Plan find_plan(const Fp8Params &f) {
   // The parts of K decide the order of a sum, so they are the same for a class of
   // batches, whose result for a row then does not depend on the others: those that
-  // suit the class's largest (2 % slower on average than each batch's own, at most
-  // 25 %).  Undivided, both kernels give the same sums.
+  // suit the class's largest (up to 1000 rows 2 % slower on average than each batch's
+  // own, at most 25 %; not compared above, where the model is not fitted either).
+  // Undivided, both kernels give the same sums.
   Fp8Params typical = f;
   typical.M = f.M <= 16 ? 16 : f.M <= 64 ? 64 : f.M <= 128 ? 128 : f.M <= 384 ? 384 : f.M <= 1024 ? 1024 : f.M <= 2560 ? 2560 : 8192;
   const int most = f.M > 8192 ? 1 : std::min(f.codes != nullptr ? 4 : 8, f.G);

@@ -94,7 +94,7 @@ constexpr int kMaxThreads = 512;
 // the two, which starts only when this grid has ended, pass an early start on.
 //
 // T threads at most.  Registers for three blocks of 256 an SM or two of 512 (17089
-// x 4096 to INT8 codes: 80 us; held to 64 registers 82, free 82).
+// x 4096 with the residual to INT8 codes: 75 us; held to 64 registers 82, free 82).
 template <int FORMAT, bool NORM, bool RES, bool EARLY, int V, int MOST>
 __global__ void __launch_bounds__(MOST, V > 4 ? 1 : MOST == 256 ? 3 : 2) norm_kernel(const NormParams par) {
   // a second row in registers only where it fits
