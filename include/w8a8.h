@@ -263,11 +263,10 @@ int w8a8_gemm_i32(const int8_t *xq, const void *Wq, int M, int N, int K,
 /* Test hook of the failure path (the method has no counterpart): sets, for
  * the launches of the tensor-core GEMM, of the cache attention and of the
  * 8-bit float products that follow (every entry point that runs them), the
- * limit of their bounded
- * device-side waits in SM clock cycles (0 = the default, about 2 s) and,
- * with skip_first_copy = 1, leaves the first weight-staging copy, or copy or
- * hand-over of keys, of each CTA out, so that the wait for it
- * gives up: the kernel then returns early, its outputs are undefined, and
+ * limit of their bounded device-side waits in SM clock cycles (0 = the
+ * default, about 2 s) and, with skip_first_copy = 1, leaves the first
+ * weight-staging copy, or copy or hand-over of keys, of each CTA out, so that
+ * the wait for it gives up: the kernel then returns early, its outputs are undefined, and
  * w8a8_check_status() reports W8A8_ERR_TIMEOUT.  No fault, trap or hang is
  * involved; the kernel still lets every copy it issued land before it
  * exits.  Process-wide; w8a8_test_set_fault(0, 0) restores normal
