@@ -1,9 +1,9 @@
 // Products of 8-bit float rows that are bound by the weights' bytes or by few
-// tiles: up to about a thousand rows, and up to 8192 where the columns are few.  The
-// arithmetic of fp8_tc.cu (block-scaled
-// tcgen05 MMAs, sums in fp32 from the first group to the last), in tiles of up
-// to 128 tokens x 128 columns, one tile a CTA, two CTAs an SM, and K divided
-// among the CTAs of a cluster where the tiles alone are too few.
+// tiles: up to about a thousand rows, and up to 8192 where the columns are few.
+// The arithmetic of fp8_tc.cu (block-scaled tcgen05 MMAs, sums in fp32 from the
+// first group to the last), in tiles of up to 128 tokens x 128 columns, one tile a
+// CTA, two CTAs an SM, and K divided among the CTAs of a cluster where the tiles
+// alone are too few.
 //
 // Above 128 rows a tile may be a pair's (cta_group::2): 256 tokens x up to 160
 // columns, each CTA fetching its own tokens and half of the weights.  What an SM
